@@ -35,8 +35,8 @@
  *     K-contiguous: W_gate, W_up are [E + n_shared, F, D], W_down is
  *     [E + n_shared, D, F], as the pages use them through W.transpose(1, 2).
  *   - Supported dtype pairs (x, W): (F32, F32), (BF16, BF16), (F16, F16),
- *     (F16, Q4B32), (F16, Q4A32), (F16, Q4A64). Anything else is
- *     MOE_EUNSUPPORTED, never a fallback.
+ *     (F16, Q4B32), (F16, Q4A32), (F16, Q4A64), (BF16, F8B128),
+ *     (F16, F8B128). Anything else is MOE_EUNSUPPORTED, never a fallback.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H
@@ -72,7 +72,19 @@ typedef enum {
      * consecutive K values of a row, its scale s then its bias b; the value
      * is q * s + b. Weights only; x must be F16. */
     MOE_Q4A32 = 4,
-    MOE_Q4A64 = 5
+    MOE_Q4A64 = 5,
+    /* 8-bit blocks: `data` is e4m3 (finite range to 448, no infinity, one
+     * byte a value), `scales` f32; a value is its code times its block's
+     * scale. Weights [.., N, K] have a scale per 128 x 128 block, [..,
+     * ceil(N / 128), ceil(K / 128)]; rows [R, K] one per row and 128
+     * values, [R, ceil(K / 128)]. A block with largest magnitude m is held
+     * with a = max(m, 2^-100), scale a / 448 and codes e4m3(v * (448 / a)),
+     * the quotients and the product rounded to f32, the code to nearest
+     * even. A block that holds a NaN or an infinity has a scale of NaN or
+     * infinity and stands for NaN. As weights of moe_forward (bf16 / f16
+     * x), the layer quantises x's rows and the SwiGLU output (f32, per pair
+     * and 128 features) and multiplies codes. */
+    MOE_F8B128 = 6
 } moe_dtype;
 
 /* Plan shape. 1 <= k <= E <= 1024; T >= 0; T*(k+1) < 2^31; n_shared in
@@ -390,6 +402,96 @@ moe_status moe_dequant_q4(const void *data, const void *scales, int64_t rows,
 moe_status moe_dequant_weights(int32_t dtype, const void *data,
                                const void *scales, int64_t rows, int64_t K,
                                void *out_f16, void *stream);
+
+/* --- 8-bit blocks --------------------------------------------------------- */
+
+/* x [rows, K] (F32, BF16 or F16) as MOE_F8B128 rows: codes q [rows, K] and
+ * scales [rows, ceil(K / 128)]. K a multiple of 8; a row's last block may be
+ * short. Pointers 16-byte aligned. MOE_EUNSUPPORTED at 2^31 blocks or more.
+ * Async on `stream`. */
+moe_status moe_quant_f8(const void *x, int32_t dtype, int64_t rows, int32_t K,
+                        void *q, float *scales, void *stream);
+
+/* w [mats, N, K] (F32, BF16 or F16) as MOE_F8B128 weights: codes q [mats, N,
+ * K] and scales [mats, ceil(N / 128), ceil(K / 128)]. K a multiple of 8; the
+ * last blocks may be short. Pointers 16-byte aligned. MOE_EUNSUPPORTED at
+ * 2^31 blocks or more. Async on `stream`. */
+moe_status moe_quant_f8_weights(const void *w, int32_t dtype, int64_t mats,
+                                int32_t N, int32_t K, void *q, float *scales,
+                                void *stream);
+
+/* Bytes of device workspace moe_gemm_f8 needs; 0 on invalid sizes. */
+size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K);
+
+/* out[M, N] = x[M, K] . w[N, K]^T on MOE_F8B128 rows and weights: the codes'
+ * products of each block of 128 summed in f32 by the matrix units, scaled by
+ * x_scales * w_scales and added in f32, rounded once to out_dtype (F32, BF16
+ * or F16). K a multiple of 16; M below 2^31, M and N any other size (0
+ * writes nothing). Pointers 16-byte aligned, ws 256-byte aligned. Async on
+ * `stream`. */
+moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,
+                       const float *w_scales, int64_t M, int32_t N, int32_t K,
+                       void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/* --- norms around a block -------------------------------------------------- */
+
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1    /* gate [D], one value a channel */
+#define MOE_GATE_TOKEN 2      /* gate [T], one value a token   */
+#define MOE_NORM_UNIT_OFFSET 1
+#define MOE_NORM_MAX_D 16384
+
+/* Rows and types of the norms around a block. D a multiple of 8 up to
+ * MOE_NORM_MAX_D. residual_dtype, block_dtype, weight_dtype (both norms'
+ * weights) and gate_dtype are F32, BF16 or F16, each on its own; x_dtype is
+ * the normed rows' type (forward: also MOE_F8B128, rows as moe_gemm_f8 reads
+ * them), in the backward dx's. MOE_NORM_UNIT_OFFSET: the weights stand for
+ * 1 + their values. */
+typedef struct {
+    int32_t T, D;
+    int32_t residual_dtype, block_dtype, x_dtype, weight_dtype, gate_dtype;
+    int32_t gate_kind, flags;
+    float alpha, eps;
+} moe_norm_desc;
+
+/* The norms after a block and before the next one, fused with the block's
+ * gate and the residual's scale; RMSnorm(v) = v / sqrt(mean(v^2) + eps):
+ *   z            = RMSnorm(block) * post_weight   (block if post_weight NULL)
+ *   residual_out = residual + alpha * gate * z
+ *   x            = RMSnorm(residual_out) * weight
+ * in f32 (x from the unrounded residual_out), each output rounded once.
+ * block NULL: the residual passes through (residual_out is not written);
+ * weight NULL: x is not written. residual_out may be residual itself and x
+ * may be block itself where their types' sizes agree (a row is read before
+ * it is written); buffers may not overlap otherwise. x_scales [T, ceil(D /
+ * 128)] only with x_dtype MOE_F8B128. Pointers 16-byte aligned. Async on
+ * `stream`. */
+moe_status moe_norm_forward(const moe_norm_desc *desc, const void *residual,
+                            const void *block, const void *post_weight,
+                            const void *gate, const void *weight,
+                            void *residual_out, void *x, float *x_scales,
+                            void *stream);
+
+/* Bytes of device workspace moe_norm_backward needs; 0 on invalid desc. */
+size_t moe_norm_backward_workspace_bytes(const moe_norm_desc *desc);
+
+/* Gradients of moe_norm_forward. Comes in: dresidual_out (residual_dtype;
+ * NULL: zero) and dx (desc's x_dtype), the forward's residual_out (as
+ * stored), block and parameters; the inverse norms are recomputed. Goes out:
+ * dresidual [T, D] (residual_dtype), dblock [T, D] (block_dtype), and f32
+ * dpost_weight [D], dgate [D] or [T], dweight [D], each of the last three
+ * only with its parameter. block NULL: no block part; weight NULL: no x, dx
+ * is not read. dresidual may be dresidual_out itself, dblock block itself.
+ * The sums over rows are the same bits from run to run. Pointers 16-byte
+ * aligned, ws 256-byte aligned. Async on `stream`. */
+moe_status moe_norm_backward(const moe_norm_desc *desc,
+                             const void *residual_out, const void *block,
+                             const void *post_weight, const void *gate,
+                             const void *weight, const void *dresidual_out,
+                             const void *dx, void *dresidual, void *dblock,
+                             float *dpost_weight, float *dgate, float *dweight,
+                             void *ws, size_t ws_bytes, void *stream);
 
 /* Milliseconds spent in each phase, summed over the moe_forward and
  * moe_route calls since the last reset that ran with MOE_OPT_PHASE_EVENTS;

@@ -19,7 +19,15 @@ Weights are torch tensors [E (+1 shared), F, D] / [E (+1), D, F] in x's dtype,
 or, for 4-bit weights, ``(packed uint8 [.., N, K/2], params fp16)`` pairs:
 params [.., N, K/32] are the block scales of the signed format, params
 [.., N, K/G, 2] the (scale, bias) pairs of the affine format with groups of
-G = 32 or 64 K values (the format follows from the params' shape).
+G = 32 or 64 K values (the format follows from the params' shape); or, for
+8-bit weights, ``(codes float8_e4m3fn [.., N, K], scales float32 [.., ceil(N /
+128), ceil(K / 128)])`` pairs as moe_quant_f8_weights makes them.
+
+Around the layer, the norms after one block and before the next, and the
+projections on 8-bit weights that read their output:
+
+    residual, x = moe_norm(residual, block_out, weight, post_weight, gate)
+    out = moe_gemm_f8(moe_quant_f8(x), moe_quant_f8_weights(w))
 """
 
 from __future__ import annotations
@@ -35,6 +43,10 @@ LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
 MOE_F32, MOE_BF16, MOE_F16, MOE_Q4B32 = 0, 1, 2, 3
 MOE_Q4A32, MOE_Q4A64 = 4, 5
+MOE_F8B128 = 6
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
+MOE_NORM_UNIT_OFFSET = 1
+MOE_NORM_MAX_D = 16384
 MOE_OPT_PHASE_EVENTS = 1
 MOE_OPT_BF16_PLAIN_H = 2
 MOE_OPT_EXACT_ROUTES = 4
@@ -68,7 +80,9 @@ EXPORTED = (
     "moe_phase_times", "moe_last_error", "moe_version",
     "moe_route_workspace_bytes", "moe_route", "moe_dequant_weights",
     "moe_backward_workspace_bytes", "moe_backward", "moe_forward_get_views",
-    "moe_forward_noalloc",
+    "moe_forward_noalloc", "moe_quant_f8", "moe_quant_f8_weights",
+    "moe_gemm_f8_workspace_bytes", "moe_gemm_f8", "moe_norm_forward",
+    "moe_norm_backward_workspace_bytes", "moe_norm_backward",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -113,6 +127,13 @@ class ForwardViews(ctypes.Structure):
                 ("fat_slot", ctypes.c_void_p),
                 ("fat_copy", ctypes.c_void_p * 3),
                 ("fat_slots", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "T", "D", "residual_dtype", "block_dtype", "x_dtype", "weight_dtype",
+        "gate_dtype", "gate_kind", "flags")] + [
+        ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -182,6 +203,21 @@ def library(path: str = LIB_PATH):
                                vp, vp, vp, vp, vp, vp, vp, vp, sz,
                                ctypes.POINTER(Options), vp]
     L.moe_backward.restype = i32
+    f8 = [vp, i32, i64, i32]
+    L.moe_quant_f8.argtypes = f8 + [vp, vp, vp]
+    L.moe_quant_f8.restype = i32
+    L.moe_quant_f8_weights.argtypes = f8 + [i32, vp, vp, vp]
+    L.moe_quant_f8_weights.restype = i32
+    L.moe_gemm_f8_workspace_bytes.argtypes = [i64, i32, i32]
+    L.moe_gemm_f8_workspace_bytes.restype = sz
+    L.moe_gemm_f8.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, sz, vp]
+    L.moe_gemm_f8.restype = i32
+    L.moe_norm_forward.argtypes = [ctypes.POINTER(NormDesc)] + [vp] * 9
+    L.moe_norm_forward.restype = i32
+    L.moe_norm_backward_workspace_bytes.argtypes = [ctypes.POINTER(NormDesc)]
+    L.moe_norm_backward_workspace_bytes.restype = sz
+    L.moe_norm_backward.argtypes = [ctypes.POINTER(NormDesc)] + [vp] * 13 + [sz, vp]
+    L.moe_norm_backward.restype = i32
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_version.argtypes = []
@@ -387,7 +423,24 @@ def q4_dtype(data: torch.Tensor, params: torch.Tensor) -> int:
                      f"match packed data of shape {tuple(data.shape)}")
 
 
+def _is_f8(w) -> bool:
+    return isinstance(w, (tuple, list)) and w[0].dtype == torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
 def _weight(w, device) -> tuple:
+    if _is_f8(w):
+        data, scales = w
+        if scales.dtype != torch.float32:
+            raise ValueError("8-bit weights are (float8_e4m3fn codes, float32 scales)")
+        if data.device != device or scales.device != device:
+            raise ValueError("weights must be on the input's device")
+        data, scales = data.contiguous(), scales.contiguous()
+        return (Weight(MOE_F8B128, data.data_ptr(), scales.data_ptr()),
+                (data, scales))
     if isinstance(w, (tuple, list)):
         data, scales = w
         if data.dtype != torch.uint8 or scales.dtype != torch.float16:
@@ -406,6 +459,8 @@ def _weight(w, device) -> tuple:
 
 
 def _dims(w_gate):
+    if _is_f8(w_gate):
+        w_gate = w_gate[0]
     if isinstance(w_gate, (tuple, list)):
         data = w_gate[0]
         return data.shape[1], data.shape[2] * 2      # F, D
@@ -421,7 +476,16 @@ def _check_weight_shapes(plan, w_gate, w_up, w_down, D: int, F: int):
     fmt = None
     for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
         N, K = want[name]
-        if isinstance(w, (tuple, list)):
+        if _is_f8(w):
+            data, scales = w
+            if data.dim() != 3 or tuple(data.shape[1:]) != (N, K):
+                raise ValueError(f"{name} codes must be [n, {N}, {K}], "
+                                 f"got {tuple(data.shape)}")
+            if tuple(scales.shape) != (data.shape[0], _blocks(N), _blocks(K)):
+                raise ValueError(f"{name} scales {tuple(scales.shape)} do not "
+                                 f"match its codes {tuple(data.shape)}")
+            f = data.dtype
+        elif isinstance(w, (tuple, list)):
             data, params = w
             if data.dim() != 3 or tuple(data.shape[1:]) != (N, K // 2):
                 raise ValueError(f"{name} packed data must be [n, {N}, {K // 2}], "
@@ -590,7 +654,8 @@ def moe_backward(plan: Plan, x: torch.Tensor, w_gate, w_up, w_down,
     if T != plan.T:
         raise ValueError(f"x has {T} tokens, the plan {plan.T}")
     if isinstance(w_gate, (tuple, list)):
-        raise ValueError("backward takes 16-bit weights (4-bit ones are frozen)")
+        raise ValueError("backward takes 16-bit weights (4-bit and 8-bit ones "
+                         "are frozen)")
     F = w_gate.shape[1]
     _check_weight_shapes(plan, w_gate, w_up, w_down, D, F)
     dy = dy.to(torch.float32).contiguous()
@@ -656,6 +721,239 @@ def moe_dequant_weights(data: torch.Tensor, params: torch.Tensor) -> torch.Tenso
     return out
 
 
+def _on(device):
+    """A guard that makes the tensors' device the current one: the library
+    launches there. The calls that have one may be made from any device."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    return torch.cuda.device(device)
+
+
+def moe_quant_f8(x: torch.Tensor) -> tuple:
+    """Rows [.., K] (float32, bfloat16 or float16; K a multiple of 8) as 8-bit
+    blocks: (codes float8_e4m3fn [.., K], scales float32 [.., ceil(K / 128)]),
+    a scale for each row and 128 values."""
+    if x.dtype not in _TORCH_TO_MOE or x.dim() < 1:
+        raise ValueError("x must be a float32/bfloat16/float16 tensor [.., K]")
+    K = x.shape[-1]
+    if K < 8 or K % 8:
+        raise ValueError(f"K={K} must be a positive multiple of 8")
+    with _on(x.device):
+        x = x.contiguous()
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty(*x.shape[:-1], _blocks(K), dtype=torch.float32, device=x.device)
+        _check(library().moe_quant_f8(x.data_ptr(), _TORCH_TO_MOE[x.dtype],
+                                      x.numel() // K, K, q.data_ptr(),
+                                      s.data_ptr(), _stream(x.device)))
+    return q, s
+
+
+def moe_quant_f8_weights(w: torch.Tensor) -> tuple:
+    """Weights [.., N, K] (float32, bfloat16 or float16; K a multiple of 8) as
+    8-bit blocks: (codes float8_e4m3fn [.., N, K], scales float32 [.., ceil(N
+    / 128), ceil(K / 128)]), a scale for each 128 x 128 block."""
+    if w.dtype not in _TORCH_TO_MOE or w.dim() < 2:
+        raise ValueError("w must be a float32/bfloat16/float16 tensor [.., N, K]")
+    N, K = w.shape[-2:]
+    if K < 8 or K % 8:
+        raise ValueError(f"K={K} must be a positive multiple of 8")
+    mats = 1
+    for n in w.shape[:-2]:
+        mats *= n
+    with _on(w.device):
+        w = w.contiguous()
+        q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+        s = torch.empty(*w.shape[:-2], _blocks(N), _blocks(K), dtype=torch.float32,
+                        device=w.device)
+        _check(library().moe_quant_f8_weights(w.data_ptr(), _TORCH_TO_MOE[w.dtype],
+                                              mats, N, K, q.data_ptr(), s.data_ptr(),
+                                              _stream(w.device)))
+    return q, s
+
+
+def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
+                out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """out [.., N] = x . w^T of 8-bit rows x = (codes [.., K], scales [..,
+    ceil(K / 128)]) and weights w = (codes [N, K], scales [ceil(N / 128),
+    ceil(K / 128)]), as moe_quant_f8 and moe_quant_f8_weights give them; K a
+    multiple of 16. The result has ``out``'s type, or ``out_dtype``
+    (float32, bfloat16 or float16)."""
+    (xq, xs), (wq, ws) = x, w
+    f8 = torch.float8_e4m3fn
+    if xq.dtype != f8 or wq.dtype != f8 or xs.dtype != torch.float32 or ws.dtype != torch.float32:
+        raise ValueError("x and w are (float8_e4m3fn codes, float32 scales)")
+    if xq.dim() < 1 or wq.dim() != 2 or xq.shape[-1] != wq.shape[1]:
+        raise ValueError(f"codes {tuple(xq.shape)} and {tuple(wq.shape)} must be "
+                         "[.., K] and [N, K]")
+    N, K = wq.shape
+    if K < 16 or K % 16:
+        raise ValueError(f"K={K} must be a positive multiple of 16")
+    if tuple(xs.shape) != (*xq.shape[:-1], _blocks(K)) \
+            or tuple(ws.shape) != (_blocks(N), _blocks(K)):
+        raise ValueError(f"scales {tuple(xs.shape)} and {tuple(ws.shape)} do not match "
+                         f"codes {tuple(xq.shape)} and {tuple(wq.shape)}")
+    if any(t.device != xq.device for t in (xs, wq, ws)):
+        raise ValueError("x, w and their scales must be on one device")
+    L = library()
+    shape = (*xq.shape[:-1], N)
+    M = xq.numel() // K
+    with _on(xq.device):
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=xq.device)
+        if out.dtype not in _TORCH_TO_MOE or tuple(out.shape) != shape \
+                or not out.is_contiguous() or out.device != xq.device:
+            raise ValueError(f"out must be a contiguous float32/bfloat16/float16 "
+                             f"{shape} tensor on x's device")
+        nbytes = L.moe_gemm_f8_workspace_bytes(M, N, K)
+        if nbytes == 0:
+            raise MoeError(MOE_EINVAL, moe_last_error())
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=xq.device)
+        xq, xs, wq, ws = (t.contiguous() for t in (xq, xs, wq, ws))
+        _check(L.moe_gemm_f8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+                             M, N, K, out.data_ptr(), _TORCH_TO_MOE[out.dtype],
+                             workspace.data_ptr(), nbytes, _stream(xq.device)))
+    return out
+
+
+def _rows_like(t, like, name: str):
+    if t.dtype not in _TORCH_TO_MOE or t.shape != like.shape or t.device != like.device:
+        raise ValueError(f"{name} must be a float32/bfloat16/float16 tensor of shape "
+                         f"{tuple(like.shape)} on the residual's device")
+    return t.contiguous()
+
+
+def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
+               unit_offset, x_dtype):
+    """The descriptor of a norm call and its contiguous tensors, checked."""
+    if residual.dtype not in _TORCH_TO_MOE or residual.dim() != 2:
+        raise ValueError("residual must be a 2-D float32/bfloat16/float16 tensor")
+    T, D = residual.shape
+    if D < 8 or D % 8 or D > MOE_NORM_MAX_D:
+        raise ValueError(f"D={D} must be a multiple of 8 in 8..{MOE_NORM_MAX_D}")
+    if block is None and (post_weight is not None or gate is not None):
+        raise ValueError("post_weight and gate need a block")
+    if block is None and weight is None:
+        raise ValueError("neither a block nor a weight: nothing to do")
+    residual = residual.contiguous()
+    if block is not None:
+        block = _rows_like(block, residual, "block")
+    vecs = [v for v in (weight, post_weight) if v is not None]
+    for v in vecs:
+        if v.dtype not in _TORCH_TO_MOE or v.dtype != vecs[0].dtype \
+                or tuple(v.shape) != (D,) or v.device != residual.device:
+            raise ValueError(f"weight and post_weight must be [{D}] tensors of one "
+                             "type (float32/bfloat16/float16) on the residual's device")
+    kind = MOE_GATE_NONE
+    if gate is not None:
+        if tuple(gate.shape) == (D,):
+            kind = MOE_GATE_CHANNEL
+        elif tuple(gate.shape) == (T, 1):
+            kind = MOE_GATE_TOKEN
+        if kind == MOE_GATE_NONE or gate.dtype not in _TORCH_TO_MOE \
+                or gate.device != residual.device:
+            raise ValueError(f"gate must be [{D}] (per channel) or [{T}, 1] (per token), "
+                             "float32/bfloat16/float16, on the residual's device")
+        gate = gate.contiguous()
+    weight, post_weight = (None if v is None else v.contiguous()
+                           for v in (weight, post_weight))
+    code = lambda t: MOE_F32 if t is None else _TORCH_TO_MOE[t.dtype]  # noqa: E731
+    d = NormDesc(T, D, code(residual), code(block), x_dtype,
+                 _TORCH_TO_MOE[vecs[0].dtype] if vecs else MOE_F32, code(gate), kind,
+                 MOE_NORM_UNIT_OFFSET if unit_offset else 0, float(alpha), float(eps))
+    return d, residual, block, weight, post_weight, gate
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_norm(residual: torch.Tensor, block: torch.Tensor | None = None,
+             weight: torch.Tensor | None = None,
+             post_weight: torch.Tensor | None = None,
+             gate: torch.Tensor | None = None, alpha: float = 1.0,
+             eps: float = 1e-6, unit_offset: bool = False,
+             x_dtype: torch.dtype = torch.bfloat16) -> tuple:
+    """The norms after a block and before the next one: (residual_out, x) with
+    z = RMSnorm(block) * post_weight (block itself without post_weight),
+    residual_out = residual + alpha * gate * z, x = RMSnorm(residual_out) *
+    weight. residual and block are [T, D] (D a multiple of 8 up to 16384),
+    the weights [D], gate [D] (per channel) or [T, 1] (per token);
+    ``unit_offset``: the weights stand for 1 + their values. x has
+    ``x_dtype``, or, for float8_e4m3fn, is (codes, scales) as moe_gemm_f8
+    takes them. Without block residual_out is residual itself; without weight
+    x is None."""
+    f8 = x_dtype == torch.float8_e4m3fn
+    if not f8 and x_dtype not in _TORCH_TO_MOE:
+        raise ValueError("x_dtype must be float32, bfloat16, float16 or float8_e4m3fn")
+    d, residual, block, weight, post_weight, gate = _norm_args(
+        residual, block, weight, post_weight, gate, alpha, eps, unit_offset,
+        MOE_F8B128 if f8 else _TORCH_TO_MOE[x_dtype])
+    with _on(residual.device):
+        out = residual if block is None else torch.empty_like(residual)
+        x = s = None
+        if weight is not None:
+            x = torch.empty(residual.shape, dtype=x_dtype, device=residual.device)
+            if f8:
+                s = torch.empty(d.T, _blocks(d.D), dtype=torch.float32,
+                                device=residual.device)
+        _check(library().moe_norm_forward(
+            ctypes.byref(d), residual.data_ptr(), _ptr(block), _ptr(post_weight),
+            _ptr(gate), _ptr(weight), out.data_ptr(), _ptr(x), _ptr(s),
+            _stream(residual.device)))
+    return out, ((x, s) if f8 and x is not None else x)
+
+
+def moe_norm_backward(residual_out: torch.Tensor, block: torch.Tensor | None,
+                      dx: torch.Tensor | None,
+                      dresidual_out: torch.Tensor | None = None,
+                      weight: torch.Tensor | None = None,
+                      post_weight: torch.Tensor | None = None,
+                      gate: torch.Tensor | None = None, alpha: float = 1.0,
+                      eps: float = 1e-6, unit_offset: bool = False) -> dict:
+    """Gradients of moe_norm from dx (x's gradient, any of its 16-bit or
+    32-bit types) and dresidual_out (in the residual's type, or None), given
+    the residual_out that moe_norm returned and its block and parameters:
+    dresidual (residual's type), dblock (block's), and float32 dweight,
+    dpost_weight [D] and dgate (gate's shape), each where its input is."""
+    if weight is not None and (dx is None or dx.dtype not in _TORCH_TO_MOE):
+        raise ValueError("dx must be a float32/bfloat16/float16 tensor")
+    if weight is None and dresidual_out is None:
+        raise ValueError("neither a weight nor dresidual_out: no gradient comes in")
+    d, residual_out, block, weight, post_weight, gate = _norm_args(
+        residual_out, block, weight, post_weight, gate, alpha, eps, unit_offset,
+        MOE_F32 if weight is None else _TORCH_TO_MOE[dx.dtype])
+    dx = None if weight is None else _rows_like(dx, residual_out, "dx")
+    if dresidual_out is not None:
+        dresidual_out = _rows_like(dresidual_out, residual_out, "dresidual_out")
+        if dresidual_out.dtype != residual_out.dtype:
+            raise ValueError("dresidual_out must have residual_out's type")
+    L = library()
+    with _on(residual_out.device):
+        nbytes = L.moe_norm_backward_workspace_bytes(ctypes.byref(d))
+        if nbytes == 0:
+            raise MoeError(MOE_EINVAL, moe_last_error())
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=residual_out.device)
+        f32 = dict(dtype=torch.float32, device=residual_out.device)
+        out = {"dresidual": torch.empty_like(residual_out)}
+        if block is not None:
+            out["dblock"] = torch.empty_like(block)
+        if weight is not None:
+            out["dweight"] = torch.empty(d.D, **f32)
+        if post_weight is not None:
+            out["dpost_weight"] = torch.empty(d.D, **f32)
+        if gate is not None:
+            out["dgate"] = torch.empty(gate.shape, **f32)
+        ptr = lambda name: _ptr(out.get(name))  # noqa: E731
+        _check(L.moe_norm_backward(
+            ctypes.byref(d), residual_out.data_ptr(), _ptr(block), _ptr(post_weight),
+            _ptr(gate), _ptr(weight), _ptr(dresidual_out), _ptr(dx), ptr("dresidual"),
+            ptr("dblock"), ptr("dpost_weight"), ptr("dgate"), ptr("dweight"),
+            workspace.data_ptr(), nbytes, _stream(residual_out.device)))
+    return out
+
+
 def moe_phase_times(reset: bool = True) -> tuple:
     """(ms per phase summed over recorded calls, number of calls)."""
     ms = (ctypes.c_double * MOE_N_PHASES)()
@@ -670,3 +968,8 @@ plan = moe_plan_create
 forward = moe_forward
 route = moe_route
 backward = moe_backward
+norm = moe_norm
+norm_backward = moe_norm_backward
+quant_f8 = moe_quant_f8
+quant_f8_weights = moe_quant_f8_weights
+gemm_f8 = moe_gemm_f8

@@ -1,0 +1,328 @@
+// C entry points of the 8-bit block format and of the norms, and the routed
+// layer's launches on MOE_F8B128 weights. Every argument is checked before
+// the first launch; every launch goes to the caller's stream.
+#include <algorithm>
+#include <cmath>
+
+#include "moe_internal.h"
+
+using namespace moe;
+
+namespace {
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+inline bool aligned16(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+inline bool plain_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16 || dt == MOE_F16; }
+
+moe_status launched(hipError_t e, const char* where) {
+  if (e == hipSuccess) return MOE_OK;
+  return set_error(MOE_EHIP, "%s: %s (%s)", where, hipGetErrorName(e), hipGetErrorString(e));
+}
+
+// The layer's workspace: quantised x, the SwiGLU outputs in f32 and
+// quantised, the pairs' unweighted outputs, the work lists.
+struct F8Layout {
+  size_t x8, xs, h, h8, hs, y, full_tiles, sk1, sk4, fat_slot, fat_list, meta, bytes;
+  int cap_tiles, cap_sk1, cap_sk4;
+};
+
+F8Layout f8_layout(const moe_plan_desc& d, int D, int F, int xdt) {
+  F8Layout L{};
+  const size_t P = (size_t)d.T * d.k + (size_t)d.n_shared * d.T;
+  const int n_exp = d.E + d.n_shared;
+  L.cap_tiles = n_exp + (int)(P / kFullBM) + 1;
+  L.cap_sk1 = n_exp;
+  L.cap_sk4 = n_exp + (int)(P / kSkRows) + 1;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
+  L.x8 = take((size_t)d.T * D);
+  L.xs = take((size_t)d.T * (D / 128) * 4);
+  L.h = take(P * F * 4);
+  L.h8 = take(P * F);
+  L.hs = take(P * (F / 128) * 4);
+  L.y = take(P * D * (xdt == MOE_F16 ? 2 : 4));
+  L.full_tiles = take((size_t)L.cap_tiles * 8);
+  L.sk1 = take((size_t)L.cap_sk1 * 16);
+  L.sk4 = take((size_t)L.cap_sk4 * 16);
+  L.fat_slot = take((size_t)n_exp * 4);
+  L.fat_list = take((size_t)n_exp * 4);
+  L.meta = take(kMetaCount * 4);
+  L.bytes = o;
+  return L;
+}
+
+}  // namespace
+
+size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt) {
+  return f8_layout(d, D, F, xdt).bytes;
+}
+
+// 0 quantise x, 1 classify, 2 / 3 gate/up of groups of <= 16 / 17..64 rows,
+// 4 quantise h, 5 / 6 down of the same groups, 7 unused, 8 combine
+int moe::f8_step_phase(int step) {
+  static const int ph[kF8Steps] = {1, 0, 3, 14, 1, 5, 15, 4, 6};
+  return ph[step];
+}
+
+hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s) {
+  const moe_plan_desc& d = p.desc;
+  const F8Layout L = f8_layout(d, l.D, l.F, l.xdt);
+  char* b = l.ws;
+  const int64_t P = (int64_t)d.T * d.k + (int64_t)d.n_shared * d.T;
+  const int n_exp = d.E + d.n_shared;
+  const bool decode = p.decode;
+  F8Args g{};
+  g.pair_token = p.pair_token;
+  g.offsets = p.offsets;
+  g.meta = decode ? p.dmeta : (const int32_t*)(b + L.meta);
+  g.clamp = l.o.swiglu_limit;
+  switch (step) {
+    case 0:
+      return launch_quant_rows(l.x, l.xdt, d.T, l.D, b + L.x8, (float*)(b + L.xs), s);
+    case 1: {
+      if (decode) return hipSuccess;
+      ClassifyArgs ca{};
+      ca.counts = p.counts;
+      ca.n_exp = n_exp;
+      ca.mode = 1;
+      ca.S = 1e30;
+      ca.full_tiles = (int32_t*)(b + L.full_tiles);
+      ca.sk1 = (int32_t*)(b + L.sk1);
+      ca.sk4 = (int32_t*)(b + L.sk4);
+      ca.offsets = p.offsets;
+      ca.pair_token = p.pair_token;
+      ca.fat_slot = (int32_t*)(b + L.fat_slot);
+      ca.fat_list = (int32_t*)(b + L.fat_list);
+      ca.meta = (int32_t*)(b + L.meta);
+      return launch_classify(ca, s);
+    }
+    case 2: case 3: case 5: case 6: {
+      const bool down = step >= 5, wide = step == 3 || step == 6;
+      if (wide && (decode || d.T <= 16)) return hipSuccess;
+      g.mode = down ? 2 : 1;
+      g.K = down ? l.F : l.D;
+      g.N = down ? l.D : l.F;
+      g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
+      g.As = (const float*)(b + (down ? L.hs : L.xs));
+      g.B0 = (const uint8_t*)(down ? l.wd : l.wg);
+      g.B0s = down ? l.wds : l.wgs;
+      g.B1 = (const uint8_t*)l.wu;
+      g.B1s = l.wus;
+      g.out = b + (down ? L.y : L.h);
+      g.odt = l.xdt == MOE_F16 ? MOE_F16 : MOE_F32;
+      g.list = wide ? (const int32_t*)(b + L.sk4)
+                    : decode ? p.dlist : (const int32_t*)(b + L.sk1);
+      g.meta_index = wide ? kMetaSk4 : kMetaSk1;
+      g.max_groups = wide ? L.cap_sk4 : (int)std::min<int64_t>(n_exp, P);
+      return launch_f8_strip(g, wide ? 4 : 1, l.ncu, s);
+    }
+    case 4:
+      return launch_quant_rows(b + L.h, MOE_F32, P, l.F, b + L.h8, (float*)(b + L.hs), s);
+    case 8:
+      return launch_combine(b + L.y, l.xdt == MOE_F16, p.tok2pair, p.w, p.offsets, d.T,
+                            l.D, d.k, d.n_shared, d.E, l.ydt, l.y, s);
+    default:
+      return hipSuccess;
+  }
+}
+
+extern "C" {
+
+moe_status moe_quant_f8(const void* x, int32_t dtype, int64_t rows, int32_t K,
+                        void* q, float* scales, void* stream) {
+  if (!plain_type(dtype))
+    return set_error(MOE_EUNSUPPORTED, "dtype %d: f32, bf16 or f16 only", dtype);
+  if (rows < 0 || K < 8 || K % 8)
+    return set_error(MOE_EINVAL, "rows=%lld must be >= 0 and K=%d a positive multiple of 8",
+                     (long long)rows, K);
+  if (rows > 0 && (!x || !q || !scales)) return set_error(MOE_EINVAL, "x, q or scales is NULL");
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scales))
+    return set_error(MOE_EINVAL, "x, q and scales must be 16-byte aligned");
+  if (rows > ((int64_t)1 << 31) / ((K + 127) / 128) - 1)
+    return set_error(MOE_EUNSUPPORTED, "rows=%lld x K=%d hold 2^31 blocks or more",
+                     (long long)rows, K);
+  if (rows == 0) return MOE_OK;
+  return launched(launch_quant_rows(x, dtype, rows, K, q, scales,
+                                    reinterpret_cast<hipStream_t>(stream)),
+                  "row quantiser");
+}
+
+moe_status moe_quant_f8_weights(const void* w, int32_t dtype, int64_t mats,
+                                int32_t N, int32_t K, void* q, float* scales,
+                                void* stream) {
+  if (!plain_type(dtype))
+    return set_error(MOE_EUNSUPPORTED, "dtype %d: f32, bf16 or f16 only", dtype);
+  if (mats < 0 || N < 0 || K < 8 || K % 8)
+    return set_error(MOE_EINVAL, "mats=%lld and N=%d must be >= 0 and K=%d a positive "
+                     "multiple of 8", (long long)mats, N, K);
+  const bool any = mats > 0 && N > 0;
+  if (any && (!w || !q || !scales)) return set_error(MOE_EINVAL, "w, q or scales is NULL");
+  if (!aligned16(w) || !aligned16(q) || !aligned16(scales))
+    return set_error(MOE_EINVAL, "w, q and scales must be 16-byte aligned");
+  if (!any) return MOE_OK;
+  const int64_t per = (((int64_t)N + 127) / 128) * (((int64_t)K + 127) / 128);
+  if (per >= ((int64_t)1 << 31) || mats > (((int64_t)1 << 31) - 1) / per)
+    return set_error(MOE_EUNSUPPORTED, "the weights hold 2^31 blocks or more");
+  return launched(launch_quant_weights(w, dtype, mats, N, K, q, scales,
+                                       reinterpret_cast<hipStream_t>(stream)),
+                  "weight quantiser");
+}
+
+size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K) {
+  if (M < 0 || N < 0 || K < 16 || K % 16) {
+    set_error(MOE_EINVAL, "M and N must be >= 0 and K=%d a positive multiple of 16", K);
+    return 0;
+  }
+  return 256;
+}
+
+moe_status moe_gemm_f8(const void* x, const float* x_scales, const void* w,
+                       const float* w_scales, int64_t M, int32_t N, int32_t K,
+                       void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!plain_type(out_dtype))
+    return set_error(MOE_EUNSUPPORTED, "output dtype %d: f32, bf16 or f16 only", out_dtype);
+  const size_t need = moe_gemm_f8_workspace_bytes(M, N, K);
+  if (need == 0) return MOE_EINVAL;
+  const bool any = M > 0 && N > 0;
+  if (any && (!x || !x_scales || !w || !w_scales || !out))
+    return set_error(MOE_EINVAL, "x, w, their scales and out must be non-NULL");
+  if (!aligned16(x) || !aligned16(x_scales) || !aligned16(w) || !aligned16(w_scales) ||
+      !aligned16(out))
+    return set_error(MOE_EINVAL, "pointers must be 16-byte aligned");
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return set_error(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
+  if (ws_bytes < need)
+    return set_error(MOE_EWORKSPACE, "product workspace %zu bytes < %zu needed", ws_bytes, need);
+  if (M > (int64_t)INT32_MAX)
+    return set_error(MOE_EUNSUPPORTED, "M=%lld must be below 2^31", (long long)M);
+  if (!any) return MOE_OK;
+  int ncu;
+  const moe_status st = current_cus(&ncu);
+  if (st != MOE_OK) return st;
+  F8Args g{};
+  g.M = M; g.N = N; g.K = K;
+  g.A = (const uint8_t*)x; g.As = x_scales;
+  g.B0 = (const uint8_t*)w; g.B0s = w_scales;
+  g.out = out; g.odt = out_dtype;
+  return launched(launch_f8_strip(g, M <= 16 ? 1 : 4, ncu, reinterpret_cast<hipStream_t>(stream)),
+                  "8-bit product");
+}
+
+// ---- norms --------------------------------------------------------------------
+
+static moe_status norm_desc_ok(const moe_norm_desc* d) {
+  if (!d) return set_error(MOE_EINVAL, "desc is NULL");
+  if (d->T < 0 || d->D < 8 || d->D % 8)
+    return set_error(MOE_EINVAL, "T=%d must be >= 0 and D=%d a positive multiple of 8", d->T, d->D);
+  if (d->D > MOE_NORM_MAX_D)
+    return set_error(MOE_EUNSUPPORTED, "D=%d above %d", d->D, MOE_NORM_MAX_D);
+  if (!plain_type(d->residual_dtype) || !plain_type(d->block_dtype) ||
+      !plain_type(d->weight_dtype) || !plain_type(d->gate_dtype))
+    return set_error(MOE_EUNSUPPORTED, "residual, block, weight and gate dtypes: f32, bf16 or f16");
+  if (!plain_type(d->x_dtype) && d->x_dtype != MOE_F8B128)
+    return set_error(MOE_EUNSUPPORTED, "x dtype %d: f32, bf16, f16 or MOE_F8B128", d->x_dtype);
+  if (d->gate_kind < MOE_GATE_NONE || d->gate_kind > MOE_GATE_TOKEN)
+    return set_error(MOE_EINVAL, "gate kind %d", d->gate_kind);
+  if (!std::isfinite(d->alpha) || !std::isfinite(d->eps) || d->eps < 0.f)
+    return set_error(MOE_EINVAL, "alpha must be finite, eps finite and >= 0");
+  if (d->flags & ~MOE_NORM_UNIT_OFFSET) return set_error(MOE_EINVAL, "flags %d", d->flags);
+  return MOE_OK;
+}
+
+moe_status moe_norm_forward(const moe_norm_desc* d, const void* residual,
+                            const void* block, const void* post_weight,
+                            const void* gate, const void* weight,
+                            void* residual_out, void* x, float* x_scales,
+                            void* stream) {
+  const moe_status st = norm_desc_ok(d);
+  if (st != MOE_OK) return st;
+  if (!block && (post_weight || d->gate_kind != MOE_GATE_NONE))
+    return set_error(MOE_EINVAL, "a post-norm or a gate needs a block output");
+  if (!block && !weight) return set_error(MOE_EINVAL, "neither a block nor a weight: nothing to do");
+  if (d->T > 0) {
+    if (!residual) return set_error(MOE_EINVAL, "residual is NULL");
+    if (block && !residual_out) return set_error(MOE_EINVAL, "residual_out is NULL");
+    if (weight && !x) return set_error(MOE_EINVAL, "x is NULL");
+    if (weight && d->x_dtype == MOE_F8B128 && !x_scales)
+      return set_error(MOE_EINVAL, "x_scales is NULL for 8-bit rows");
+    if (d->gate_kind != MOE_GATE_NONE && !gate) return set_error(MOE_EINVAL, "gate is NULL");
+  }
+  for (const void* p : {residual, block, post_weight, gate, weight, (const void*)residual_out,
+                        (const void*)x, (const void*)x_scales})
+    if (!aligned16(p)) return set_error(MOE_EINVAL, "pointers must be 16-byte aligned");
+  if (d->T == 0) return MOE_OK;
+  NormArgs a{};
+  a.T = d->T; a.D = d->D; a.nb = (d->D + 127) / 128;
+  a.rdt = d->residual_dtype; a.udt = d->block_dtype; a.xdt = d->x_dtype;
+  a.wdt = d->weight_dtype; a.gdt = d->gate_dtype;
+  a.gate_token = d->gate_kind == MOE_GATE_TOKEN;
+  a.unit = (d->flags & MOE_NORM_UNIT_OFFSET) != 0;
+  a.alpha = d->alpha; a.eps = d->eps;
+  a.r = residual; a.u = block; a.p = post_weight;
+  a.g = d->gate_kind == MOE_GATE_NONE ? nullptr : gate;
+  a.w = weight;
+  a.r_out = residual_out; a.x = x; a.xs = x_scales;
+  return launched(launch_norm_forward(a, reinterpret_cast<hipStream_t>(stream)), "norm kernel");
+}
+
+size_t moe_norm_backward_workspace_bytes(const moe_norm_desc* d) {
+  if (norm_desc_ok(d) != MOE_OK) return 0;
+  return align256(norm_backward_part_floats(d->T, d->D) * 4);
+}
+
+moe_status moe_norm_backward(const moe_norm_desc* d, const void* residual_out,
+                             const void* block, const void* post_weight,
+                             const void* gate, const void* weight,
+                             const void* dresidual_out, const void* dx,
+                             void* dresidual, void* dblock,
+                             float* dpost_weight, float* dgate, float* dweight,
+                             void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = norm_desc_ok(d);
+  if (st != MOE_OK) return st;
+  if (d->x_dtype == MOE_F8B128)
+    return set_error(MOE_EUNSUPPORTED, "dx is f32, bf16 or f16");
+  if (!block && (post_weight || d->gate_kind != MOE_GATE_NONE))
+    return set_error(MOE_EINVAL, "a post-norm or a gate needs a block output");
+  if (!weight && !dresidual_out)
+    return set_error(MOE_EINVAL, "neither a weight nor dresidual_out: no gradient comes in");
+  if ((weight && !dweight) || (post_weight && !dpost_weight) ||
+      (d->gate_kind != MOE_GATE_NONE && (!gate || !dgate)))
+    return set_error(MOE_EINVAL, "a parameter or its gradient is NULL");
+  if (d->T > 0 && (!dresidual || (block && !dblock) || (weight && (!residual_out || !dx))))
+    return set_error(MOE_EINVAL, "residual_out, dx, dresidual or dblock is NULL");
+  for (const void* p : {residual_out, block, post_weight, gate, weight, dresidual_out, dx,
+                        (const void*)dresidual, (const void*)dblock, (const void*)dpost_weight,
+                        (const void*)dgate, (const void*)dweight})
+    if (!aligned16(p)) return set_error(MOE_EINVAL, "pointers must be 16-byte aligned");
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return set_error(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
+  const size_t need = align256(norm_backward_part_floats(d->T, d->D) * 4);
+  if (ws_bytes < need)
+    return set_error(MOE_EWORKSPACE, "norm workspace %zu bytes < %zu needed", ws_bytes, need);
+  NormBwdArgs a{};
+  a.T = d->T; a.D = d->D;
+  a.rdt = d->residual_dtype; a.udt = d->block_dtype; a.dxdt = d->x_dtype;
+  a.wdt = d->weight_dtype; a.gdt = d->gate_dtype;
+  a.gate_token = d->gate_kind == MOE_GATE_TOKEN;
+  a.unit = (d->flags & MOE_NORM_UNIT_OFFSET) != 0;
+  a.alpha = d->alpha; a.eps = d->eps;
+  a.r = residual_out; a.u = block; a.p = post_weight;
+  a.g = d->gate_kind == MOE_GATE_NONE ? nullptr : gate;
+  a.w = weight;
+  a.dr = dresidual_out; a.dx = dx;
+  a.dr_out = dresidual; a.du = dblock;
+  a.dw = weight ? dweight : nullptr;
+  a.dp = post_weight ? dpost_weight : nullptr;
+  a.dg_channel = d->gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr;
+  a.dg_token = d->gate_kind == MOE_GATE_TOKEN ? dgate : nullptr;
+  a.part = static_cast<float*>(ws);
+  return launched(launch_norm_backward(a, reinterpret_cast<hipStream_t>(stream)),
+                  "norm backward kernel");
+}
+
+}  // extern "C"

@@ -255,7 +255,8 @@ bool dtypes_ok(int xdt, int wdt) {
   return (xdt == MOE_F32 && wdt == MOE_F32) ||
          (xdt == MOE_BF16 && wdt == MOE_BF16) ||
          (xdt == MOE_F16 && wdt == MOE_F16) ||
-         (xdt == MOE_F16 && q4_fmt(wdt) >= 0);
+         (xdt == MOE_F16 && q4_fmt(wdt) >= 0) ||
+         ((xdt == MOE_BF16 || xdt == MOE_F16) && wdt == MOE_F8B128);
 }
 
 int effective_fat_rows(const moe_options& o) {
@@ -352,6 +353,10 @@ bool weight_ok(const moe_weight& w, int wdt, std::string* why, const char* name)
   }
   if (!w.data) { snprintf(buf, sizeof buf, "%s data is NULL", name); *why = buf; return false; }
   if (!aligned16(w.data)) { snprintf(buf, sizeof buf, "%s data not 16-byte aligned", name); *why = buf; return false; }
+  if (wdt == MOE_F8B128) {
+    if (!w.scales) { snprintf(buf, sizeof buf, "%s scales NULL for 8-bit weights", name); *why = buf; return false; }
+    if (!aligned16(w.scales)) { snprintf(buf, sizeof buf, "%s scales not 16-byte aligned", name); *why = buf; return false; }
+  }
   if (q4_fmt(wdt) >= 0) {
     if (!w.scales) { snprintf(buf, sizeof buf, "%s scales NULL for 4-bit weights", name); *why = buf; return false; }
     // a lane reads two adjacent parameters as one load
@@ -404,6 +409,14 @@ moe_status launch_plan(const moe_plan_desc& d, const float* logits,
     }
   }
   return MOE_OK;
+}
+
+moe_status moe::current_cus(int* ncu) {
+  int dev;
+  DevInfo info;
+  const moe_status st = device_info(&dev, &info);
+  *ncu = info.ncu;
+  return st;
 }
 
 struct moe_plan {
@@ -605,6 +618,7 @@ size_t moe_forward_workspace_bytes(const moe_plan* p, int32_t D, int32_t F,
     return 0;
   }
   const moe_options o = opt ? *opt : defaults();
+  if (w_dtype == MOE_F8B128) return f8_layer_bytes(p->desc, D, F, x_dtype);
   return fwd_layout(p->desc, D, F, x_dtype, w_dtype, o).bytes;
 }
 
@@ -634,7 +648,10 @@ moe_status moe_forward(const moe_plan* p, const void* x, int32_t x_dtype,
     return fail(MOE_EINVAL, "x and y must be 16-byte aligned");
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return fail(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
-  const FwdLayout L = fwd_layout(d, D, F, x_dtype, wdt, o);
+  const bool f8 = wdt == MOE_F8B128;
+  FwdLayout L{};
+  if (f8) L.bytes = f8_layer_bytes(d, D, F, x_dtype);
+  else L = fwd_layout(d, D, F, x_dtype, wdt, o);
   const size_t Pmax_rows = (size_t)d.T * d.k + (size_t)d.n_shared * d.T;
   const size_t lim31 = ((size_t)1 << 31) - 1;
   if ((size_t)d.T * D * xbytes(x_dtype) > lim31 ||
@@ -658,9 +675,32 @@ moe_status moe_forward(const moe_plan* p, const void* x, int32_t x_dtype,
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* b = static_cast<char*>(ws);
   char* pb = p->ws;
+  hipError_t e;
+  if (f8) {
+    F8Plan fp{};
+    fp.desc = d;
+    fp.ids = (const int32_t*)(pb + p->L.ids);
+    fp.w = (const float*)(pb + p->L.w);
+    fp.tok2pair = (const int32_t*)(pb + p->L.tok2pair);
+    fp.counts = (const int32_t*)(pb + p->L.counts);
+    fp.offsets = (const int32_t*)(pb + p->L.offsets);
+    fp.pair_token = (const int32_t*)(pb + p->L.pair_token);
+    fp.decode = p->L.decode;
+    fp.dlist = (const int32_t*)(pb + p->L.dlist);
+    fp.dmeta = (const int32_t*)(pb + p->L.dmeta);
+    const F8Layer fl{x, x_dtype, w_gate.data, (const float*)w_gate.scales,
+                     w_up.data, (const float*)w_up.scales, w_down.data,
+                     (const float*)w_down.scales, D, F, info.ncu, y, y_dtype, b, o};
+    for (int step = 0; step < kF8Steps; ++step) {
+      const int ph = f8_step_phase(step);
+      PhaseScope ps(rec, ph, s);
+      e = launch_f8_step(fp, fl, step, s);
+      if (e != hipSuccess) return hip_fail(e, "8-bit layer kernel");
+    }
+    return MOE_OK;
+  }
   const int n_exp = d.E + d.n_shared;
   int32_t* meta = (int32_t*)(b + L.meta);
-  hipError_t e;
   // A decode-shaped plan holds at most kDecodeT pairs an expert, so every
   // expert is one thin group unless the S rule sends experts of that size
   // to the full tile; then the plan's own group list stands in for the
@@ -935,6 +975,8 @@ moe_status moe_forward_get_views(const moe_plan* p, int32_t D, int32_t F,
   if (!p || !ws || !v) return fail(MOE_EINVAL, "NULL plan, workspace or views");
   if (D <= 0 || F <= 0 || D % 128 || F % 128 || !dtypes_ok(x_dtype, w_dtype))
     return fail(MOE_EINVAL, "bad sizes or dtypes for the forward views");
+  if (w_dtype == MOE_F8B128)
+    return fail(MOE_EUNSUPPORTED, "no forward views of a layer on 8-bit weights");
   const moe_options o = opt ? *opt : defaults();
   const FwdLayout L = fwd_layout(p->desc, D, F, x_dtype, w_dtype, o);
   const char* b = static_cast<const char*>(ws);

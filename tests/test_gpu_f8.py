@@ -1,0 +1,259 @@
+"""
+The 8-bit block format on the GPU: quantisers bit for bit, the product and
+the routed layer against f64, each within the error that f32 sums and one
+rounding of the output allow (tests/f8_ref.py).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import f8_ref as R
+import mixture_experts_routed_route_amd as moe
+import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _same_values(a, b):
+    a, b = a.float().cpu(), b.float().cpu()
+    return a.shape == b.shape and bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+def _rows(M, K, dt, seed, wide=True):
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randn(M, K, generator=g) * torch.exp(torch.randn(M, 1, generator=g))
+    if wide and K > 8:
+        v[:, 5] *= 50.0
+    return v.to(DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,K", [(1, 8), (1, 128), (3, 136), (17, 1000), (64, 2048), (301, 1544)])
+def test_quant_rows_bit_exact(dt, M, K):
+    v = _rows(M, K, dt, seed=M * 7 + K)
+    q, s = moe.moe_quant_f8(v.cuda())
+    rq, rs = R.quant_rows(v)
+    assert q.dtype == R.F8 and torch.equal(s.cpu(), rs)
+    assert _same_values(q, rq)
+
+
+def test_quant_rows_special_values():
+    """Zero, tiny, halfway, infinite and NaN blocks."""
+    v = torch.zeros(8, 256)
+    v[1, :128] = 1e-35                      # below the scale's floor
+    v[2, :128] = torch.linspace(-1, 1, 128)  # 1 -> 448 exactly
+    v[3, :16] = torch.arange(16) / 16.0
+    v[3, 16] = 1.75                          # 448 / 1.75 = 256: ties
+    v[4, 3] = float("inf")
+    v[5, 200] = float("nan")
+    v[6] = 3e38
+    v[7] = -1e-3
+    v[7, 130] = 5.0
+    q, s = moe.moe_quant_f8(v.cuda())
+    rq, rs = R.quant_rows(v)
+    fine = torch.isfinite(rs)
+    assert torch.equal(s.cpu()[fine], rs[fine])
+    assert not torch.isfinite(s.cpu()[~fine]).any() and (~fine).sum() == 2
+    deq, ref = R.rows_f64(q.cpu(), s.cpu()), R.rows_f64(rq, rs)
+    assert torch.equal(torch.isnan(deq), torch.isnan(ref))
+    ok = ~torch.isnan(ref)
+    assert torch.equal(deq[ok], ref[ok])
+    assert torch.isnan(deq[4, :128]).all() and not torch.isnan(deq[4, 128:]).any()
+
+
+def test_quant_rows_view_and_leading_axes():
+    base = torch.randn(4, 6, 512).to(torch.bfloat16).cuda()
+    q, s = moe.moe_quant_f8(base[:, ::2, :256])   # strided view
+    rq, rs = R.quant_rows(base[:, ::2, :256].reshape(-1, 256).cpu())
+    assert q.shape == (4, 3, 256) and s.shape == (4, 3, 2)
+    assert _same_values(q.view(-1, 256), rq) and torch.equal(s.view(-1, 2).cpu(), rs)
+    q, s = moe.moe_quant_f8(torch.empty(0, 64, device="cuda"))
+    assert q.shape == (0, 64) and s.shape == (0, 1)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,N,K", [(1, 1, 8), (1, 128, 128), (3, 200, 136), (2, 129, 1000), (5, 384, 512)])
+def test_quant_weights_bit_exact(dt, n, N, K):
+    w = _rows(n * N, K, dt, seed=N + K).view(n, N, K)
+    q, s = moe.moe_quant_f8_weights(w.cuda())
+    rq, rs = R.quant_weights(w)
+    assert torch.equal(s.cpu(), rs) and _same_values(q, rq)
+    q2, s2 = moe.moe_quant_f8_weights(w[0].cuda())
+    assert q2.shape == (N, K) and torch.equal(s2.cpu(), rs[0])
+
+
+def _product(M, N, K, out, seed=0):
+    a = R.quant_rows(_rows(M, K, "bf16", seed))
+    w = R.quant_weights((_rows(N, K, "f32", seed + 1, wide=False) * K ** -0.5)[None])
+    w = (w[0][0], w[1][0])
+    got = moe.moe_gemm_f8(tuple(t.cuda() for t in a), tuple(t.cuda() for t in w), out_dtype=DT[out])
+    af, wf = R.rows_f64(*a), R.weights_f64(*w)
+    ref = af @ wf.t()
+    return got, ref, R.product_bound(af, wf, DT[out], ref)
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 16), (1, 16, 128), (1, 2048, 2048), (2, 130, 144), (5, 77, 400), (16, 256, 1024),
+    (17, 33, 256), (63, 129, 1040), (64, 512, 768), (65, 100, 2064), (128, 128, 128),
+    (129, 257, 384), (255, 384, 640), (256, 256, 512), (257, 513, 1296), (517, 1001, 1040),
+    (700, 640, 4096), (1025, 896, 256), (2049, 320, 528)])
+def test_product_against_f64(M, N, K):
+    for out in (["f32", "bf16", "f16"] if M * N < 40000 else ["f32" if M % 2 else "bf16"]):
+        got, ref, bound = _product(M, N, K, out, seed=M + N + K)
+        err = (got.cpu().double() - ref).abs()
+        assert bool((err <= bound).all()), (out, float((err / bound).max()))
+
+
+def test_product_empty_and_leading_axes():
+    a = tuple(t.cuda() for t in R.quant_rows(_rows(12, 256, "bf16", 3)))
+    w = tuple(t[0].cuda() for t in R.quant_weights(torch.randn(1, 40, 256)))
+    one = moe.moe_gemm_f8(a, w, out_dtype=torch.float32)
+    two = moe.moe_gemm_f8((a[0].view(3, 4, 256), a[1].view(3, 4, 2)), w, out_dtype=torch.float32)
+    assert two.shape == (3, 4, 40) and torch.equal(two.view(12, 40), one)
+    none = moe.moe_gemm_f8((a[0][:0], a[1][:0]), w)
+    assert none.shape == (0, 40)
+    # strided codes and scales, and an output given by the caller
+    wide = torch.zeros(12, 512, dtype=torch.float8_e4m3fn, device="cuda")
+    wide[:, :256] = a[0]
+    out = torch.full((12, 40), 7.0, device="cuda")
+    assert moe.moe_gemm_f8((wide[:, :256], a[1]), w, out=out) is out
+    assert torch.equal(out, one)
+
+
+def test_product_keeps_rows_apart():
+    """A NaN row, an infinite scale and a huge row leave the others as they
+    were; rows past the last are not written."""
+    a = list(t.cuda() for t in R.quant_rows(_rows(70, 384, "bf16", 9)))
+    w = tuple(t[0].cuda() for t in R.quant_weights(torch.randn(1, 200, 384)))
+    ref = moe.moe_gemm_f8(tuple(a), w, out_dtype=torch.float32)
+    v = _rows(70, 384, "bf16", 9).float()
+    v[11, 40] = float("nan")
+    v[69, 300] = float("inf")
+    b = moe.moe_quant_f8(v.cuda())
+    store = torch.full((80, 200), 5.0, device="cuda")
+    got = moe.moe_gemm_f8(b, w, out=store[:70])
+    ok = torch.ones(70, dtype=torch.bool)
+    ok[[11, 69]] = False
+    assert torch.equal(got[ok], ref[ok])
+    assert not torch.isfinite(got[~ok]).any()
+    assert bool((store[70:] == 5.0).all())
+
+
+def _layer(T, D, F, E, k, dt, shared=0, cf=0.0, seed=0, bias=None, limit=7.0, x_std=1.0):
+    wl = W.make_layer(T, D, F, E, k, dt, n_shared=shared, seed=seed, capacity_factor=cf,
+                      logit_bias=bias, swiglu_limit=limit, w_std=0.05, x_std=x_std)
+    ws = {n: R.quant_weights(wl[n].float()) for n in ("w_gate", "w_up", "w_down")}
+    return wl, ws
+
+
+def _run(wl, ws, y_dtype, options=None, plan=None):
+    p = plan or moe.moe_plan_create(wl["logits"].cuda(), wl["k"], wl["capacity_factor"], wl["n_shared"])
+    dev = {n: tuple(t.cuda() for t in v) for n, v in ws.items()}
+    opts = options or moe.make_options(swiglu_limit=wl["swiglu_limit"])
+    y = moe.moe_forward(p, wl["x"].cuda(), dev["w_gate"], dev["w_up"], dev["w_down"],
+                        options=opts, y_dtype=y_dtype)
+    return p, y
+
+
+def _check(wl, ws, y_dtype, options=None):
+    p, y = _run(wl, ws, y_dtype, options)
+    v = moe.moe_plan_get_views(p)
+    ids, w = v["topk_id"].cpu().long(), v["topk_w"].cpu()
+    keep = v["tok2pair"].cpu() >= 0
+    pair = torch.float16 if wl["x"].dtype == torch.float16 else torch.float32
+    ref, bound = R.layer(wl["x"], ws["w_gate"], ws["w_up"], ws["w_down"], ids, w, keep,
+                         wl["E"], wl["n_shared"], wl["swiglu_limit"], y_dtype, pair)
+    err = (y.cpu().double() - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    # and the bound says something: it lies below the outputs' size (it adds
+    # absolute values, so terms that cancel in an output do not cancel in it)
+    assert float(bound.mean()) < 0.25 * float(ref.abs().mean())
+    return y
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,D,F,E,k,shared,cf", [
+    (1, 128, 128, 4, 1, 0, 0.0), (1, 256, 384, 8, 3, 1, 0.0), (3, 512, 128, 16, 4, 0, 0.0),
+    (16, 256, 256, 4, 2, 1, 0.0), (17, 384, 256, 5, 2, 0, 1.0), (40, 256, 384, 3, 3, 1, 0.0),
+    (130, 256, 256, 6, 2, 1, 1.25), (300, 384, 128, 4, 1, 0, 0.0), (700, 256, 256, 2, 1, 1, 0.0)])
+def test_layer_against_f64(dt, T, D, F, E, k, shared, cf):
+    wl, ws = _layer(T, D, F, E, k, dt, shared, cf, seed=T + D + E)
+    _check(wl, ws, DT[dt])
+    _check(wl, ws, torch.float32)
+
+
+def test_layer_skewed_and_clamped():
+    """One expert takes most rows, two take none, and the clamp binds."""
+    bias = torch.tensor([8.0, 0.0, -40.0, 1.0, -40.0, 0.5])
+    wl, ws = _layer(900, 256, 384, 6, 2, "bf16", 1, 0.0, seed=4, bias=bias, limit=0.4, x_std=2.0)
+    _check(wl, ws, torch.float32)
+    wl["swiglu_limit"] = 0.0     # no clamp
+    _check(wl, ws, torch.float32)
+
+
+def test_layer_determinism_and_noalloc():
+    wl, ws = _layer(33, 256, 256, 8, 2, "bf16", 1, seed=3)
+    p, y = _run(wl, ws, torch.float32)
+    _, z = _run(wl, ws, torch.float32, plan=p)
+    assert torch.equal(y, z)
+    dev = {n: tuple(t.cuda() for t in v) for n, v in ws.items()}
+    n = moe.moe_forward_noalloc(p, wl["x"].cuda(), dev["w_gate"], dev["w_up"], dev["w_down"])
+    assert torch.equal(y, n)
+
+
+def test_layer_zero_tokens():
+    wl, ws = _layer(4, 128, 128, 4, 2, "bf16")
+    p = moe.moe_plan_create(torch.empty(0, 4, device="cuda"), 2)
+    dev = {n: tuple(t.cuda() for t in v) for n, v in ws.items()}
+    y = moe.moe_forward(p, torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"),
+                        dev["w_gate"], dev["w_up"], dev["w_down"])
+    assert y.shape == (0, 128)
+
+
+def test_layer_phases():
+    wl, ws = _layer(300, 256, 256, 8, 2, "bf16", seed=3)
+    moe.moe_phase_times(reset=True)
+    _run(wl, ws, torch.float32, moe.make_options(flags=moe.MOE_OPT_PHASE_EVENTS))
+    ms, calls = moe.moe_phase_times(reset=True)
+    assert calls == 1 and ms["combine"] > 0 and ms["dequant_once"] > 0
+
+
+def test_graph_replays_and_streams():
+    """The layer, a quantiser and a product captured together, replayed on new
+    inputs between eager work, and run on a stream of their own."""
+    wl, ws = _layer(200, 256, 384, 8, 2, "bf16", 1, seed=8)
+    dev = {n: tuple(t.cuda() for t in v) for n, v in ws.items()}
+    proj = tuple(t[0].cuda() for t in R.quant_weights(torch.randn(1, 192, 256) * 0.1))
+    x, logits = wl["x"].cuda(), wl["logits"].cuda()
+    opts = moe.make_options()
+
+    def step():
+        p = moe.moe_plan_create(logits, 2, 0.0, 1)
+        y = moe.moe_forward(p, x, dev["w_gate"], dev["w_up"], dev["w_down"], options=opts,
+                            y_dtype=torch.bfloat16)
+        q = moe.moe_quant_f8(y)
+        return p, y, moe.moe_gemm_f8(q, proj, out_dtype=torch.float32)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept, gy, gz = step()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for _ in range(3):
+        x.copy_(torch.randn(200, 256, generator=g, device="cuda"))
+        logits.copy_(torch.randn(200, 8, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        ry, rz = gy.clone(), gz.clone()
+        _, y, z = step()
+        assert torch.equal(ry, y) and torch.equal(rz, z)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _, y2, z2 = step()
+    side.synchronize()
+    assert torch.equal(y2, y) and torch.equal(z2, z)
