@@ -424,9 +424,13 @@ moe_status moe_quant_f8_weights(const void *w, int32_t dtype, int64_t mats,
 size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K);
 
 /* out[M, N] = x[M, K] . w[N, K]^T on MOE_F8B128 rows and weights: the codes'
- * products of each block of 128 summed in f32 by the matrix units, scaled by
+ * products of each block of 128 summed by the matrix units, scaled by
  * x_scales * w_scales and added in f32, rounded once to out_dtype (F32, BF16
- * or F16). K a multiple of 16; M below 2^31, M and N any other size (0
+ * or F16). An F32 output's sums are f32 throughout; for a 16-bit output of
+ * more than 64 rows each eight neighbouring products are aligned to the
+ * largest among them, bits below 2^-13 of its exponent dropped (the 8-bit
+ * matrix unit's sum; about 1.5e-5 of the output). K a multiple of 16 up to
+ * 2^22; M below 2^31, M and N any other size (0
  * writes nothing). Pointers 16-byte aligned, ws 256-byte aligned. Async on
  * `stream`. */
 moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,

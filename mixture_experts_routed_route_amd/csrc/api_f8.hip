@@ -23,6 +23,9 @@ moe_status launched(hipError_t e, const char* where) {
   return set_error(MOE_EHIP, "%s: %s (%s)", where, hipGetErrorName(e), hipGetErrorString(e));
 }
 
+// 256 rows of codes stay below 2 GiB
+constexpr int kF8MaxK = 1 << 22;
+
 // The layer's workspace: quantised x, the SwiGLU outputs in f32 and
 // quantised, the pairs' unweighted outputs, the work lists.
 struct F8Layout {
@@ -62,11 +65,15 @@ size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt) {
 }
 
 // 0 quantise x, 1 classify, 2 / 3 gate/up of groups of <= 16 / 17..64 rows,
-// 4 quantise h, 5 / 6 down of the same groups, 7 unused, 8 combine
+// 4 gate/up tile, 5 quantise the groups' h, 6 / 7 down of the groups, 8 down
+// tile, 9 combine
 int moe::f8_step_phase(int step) {
-  static const int ph[kF8Steps] = {1, 0, 3, 14, 1, 5, 15, 4, 6};
+  static const int ph[kF8Steps] = {1, 0, 3, 14, 2, 1, 5, 15, 4, 6};
   return ph[step];
 }
+
+// Experts of more rows than this take the tile.
+constexpr int kF8ThinRows = 64;
 
 hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s) {
   const moe_plan_desc& d = p.desc;
@@ -80,6 +87,22 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   g.offsets = p.offsets;
   g.meta = decode ? p.dmeta : (const int32_t*)(b + L.meta);
   g.clamp = l.o.swiglu_limit;
+  const bool down = step >= 6;
+  g.mode = down ? 2 : 1;
+  g.K = down ? l.F : l.D;
+  g.N = down ? l.D : l.F;
+  g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
+  g.As = (const float*)(b + (down ? L.hs : L.xs));
+  g.B0 = (const uint8_t*)(down ? l.wd : l.wg);
+  g.B0s = down ? l.wds : l.wgs;
+  g.B1 = (const uint8_t*)l.wu;
+  g.B1s = l.wus;
+  g.odt = l.xdt == MOE_F16 ? MOE_F16 : MOE_F32;
+  const int32_t* sk1 = decode ? p.dlist : (const int32_t*)(b + L.sk1);
+  const int32_t* sk4 = (const int32_t*)(b + L.sk4);
+  // an expert holds at most T pairs
+  const bool some4 = !decode && d.T > 16, some_tile = !decode && d.T > kF8ThinRows;
+  const int groups1 = (int)std::min<int64_t>(n_exp, P);
   switch (step) {
     case 0:
       return launch_quant_rows(l.x, l.xdt, d.T, l.D, b + L.x8, (float*)(b + L.xs), s);
@@ -89,7 +112,7 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       ca.counts = p.counts;
       ca.n_exp = n_exp;
       ca.mode = 1;
-      ca.S = 1e30;
+      ca.S = kF8ThinRows;
       ca.full_tiles = (int32_t*)(b + L.full_tiles);
       ca.sk1 = (int32_t*)(b + L.sk1);
       ca.sk4 = (int32_t*)(b + L.sk4);
@@ -100,29 +123,34 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       ca.meta = (int32_t*)(b + L.meta);
       return launch_classify(ca, s);
     }
-    case 2: case 3: case 5: case 6: {
-      const bool down = step >= 5, wide = step == 3 || step == 6;
-      if (wide && (decode || d.T <= 16)) return hipSuccess;
-      g.mode = down ? 2 : 1;
-      g.K = down ? l.F : l.D;
-      g.N = down ? l.D : l.F;
-      g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
-      g.As = (const float*)(b + (down ? L.hs : L.xs));
-      g.B0 = (const uint8_t*)(down ? l.wd : l.wg);
-      g.B0s = down ? l.wds : l.wgs;
-      g.B1 = (const uint8_t*)l.wu;
-      g.B1s = l.wus;
+    case 2: case 3: case 6: case 7: {
+      const bool wide = step == 3 || step == 7;
+      if (wide && !some4) return hipSuccess;
       g.out = b + (down ? L.y : L.h);
-      g.odt = l.xdt == MOE_F16 ? MOE_F16 : MOE_F32;
-      g.list = wide ? (const int32_t*)(b + L.sk4)
-                    : decode ? p.dlist : (const int32_t*)(b + L.sk1);
+      g.list = wide ? sk4 : sk1;
       g.meta_index = wide ? kMetaSk4 : kMetaSk1;
-      g.max_groups = wide ? L.cap_sk4 : (int)std::min<int64_t>(n_exp, P);
+      g.max_groups = wide ? L.cap_sk4 : groups1;
       return launch_f8_strip(g, wide ? 4 : 1, l.ncu, s);
     }
-    case 4:
-      return launch_quant_rows(b + L.h, MOE_F32, P, l.F, b + L.h8, (float*)(b + L.hs), s);
-    case 8:
+    case 4: case 8:
+      if (!some_tile) return hipSuccess;
+      g.out = b + (down ? L.y : L.h8);
+      g.out_s = (float*)(b + L.hs);
+      g.list = (const int32_t*)(b + L.full_tiles);
+      g.meta_index = kMetaFullTiles;
+      g.max_groups = L.cap_tiles;
+      // an f16 layer's gate/up sums stay exact: a code of h that moves by a
+      // step weighs more than f16's rounding of y
+      return launch_f8_tile(g, !down && l.xdt == MOE_F16, s);
+    case 5: {
+      const float* h = (const float*)(b + L.h);
+      hipError_t e = launch_quant_groups(h, l.F, b + L.h8, (float*)(b + L.hs), sk1,
+                                         g.meta + kMetaSk1, groups1, 16, s);
+      if (e != hipSuccess || !some4) return e;
+      return launch_quant_groups(h, l.F, b + L.h8, (float*)(b + L.hs), sk4,
+                                 g.meta + kMetaSk4, L.cap_sk4, 64, s);
+    }
+    case 9:
       return launch_combine(b + L.y, l.xdt == MOE_F16, p.tok2pair, p.w, p.offsets, d.T,
                             l.D, d.k, d.n_shared, d.E, l.ydt, l.y, s);
     default:
@@ -173,8 +201,8 @@ moe_status moe_quant_f8_weights(const void* w, int32_t dtype, int64_t mats,
 }
 
 size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K) {
-  if (M < 0 || N < 0 || K < 16 || K % 16) {
-    set_error(MOE_EINVAL, "M and N must be >= 0 and K=%d a positive multiple of 16", K);
+  if (M < 0 || N < 0 || K < 16 || K % 16 || K > kF8MaxK) {
+    set_error(MOE_EINVAL, "M and N must be >= 0 and K=%d a multiple of 16 in 16..%d", K, kF8MaxK);
     return 0;
   }
   return 256;
@@ -209,8 +237,10 @@ moe_status moe_gemm_f8(const void* x, const float* x_scales, const void* w,
   g.A = (const uint8_t*)x; g.As = x_scales;
   g.B0 = (const uint8_t*)w; g.B0s = w_scales;
   g.out = out; g.odt = out_dtype;
-  return launched(launch_f8_strip(g, M <= 16 ? 1 : 4, ncu, reinterpret_cast<hipStream_t>(stream)),
-                  "8-bit product");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (M > kF8ThinRows)
+    return launched(launch_f8_tile(g, out_dtype == MOE_F32, s), "8-bit product");
+  return launched(launch_f8_strip(g, M <= 16 ? 1 : 4, ncu, s), "8-bit product");
 }
 
 // ---- norms --------------------------------------------------------------------

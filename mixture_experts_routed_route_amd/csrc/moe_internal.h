@@ -310,6 +310,13 @@ hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
 hipError_t launch_quant_weights(const void* w, int dt, int64_t mats, int N,
                                 int K, void* q, float* s, hipStream_t st);
 
+// The rows of a plan's groups (expert, row0, rows, first pair), *n_groups of
+// them (at most max_groups, at most group_rows rows each): f32 rows of pairs
+// [P, F] to codes and scales.
+hipError_t launch_quant_groups(const float* h, int F, void* q, float* s,
+                               const int32_t* list, const int32_t* n_groups,
+                               int max_groups, int group_rows, hipStream_t st);
+
 // One product on e4m3 rows: out[row, n] = sum_b As[row, b] Bs[n / 128, b]
 // sum_{k in block b} A[row, k] B[n, k].
 struct F8Args {
@@ -327,10 +334,15 @@ struct F8Args {
   const int32_t* list;      // strip: (expert, row0, rows, first pair) groups
   const int32_t* meta; int meta_index;
   int max_groups;           // most groups the list can hold
-  void* out; int odt;       // plain and down: [rows, N]; gate/up: f32 [P, N]
+  void* out; int odt;       // plain and down: [rows, N]; gate/up: strip f32
+                            // [P, N], tile codes [P, N] ...
+  float* out_s;             // ... with scales [P, N / 128]
   float clamp;
 };
 hipError_t launch_f8_strip(const F8Args& a, int rb, int ncu, hipStream_t s);
+// list: (expert, row0) tiles of kFullBM rows, max_groups of them at most.
+// prec 0: codes in the 8-bit matrix unit; 1: widened to f16
+hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s);
 
 // The layer on MOE_F8B128 weights (api_f8.hip): its device workspace and its
 // launches, on a plan's arrays.
@@ -353,7 +365,7 @@ struct F8Layer {
 };
 size_t f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt);
 // steps of the layer in order; `phase` is the index moe_phase_times reports
-constexpr int kF8Steps = 9;
+constexpr int kF8Steps = 10;
 int f8_step_phase(int step);
 hipError_t launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s);
 

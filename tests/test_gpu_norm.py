@@ -256,7 +256,7 @@ def test_layer_step_together():
     assert bool(((deq - ref_x).abs() <= R.half_step(R.F8) * (ref_x.abs() + ex) + step8 * 2.0 ** -10 + 2 * ex).all())
     wf = R.weights_f64(*cpu(proj))
     ref_z = deq @ wf.t()
-    assert bool(((z.cpu().double() - ref_z).abs() <= R.product_bound(deq, wf, bf, ref_z)).all())
+    assert bool(((z.cpu().double() - ref_z).abs() <= R.product_bound(deq, wf, bf, ref_z, units8=True)).all())
 
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
