@@ -30,6 +30,11 @@ constexpr int kStageB = kStageW + kTT * 128;
 constexpr int kScaleK = 32;              // blocks of K whose row scales are held at once
 constexpr int kTileLds = 2 * kStageB + kScaleK * kTT * 4;   // 160 KB
 
+// Fragments are read as vector types: a read of a struct (uint4) loses its
+// type on the way to the instruction, and the compiler then guards it with a
+// wait for every direct-to-LDS load in flight.
+typedef int v4i32 __attribute__((ext_vector_type(4)));
+
 // 16-byte piece c of row r of a stage lies at piece c ^ ((r >> 1) & 7) of
 // the row's 128 bytes: the 16 rows that one fragment read touches then
 // spread over all 64 banks.
@@ -152,13 +157,37 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
 #pragma unroll
       for (int t = 0; t < TB; ++t) acc[i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
 
+    using Frag = std::conditional_t<PREC == 0, v8i32, Codes>;
+    auto frag = [&](const char* base, int r) {
+      const v4i32 lo = *reinterpret_cast<const v4i32*>(base + piece(r, 2 * lq));
+      const v4i32 hi = *reinterpret_cast<const v4i32*>(base + piece(r, 2 * lq + 1));
+      return (v8i32)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto operand = [&](const v8i32& v) -> Frag {
+      if constexpr (PREC == 0) return v;
+      else return widen(v);
+    };
+    auto product = [&](const Frag& x, const Frag& y) {
+      if constexpr (PREC == 0) return mfma_f8(x, y, floatx4{0.f, 0.f, 0.f, 0.f});
+      else return block_product(x, y);
+    };
+    // the weights' scales of the held blocks, one a lane (a load inside the
+    // K loop would wait for every load of the next stage)
+    float wl0 = 0.f, wl1 = 0.f;
+    auto lane_of = [](float v, int l) {
+      return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+    };
+
     issue(0);
     for (int kt = 0; kt < nk; ++kt) {
       const int kc = kt % kScaleK;
       if (kc == 0) {
-        // the previous scales' readers are past the barrier below when kt > 0
+        // the previous scales' readers are past this barrier
         if (kt) { fence(); __builtin_amdgcn_s_barrier(); fence(); }
         load_scales(kt);
+        const int c = min(kt + (lane & (kScaleK - 1)), nk - 1);
+        wl0 = ws0[c];
+        if (MODE == 1) wl1 = ws1[c];
       }
       // this wave's loads have landed (and its scale writes); after the
       // barrier every wave's have, and every wave is past its reads of the
@@ -170,41 +199,39 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
       if (kt + 1 < nk) issue(kt + 1);
       const char* sw = smem + (kt & 1) * kStageB;
       const char* st = sw + kStageW;
-      auto frag = [&](const char* base, int r) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(base + piece(r, 2 * lq));
-        const uint4 hi = *reinterpret_cast<const uint4*>(base + piece(r, 2 * lq + 1));
-        return v8i32{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
-                     (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-      };
-      using Frag = std::conditional_t<PREC == 0, v8i32, Codes>;
-      auto as_frag = [&](const v8i32& v) -> Frag {
-        if constexpr (PREC == 0) return v;
-        else return widen(v);
-      };
-      auto product = [&](const Frag& x, const Frag& y) {
-        if constexpr (PREC == 0) return mfma_f8(x, y, floatx4{0.f, 0.f, 0.f, 0.f});
-        else return block_product(x, y);
-      };
-      Frag xt[TB];
+      Frag xt[TB], wv;
+      v8i32 wf[2];
       float s0[TB], s1[TB];
-      const float w0 = ws0[kt], w1 = ws1[kt];
+      const float w0 = lane_of(wl0, kc), w1 = MODE == 1 ? lane_of(wl1, kc) : w0;
+      wf[0] = frag(sw, ww * 128 + lr);
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         const int r = (wt * TB + t) * 16 + lr;
-        xt[t] = as_frag(frag(st, r));
+        xt[t] = operand(frag(st, r));
         const float sr = srow[kc * kTT + r];
         s0[t] = sr * w0;
         s1[t] = MODE == 1 ? sr * w1 : s0[t];
       }
+      // block sums go to the accumulators kLag products later, so that a
+      // wave's matrix instructions do not wait for one another's results
+      constexpr int kN = 8 * TB, kLag = PREC == 0 ? 2 : 1;
+      floatx4 p[kLag + 1];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const Frag wf = as_frag(frag(sw, ww * 128 + i * 16 + lr));
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-          const floatx4 p = product(wf, xt[t]);
+      for (int j = 0; j < kN + kLag; ++j) {
+        if (j < kN) {
+          const int i = j / TB, t = j % TB;
+          if (t == 0) {
+            wv = operand(wf[i & 1]);
+            if (i < 7) wf[(i + 1) & 1] = frag(sw, ww * 128 + (i + 1) * 16 + lr);
+          }
+          p[j % (kLag + 1)] = product(wv, xt[t]);
+        }
+        if (j >= kLag) {
+          const int d = j - kLag, i = d / TB, t = d % TB;
           const float sc = (i & 1) ? s1[t] : s0[t];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][t][q] = fmaf(p[q], sc, acc[i][t][q]);
+          for (int q = 0; q < 4; ++q)
+            acc[i][t][q] = fmaf(p[d % (kLag + 1)][q], sc, acc[i][t][q]);
         }
       }
     }
