@@ -113,6 +113,10 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       ca.n_exp = n_exp;
       ca.mode = 1;
       ca.S = kF8ThinRows;
+      // too few tiles for one round of the compute units: experts of up to
+      // 256 rows go to the strips, 64 rows a group
+      ca.full_nnb = l.F / 128;
+      ca.full_fill = l.ncu;
       ca.full_tiles = (int32_t*)(b + L.full_tiles);
       ca.sk1 = (int32_t*)(b + L.sk1);
       ca.sk4 = (int32_t*)(b + L.sk4);
@@ -156,6 +160,38 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
     default:
       return hipSuccess;
   }
+}
+
+// How a plain product's rows are cut: strips of 64 rows (false), or row tiles
+// of 256, then of 128 or 64 (true; g's tile counts). Each kind's time is
+// rounds of the compute units x steps of 128 codes x the microseconds that a
+// step of its tile was measured to take (8-bit / f16 sums): 256 rows 2.1 /
+// 4.1, 128 rows 1.5 / 1.95, 64 rows 0.87 / 1.25, and a strip launch runs at
+// 172 TFLOP/s. Full rounds of 256-row tiles with a tail of smaller ones beat
+// a last round that few tiles share: 13312 x 4096 x 4096 takes 3 rounds and
+// a tail, not 4.
+static bool f8_split(F8Args* g, bool f32, int ncu) {
+  if (g->M <= kF8ThinRows) return false;
+  const double c256 = f32 ? 4.1 : 2.1, c128 = f32 ? 1.95 : 1.5, c64 = f32 ? 1.25 : 0.87;
+  const int64_t nnb = (g->N + 255) / 256, nk = (g->K + 127) / 128;
+  auto rounds = [&](int64_t tiles) { return (double)((tiles * nnb + ncu - 1) / ncu); };
+  double best = 2.0 * ((g->M + 63) / 64 * 64) * g->N * g->K / 172e6;
+  bool tile = false;
+  const int64_t all = (g->M + 255) / 256, full = all * nnb / ncu * ncu / nnb;
+  for (const int64_t t : {all, std::min(full, g->M / 256), (int64_t)0})
+    for (const int tail : {128, 64}) {
+      const int64_t rest = std::max<int64_t>(0, g->M - t * 256);
+      const int64_t n = (rest + tail - 1) / tail;
+      const double us = nk * (rounds(t) * c256 + rounds(n) * (tail == 128 ? c128 : c64));
+      if (us < best) {
+        best = us;
+        tile = true;
+        g->tiles256 = (int)t;
+        g->tail_rows = tail;
+        g->tail_tiles = (int)n;
+      }
+    }
+  return tile;
 }
 
 extern "C" {
@@ -238,8 +274,8 @@ moe_status moe_gemm_f8(const void* x, const float* x_scales, const void* w,
   g.B0 = (const uint8_t*)w; g.B0s = w_scales;
   g.out = out; g.odt = out_dtype;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (M > kF8ThinRows)
-    return launched(launch_f8_tile(g, out_dtype == MOE_F32, s), "8-bit product");
+  const bool f32 = out_dtype == MOE_F32;
+  if (f8_split(&g, f32, ncu)) return launched(launch_f8_tile(g, f32, s), "8-bit product");
   return launched(launch_f8_strip(g, M <= 16 ? 1 : 4, ncu, s), "8-bit product");
 }
 

@@ -1,8 +1,9 @@
 // Products on 8-bit blocks, many rows: a 256 x 256 tile on gfx950.
 //
-// One block of 8 waves computes 256 weight rows x up to 256 rows; a wave
-// owns 128 weight rows x 64, 32 or 16 rows (4, 2 or 1 fragments of 16: the
-// tile's rows rounded up to 256, 128 or 64). K streams in steps of one scale
+// One block of 8 waves computes 256 weight rows x up to 256, 128 or 64 rows;
+// the waves stand 2 x 4, 4 x 2 or 8 x 1, so that each owns 64 rows and 128,
+// 64 or 32 weight rows (the layout that reads the fewest fragments from LDS
+// at each size). K streams in steps of one scale
 // block, 128 codes, through two LDS stages of 64 KB that buffer_load ... lds
 // fills directly while the other is multiplied. A fragment's block sum
 // starts from zero in the matrix unit and one fma a value adds it, scaled,
@@ -27,8 +28,8 @@ constexpr int kTW = 256;                 // weight rows of a tile
 constexpr int kTT = 256;                 // rows of a tile
 constexpr int kStageW = kTW * 128;       // bytes of a stage's weight codes
 constexpr int kStageB = kStageW + kTT * 128;
-constexpr int kScaleK = 32;              // blocks of K whose row scales are held at once
-constexpr int kTileLds = 2 * kStageB + kScaleK * kTT * 4;   // 160 KB
+constexpr int kScaleK = 4;               // blocks of K whose row scales are loaded at once
+constexpr int kTileLds = 2 * kStageB + 2 * kScaleK * kTT * 4;   // 136 KB
 
 // Fragments are read as vector types: a read of a struct (uint4) loses its
 // type on the way to the instruction, and the compiler then guards it with a
@@ -36,8 +37,11 @@ constexpr int kTileLds = 2 * kStageB + kScaleK * kTT * 4;   // 160 KB
 typedef int v4i32 __attribute__((ext_vector_type(4)));
 
 // 16-byte piece c of row r of a stage lies at piece c ^ ((r >> 1) & 7) of
-// the row's 128 bytes: the 16 rows that one fragment read touches then
-// spread over all 64 banks.
+// the row's 128 bytes. Lane group q of a fragment reads pieces q and q + 4
+// (both operands the same, so the order of K within a block is free): the
+// LDS serves a 16-byte read in groups of 16 lanes such as 0-3, 12-15, 20-27,
+// and these then touch all 64 banks once (pieces 2 q and 2 q + 1 met in
+// pairs: half of the LDS cycles of an 8192^3 product were conflicts).
 __device__ __forceinline__ int piece(int r, int c) {
   return r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
 }
@@ -49,28 +53,43 @@ __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
 template <int MODE, int PREC>
 __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
   __shared__ __attribute__((aligned(1024))) char smem[kTileLds];
-  float* const srow = reinterpret_cast<float*>(smem + 2 * kStageB);   // [kScaleK][kTT]
+  float* const srow = reinterpret_cast<float*>(smem + 2 * kStageB);   // [2 kScaleK][kTT]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ww = wave >> 2, wt = wave & 3;
   const int lr = lane & 15, lq = lane >> 4;
   const int K = a.K, N = a.N;
   const int nk = (K + 127) / 128;
   const int NNB = MODE == 1 ? N / 128 : (N + kTW - 1) / kTW;
-  const int n_tiles = MODE == 0 ? (int)((a.M + kTT - 1) / kTT) : a.meta[a.meta_index];
-  const int n_items = n_tiles * NNB;
-  const int b = xcd_item(0, blockIdx.x, gridDim.x, n_items);
-  if (b < 0) return;   // the whole block, before any barrier
-  // 4 row tiles x all column blocks at a time, rows first
-  const int group = b / (4 * NNB), first = group * 4;
-  const int gm = min(4, n_tiles - first);
-  const int within = b - first * NNB;
-  const int ti = first + within % gm, nb = within / gm;
+  // Block b runs on XCD b mod 8, whose L2 its neighbours share.
+  int ti, nb;
+  if (MODE == 0) {
+    // a.tiles256 tiles of 256 rows, then tiles of a.tail_rows; each kind's
+    // items in eight contiguous runs, one an XCD, four row tiles by all
+    // column blocks at a time
+    const int n_big = a.tiles256 * NNB, g_big = (n_big + 7) & ~7;
+    const bool big = (int)blockIdx.x < g_big;
+    const int n = big ? a.tiles256 : a.tail_tiles;
+    const int it = big ? xcd_item(0, blockIdx.x, g_big, n_big)
+                       : xcd_item(0, blockIdx.x - g_big, gridDim.x - g_big, n * NNB);
+    if (it < 0) return;   // the whole block, before any barrier
+    const int first = it / (4 * NNB) * 4;
+    const int gm = min(4, n - first), within = it - first * NNB;
+    ti = first + within % gm + (big ? 0 : a.tiles256);
+    nb = within / gm;
+  } else {
+    // the list's tiles, most rows first, go to the XCDs in turn
+    const int m = blockIdx.x >> 3;
+    ti = m / NNB * 8 + (blockIdx.x & 7);
+    nb = m % NNB;
+    if (ti >= a.meta[a.meta_index]) return;
+  }
   int e = 0, rows;
   int64_t row0;
   if (MODE == 0) {
-    row0 = (int64_t)ti * kTT;
-    rows = (int)min((int64_t)kTT, a.M - row0);
+    const int tail = ti - a.tiles256;
+    row0 = tail < 0 ? (int64_t)ti * kTT
+                    : (int64_t)a.tiles256 * kTT + (int64_t)tail * a.tail_rows;
+    rows = (int)min((int64_t)(tail < 0 ? kTT : a.tail_rows), a.M - row0);
   } else {
     e = a.list[2 * ti];
     const int r0 = a.list[2 * ti + 1], off = a.offsets[e];
@@ -79,10 +98,15 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
   }
   const int n0 = nb * (MODE == 1 ? 128 : kTW);
 
-  auto run = [&](auto tb_c) {
-    constexpr int TB = decltype(tb_c)::value;   // 16-row fragments a wave
+  // NW waves along the weight rows, 8 / NW along the rows
+  auto run = [&](auto nw_c) {
+    constexpr int NW = decltype(nw_c)::value, NT = 8 / NW;
+    constexpr int FW = 16 / NW;      // a wave's fragments of 16 weight rows
+    constexpr int TB = 4;            // and of 16 rows
+    constexpr int DT = NT;           // 8-row loads of a wave's share of a stage's rows
+    const int ww = wave / NT, wt = wave % NT;
     // ---- this lane's sources of a stage: wave w fills weight rows 32 w ..
-    // 32 w + 31 (four loads of 8 rows) and rows 8 TB w .. of the tile
+    // 32 w + 31 (four loads of 8 rows) and rows 8 DT w .. of the tile
     const int dr = lane >> 3, dc = lane & 7;
     const size_t mat = (size_t)e * N * K;
     const __amdgpu_buffer_rsrc_t rw0 =
@@ -92,26 +116,25 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
     const __amdgpu_buffer_rsrc_t rt =
         MODE == 1 ? make_rsrc(a.A, 0x7FFFFFFFu)
                   : make_rsrc(a.A + (size_t)row0 * K, (uint32_t)(rows * (int64_t)K));
-    uint32_t vw[4], vt[TB];
-    int cw[4], ct[TB];   // byte of the row at which the lane's piece starts
+    uint32_t vw[4], vt[DT];
+    // byte of the row at which the lane's piece starts, for even and odd
+    // groups of 8 stage rows
+    const int cb[2] = {(dc ^ (dr >> 1)) * 16, (dc ^ (dr >> 1) ^ 4) * 16};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int R = 32 * wave + 8 * j + dr;
-      cw[j] = (dc ^ ((R >> 1) & 7)) * 16;
       int row = R;
-      // gate/up: fragments of 16 rows alternate W_gate / W_up, 64 features
-      // a half of the tile
-      if (MODE == 1) row = (R >> 7) * 64 + ((R >> 5) & 3) * 16 + (R & 15);
+      // gate/up: fragments of 16 rows alternate W_gate / W_up
+      if (MODE == 1) row = (R >> 5) * 16 + (R & 15);
       else row = min(R, N - n0 - 1);
-      vw[j] = (uint32_t)row * (uint32_t)K + (uint32_t)cw[j];
+      vw[j] = (uint32_t)row * (uint32_t)K + (uint32_t)cb[j & 1];
     }
 #pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      const int R = (wave * TB + j) * 8 + dr;
-      ct[j] = (dc ^ ((R >> 1) & 7)) * 16;
+    for (int j = 0; j < DT; ++j) {
+      const int R = (wave * DT + j) * 8 + dr;
       const int rr = min(R, rows - 1);
       const int src = MODE == 1 ? a.pair_token[row0 + rr] : rr;
-      vt[j] = (uint32_t)src * (uint32_t)K + (uint32_t)ct[j];
+      vt[j] = (uint32_t)src * (uint32_t)K + (uint32_t)cb[(DT == 1 ? wave : j) & 1];
     }
     auto issue = [&](int kt) {
       char* st = smem + (kt & 1) * kStageB;
@@ -121,46 +144,51 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
         // gate/up: rows 16..31 of every 32 are W_up's
         const __amdgpu_buffer_rsrc_t r = MODE == 1 && (j & 2) ? rw1 : rw0;
         uint32_t v = vw[j];
-        if (MODE == 0 && k0 + cw[j] >= K) v = 0x80000000u;   // past the row: zeros
+        if (MODE == 0 && k0 + cb[j & 1] >= K) v = 0x80000000u;   // past the row: zeros
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(st + (wave * 4 + j) * 1024), 16,
                                                  (int)v, k0, 0, 0);
       }
 #pragma unroll
-      for (int j = 0; j < TB; ++j) {
+      for (int j = 0; j < DT; ++j) {
         uint32_t v = vt[j];
-        if (MODE == 0 && k0 + ct[j] >= K) v = 0x80000000u;
+        if (MODE == 0 && k0 + cb[(DT == 1 ? wave : j) & 1] >= K) v = 0x80000000u;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rt, (lds_ptr_t)(st + kStageW + (wave * TB + j) * 1024), 16, (int)v, k0, 0, 0);
+            rt, (lds_ptr_t)(st + kStageW + (wave * DT + j) * 1024), 16, (int)v, k0, 0, 0);
       }
     };
-    // row scales of blocks kc .. kc + kScaleK - 1 to srow[block][row]: lane
-    // groups of 16 take neighbouring blocks of one row
-    auto load_scales = [&](int kc) {
-      const int nc = min(kScaleK, nk - kc);
-      for (int i = tid; i < 64 * TB * 16; i += 512) {
-        const int r = i >> 4;
-        const int rr = min(r, rows - 1);
-        const int64_t src = MODE == 1 ? (int64_t)a.pair_token[row0 + rr] : row0 + rr;
-        for (int c = i & 15; c < nc; c += 16) srow[c * kTT + r] = a.As[src * nk + kc + c];
-      }
+    // Row scales, four blocks at a time: thread (row, half) loads two of them
+    // with the first stage of the four before, and writes them to LDS one
+    // step later, when every load has landed anyway.
+    const int sc_r = tid & (kTT - 1), sc_h = 2 * (tid >> 8);
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(MODE == 1 ? a.As : a.As + (size_t)row0 * nk, 0x7FFFFFFFu);
+    uint32_t sc_off;
+    {
+      const int rr = min(sc_r, rows - 1);
+      sc_off = (uint32_t)(MODE == 1 ? a.pair_token[row0 + rr] : rr) * (uint32_t)nk * 4u;
+    }
+    float sc_v[2];
+    auto load_scales = [&](int kb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        sc_v[j] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            rs, (int)(sc_off + (uint32_t)min(kb + sc_h + j, nk - 1) * 4u), 0, 0));
+    };
+    auto write_scales = [&](int kb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) srow[((kb & 4) + sc_h + j) * kTT + sc_r] = sc_v[j];
     };
     // the weights' scales: one a wave's 128 rows and block (gate/up: one of
     // each matrix)
     const int nn = (N + 127) / 128;
-    const int sb = MODE == 1 ? nb : min(nb * 2 + ww, nn - 1);
+    const int sb = MODE == 1 ? nb : min(nb * 2 + ww / (NW / 2), nn - 1);
     const float* ws0 = a.B0s + ((size_t)e * nn + sb) * nk;
     const float* ws1 = MODE == 1 ? a.B1s + ((size_t)e * nn + sb) * nk : ws0;
 
-    floatx4 acc[8][TB];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int t = 0; t < TB; ++t) acc[i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-
     using Frag = std::conditional_t<PREC == 0, v8i32, Codes>;
     auto frag = [&](const char* base, int r) {
-      const v4i32 lo = *reinterpret_cast<const v4i32*>(base + piece(r, 2 * lq));
-      const v4i32 hi = *reinterpret_cast<const v4i32*>(base + piece(r, 2 * lq + 1));
+      const v4i32 lo = *reinterpret_cast<const v4i32*>(base + piece(r, lq));
+      const v4i32 hi = *reinterpret_cast<const v4i32*>(base + piece(r, lq + 4));
       return (v8i32)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     auto operand = [&](const v8i32& v) -> Frag {
@@ -171,50 +199,79 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
       if constexpr (PREC == 0) return mfma_f8(x, y, floatx4{0.f, 0.f, 0.f, 0.f});
       else return block_product(x, y);
     };
-    // the weights' scales of the held blocks, one a lane (a load inside the
-    // K loop would wait for every load of the next stage)
+    // the weights' scales of 64 blocks, one a lane (a load at every step
+    // would wait for every load of the next stage)
     float wl0 = 0.f, wl1 = 0.f;
     auto lane_of = [](float v, int l) {
       return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
     };
 
+    auto fill_weights = [&](int kb) {
+      const int c = min(kb + lane, nk - 1);
+      wl0 = ws0[c];
+      if (MODE == 1) wl1 = ws1[c];
+    };
+    fill_weights(0);
+    load_scales(0);
     issue(0);
-    for (int kt = 0; kt < nk; ++kt) {
-      const int kc = kt % kScaleK;
-      if (kc == 0) {
-        // the previous scales' readers are past this barrier
-        if (kt) { fence(); __builtin_amdgcn_s_barrier(); fence(); }
-        load_scales(kt);
-        const int c = min(kt + (lane & (kScaleK - 1)), nk - 1);
-        wl0 = ws0[c];
-        if (MODE == 1) wl1 = ws1[c];
-      }
-      // this wave's loads have landed (and its scale writes); after the
-      // barrier every wave's have, and every wave is past its reads of the
-      // other stage, which the next loads fill
+    write_scales(0);
+    floatx4 acc[FW][TB];
+#pragma unroll
+    for (int i = 0; i < FW; ++i)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) acc[i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    // Once every wave is past its reads of stage kn - 1 and its loads of
+    // stage kn (and its scale writes) have landed: the next stage's loads and
+    // the scales of the blocks ahead.
+    auto next_stage = [&](int kn) {
       fence();
       wait_vm_lgkm0<0>();
       __builtin_amdgcn_s_barrier();
       fence();
-      if (kt + 1 < nk) issue(kt + 1);
+      if ((kn & 3) == 1 && kn + 3 < nk) write_scales(kn + 3);
+      if (kn && (kn & 63) == 0) {
+        fill_weights(kn);
+        // waited for here, before the next stage's loads: at their use the
+        // wait would cover those too
+        wait_vmcnt<0>();
+        asm volatile("" : "+v"(wl0), "+v"(wl1));
+      }
+      if ((kn & 3) == 0 && kn + 4 < nk) load_scales(kn + 4);
+      if (kn + 1 < nk) issue(kn + 1);
+    };
+    auto row_scale = [&](int kt, int t) {
+      return srow[(kt & 7) * kTT + (wt * TB + t) * 16 + lr];
+    };
+    Frag xt[TB], wv;
+    v8i32 wf[2];
+    float sr[TB], s0[TB], s1[TB];
+    auto first_weights = [&](int kt) {
+      wf[0] = frag(smem + (kt & 1) * kStageB, ww * FW * 16 + lr);
+    };
+    auto row_fragment = [&](int kt, int t) {
+      xt[t] = operand(frag(smem + (kt & 1) * kStageB + kStageW, (wt * TB + t) * 16 + lr));
+      sr[t] = row_scale(kt, t);
+    };
+    next_stage(0);
+    first_weights(0);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) row_fragment(0, t);
+    for (int kt = 0; kt < nk; ++kt) {
       const char* sw = smem + (kt & 1) * kStageB;
-      const char* st = sw + kStageW;
-      Frag xt[TB], wv;
-      v8i32 wf[2];
-      float s0[TB], s1[TB];
-      const float w0 = lane_of(wl0, kc), w1 = MODE == 1 ? lane_of(wl1, kc) : w0;
-      wf[0] = frag(sw, ww * 128 + lr);
+      const float w0 = lane_of(wl0, kt & 63), w1 = MODE == 1 ? lane_of(wl1, kt & 63) : w0;
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        const int r = (wt * TB + t) * 16 + lr;
-        xt[t] = operand(frag(st, r));
-        const float sr = srow[kc * kTT + r];
-        s0[t] = sr * w0;
-        s1[t] = MODE == 1 ? sr * w1 : s0[t];
+        s0[t] = sr[t] * w0;
+        s1[t] = MODE == 1 ? sr[t] * w1 : s0[t];
       }
-      // block sums go to the accumulators kLag products later, so that a
-      // wave's matrix instructions do not wait for one another's results
-      constexpr int kN = 8 * TB, kLag = PREC == 0 ? 2 : 1;
+      // Block sums go to the accumulators kLag products later, so that a
+      // wave's matrix instructions do not wait for one another's results.
+      // The stages change hands before the last weight fragment's products,
+      // whose rows' registers then take the next step's fragments one by
+      // one: the next step's products start without a wait (all waves read
+      // their first fragments at once otherwise, a quarter of the step).
+      constexpr int kN = FW * TB, kLag = PREC == 0 ? 3 : 1;
       floatx4 p[kLag + 1];
 #pragma unroll
       for (int j = 0; j < kN + kLag; ++j) {
@@ -222,9 +279,15 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
           const int i = j / TB, t = j % TB;
           if (t == 0) {
             wv = operand(wf[i & 1]);
-            if (i < 7) wf[(i + 1) & 1] = frag(sw, ww * 128 + (i + 1) * 16 + lr);
+            if (i < FW - 1) {
+              wf[(i + 1) & 1] = frag(sw, (ww * FW + i + 1) * 16 + lr);
+            } else {   // after the last step: a barrier, and reads of no use
+              next_stage(kt + 1);
+              if (PREC == 0) first_weights(kt + 1);
+            }
           }
           p[j % (kLag + 1)] = product(wv, xt[t]);
+          if (PREC == 0 && i == FW - 1) row_fragment(kt + 1, t);
         }
         if (j >= kLag) {
           const int d = j - kLag, i = d / TB, t = d % TB;
@@ -232,24 +295,34 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             acc[i][t][q] = fmaf(p[d % (kLag + 1)][q], sc, acc[i][t][q]);
+          // here, not behind the branches of next_stage
+          asm volatile("" : "+v"(acc[i][t]));
         }
+        // keeps this order: the scheduler would bring each sum back next to
+        // its product and fill the wait with no-ops
+        if (PREC == 0) __builtin_amdgcn_sched_barrier(0);
+      }
+      if (PREC != 0) {   // widened rows: no registers to spare
+        first_weights(kt + 1);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) row_fragment(kt + 1, t);
       }
     }
 
     // ---- epilogue
     if constexpr (MODE == 1) {
-      // h of 64 features a wave; a block's largest magnitude is the maximum
-      // over the lane's four groups, the four lane groups and both halves
+      // h of 128 / NW features a wave; a block's largest magnitude is the
+      // maximum over a lane's, the four lane groups' and the NW waves' values
       fence();
       __builtin_amdgcn_s_barrier();   // every wave is done with the stages
       fence();
-      uint32_t* mx = reinterpret_cast<uint32_t*>(smem);   // [2][kTT]
+      uint32_t* mx = reinterpret_cast<uint32_t*>(smem);   // [NW][kTT]
       uint32_t m[TB];
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         m[t] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2)
+        for (int i = 0; i < FW; i += 2)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float h = swiglu(acc[i][t][q], acc[i + 1][t][q], a.clamp);
@@ -265,12 +338,15 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
       for (int t = 0; t < TB; ++t) {
         const int r = (wt * TB + t) * 16 + lr;
         if (r >= rows) continue;
-        const F8Scale sc = f8_scale(max(mx[r], mx[kTT + r]));
+        uint32_t mm = mx[r];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) mm = max(mm, mx[w * kTT + r]);
+        const F8Scale sc = f8_scale(mm);
         const size_t pr = (size_t)(row0 + r);
         if (ww == 0 && lq == 0) a.out_s[pr * (N / 128) + nb] = sc.s;
-        uint8_t* dst = static_cast<uint8_t*>(a.out) + pr * N + n0 + ww * 64 + lq * 4;
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + pr * N + n0 + ww * FW * 8 + lq * 4;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int i = 0; i < FW; i += 2) {
           int w = 0;
           w = __builtin_amdgcn_cvt_pk_fp8_f32(acc[i][t][0] * sc.inv, acc[i][t][1] * sc.inv, w, false);
           w = __builtin_amdgcn_cvt_pk_fp8_f32(acc[i][t][2] * sc.inv, acc[i][t][3] * sc.inv, w, true);
@@ -284,8 +360,8 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
         const int r = (wt * TB + t) * 16 + lr;
         if (r >= rows) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int n = n0 + ww * 128 + i * 16 + lq * 4;
+        for (int i = 0; i < FW; ++i) {
+          const int n = n0 + (ww * FW + i) * 16 + lq * 4;
           const size_t at = (size_t)(row0 + r) * N + n;
           const float v[4] = {acc[i][t][0], acc[i][t][1], acc[i][t][2], acc[i][t][3]};
           if (vec) {
@@ -299,16 +375,19 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
       }
     }
   };
-  if (rows > 128) run(std::integral_constant<int, 4>{});
-  else if (rows > 64) run(std::integral_constant<int, 2>{});
-  else run(std::integral_constant<int, 1>{});
+  if (rows > 128) run(std::integral_constant<int, 2>{});
+  else if (rows > 64) run(std::integral_constant<int, 4>{});
+  else run(std::integral_constant<int, 8>{});
 }
 
 hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s) {
-  const int64_t tiles = a.mode == 0 ? (a.M + kTT - 1) / kTT : a.max_groups;
-  const int64_t items = tiles * (a.mode == 1 ? a.N / 128 : (a.N + kTW - 1) / kTW);
-  if (items == 0) return hipSuccess;
-  const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(512);
+  const int64_t tiles = a.mode == 0 ? a.tiles256 + a.tail_tiles : a.max_groups;
+  const int64_t nnb = a.mode == 1 ? a.N / 128 : (a.N + kTW - 1) / kTW;
+  if (tiles * nnb == 0) return hipSuccess;
+  const int64_t blocks = a.mode == 0
+      ? (a.tiles256 * nnb + 7) / 8 * 8 + (a.tail_tiles * nnb + 7) / 8 * 8
+      : (tiles + 7) / 8 * 8 * nnb;
+  const dim3 grid((unsigned)blocks), block(512);
   if (prec) {
     if (a.mode == 0) hipLaunchKernelGGL((f8_tile_kernel<0, 1>), grid, block, 0, s, a);
     else if (a.mode == 1) hipLaunchKernelGGL((f8_tile_kernel<1, 1>), grid, block, 0, s, a);

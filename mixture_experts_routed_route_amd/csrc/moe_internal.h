@@ -323,7 +323,9 @@ struct F8Args {
   int mode;                 // 0: plain, rows 0 .. M; 1: gate/up with SwiGLU
                             // over a plan's pairs, x's rows gathered; 2: down
                             // over a plan's pairs, rows in pair order
-  int64_t M;                // mode 0: rows
+  int64_t M;                // mode 0: rows; on the tile split into
+  int tiles256;             // ... this many tiles of 256 rows, then
+  int tail_tiles, tail_rows;// tiles of tail_rows (128 or 64)
   int K, N;                 // reduction; output width (gate/up: features)
   const uint8_t* A;         // [rows, K]
   const float* As;          // [rows, ceil(K / 128)]
