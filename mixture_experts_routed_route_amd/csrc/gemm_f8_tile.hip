@@ -260,11 +260,6 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
     for (int kt = 0; kt < nk; ++kt) {
       const char* sw = smem + (kt & 1) * kStageB;
       const float w0 = lane_of(wl0, kt & 63), w1 = MODE == 1 ? lane_of(wl1, kt & 63) : w0;
-#pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        s0[t] = sr[t] * w0;
-        s1[t] = MODE == 1 ? sr[t] * w1 : s0[t];
-      }
       // Block sums go to the accumulators kLag products later, so that a
       // wave's matrix instructions do not wait for one another's results.
       // The stages change hands before the last weight fragment's products,
@@ -288,6 +283,13 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
           }
           p[j % (kLag + 1)] = product(wv, xt[t]);
           if (PREC == 0 && i == FW - 1) row_fragment(kt + 1, t);
+        }
+        // the step's scales, one by one before the first sums that take them
+        // (all at once would wait for the last row's reads)
+        if (j >= kLag - 1 && j < kLag - 1 + TB) {
+          const int t = j - (kLag - 1);
+          s0[t] = sr[t] * w0;
+          s1[t] = MODE == 1 ? sr[t] * w1 : s0[t];
         }
         if (j >= kLag) {
           const int d = j - kLag, i = d / TB, t = d % TB;
