@@ -420,9 +420,6 @@ moe_status moe_quant_f8_weights(const void *w, int32_t dtype, int64_t mats,
                                 int32_t N, int32_t K, void *q, float *scales,
                                 void *stream);
 
-/* Bytes of device workspace moe_gemm_f8 needs; 0 on invalid sizes. */
-size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K);
-
 /* out[M, N] = x[M, K] . w[N, K]^T on MOE_F8B128 rows and weights: the codes'
  * products of each block of 128 summed by the matrix units, scaled by
  * x_scales * w_scales and added in f32, rounded once to out_dtype (F32, BF16
@@ -431,12 +428,10 @@ size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K);
  * largest among them, bits below 2^-13 of its exponent dropped (the 8-bit
  * matrix unit's sum; about 1.5e-5 of the output). K a multiple of 16 up to
  * 2^22; M below 2^31, M and N any other size (0
- * writes nothing). Pointers 16-byte aligned, ws 256-byte aligned. Async on
- * `stream`. */
+ * writes nothing). Pointers 16-byte aligned. Async on `stream`. */
 moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,
                        const float *w_scales, int64_t M, int32_t N, int32_t K,
-                       void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
-                       void *stream);
+                       void *out, int32_t out_dtype, void *stream);
 
 /* --- norms around a block -------------------------------------------------- */
 

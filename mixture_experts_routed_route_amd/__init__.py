@@ -32,6 +32,7 @@ projections on 8-bit weights that read their output:
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -81,7 +82,7 @@ EXPORTED = (
     "moe_route_workspace_bytes", "moe_route", "moe_dequant_weights",
     "moe_backward_workspace_bytes", "moe_backward", "moe_forward_get_views",
     "moe_forward_noalloc", "moe_quant_f8", "moe_quant_f8_weights",
-    "moe_gemm_f8_workspace_bytes", "moe_gemm_f8", "moe_norm_forward",
+    "moe_gemm_f8", "moe_norm_forward",
     "moe_norm_backward_workspace_bytes", "moe_norm_backward",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -208,9 +209,7 @@ def library(path: str = LIB_PATH):
     L.moe_quant_f8.restype = i32
     L.moe_quant_f8_weights.argtypes = f8 + [i32, vp, vp, vp]
     L.moe_quant_f8_weights.restype = i32
-    L.moe_gemm_f8_workspace_bytes.argtypes = [i64, i32, i32]
-    L.moe_gemm_f8_workspace_bytes.restype = sz
-    L.moe_gemm_f8.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, sz, vp]
+    L.moe_gemm_f8.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp]
     L.moe_gemm_f8.restype = i32
     L.moe_norm_forward.argtypes = [ctypes.POINTER(NormDesc)] + [vp] * 9
     L.moe_norm_forward.restype = i32
@@ -240,7 +239,11 @@ def _check(status: int):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream's handle (what torch.cuda.current_stream(device)
+    .cuda_stream gives, without the two objects: 0.1 us, not 1.9)."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def moe_options_default() -> Options:
@@ -721,11 +724,16 @@ def moe_dequant_weights(data: torch.Tensor, params: torch.Tensor) -> torch.Tenso
     return out
 
 
+_NO_GUARD = contextlib.nullcontext()
+
+
 def _on(device):
     """A guard that makes the tensors' device the current one: the library
     launches there. The calls that have one may be made from any device."""
     if device.type != "cuda":
         raise ValueError("tensors must be on a GPU")
+    if torch._C._cuda_getDevice() == device.index:
+        return _NO_GUARD
     return torch.cuda.device(device)
 
 
@@ -740,8 +748,8 @@ def moe_quant_f8(x: torch.Tensor) -> tuple:
         raise ValueError(f"K={K} must be a positive multiple of 8")
     with _on(x.device):
         x = x.contiguous()
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty(*x.shape[:-1], _blocks(K), dtype=torch.float32, device=x.device)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        s = x.new_empty((*x.shape[:-1], _blocks(K)), dtype=torch.float32)
         _check(library().moe_quant_f8(x.data_ptr(), _TORCH_TO_MOE[x.dtype],
                                       x.numel() // K, K, q.data_ptr(),
                                       s.data_ptr(), _stream(x.device)))
@@ -762,9 +770,8 @@ def moe_quant_f8_weights(w: torch.Tensor) -> tuple:
         mats *= n
     with _on(w.device):
         w = w.contiguous()
-        q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
-        s = torch.empty(*w.shape[:-2], _blocks(N), _blocks(K), dtype=torch.float32,
-                        device=w.device)
+        q = torch.empty_like(w, dtype=torch.float8_e4m3fn)
+        s = w.new_empty((*w.shape[:-2], _blocks(N), _blocks(K)), dtype=torch.float32)
         _check(library().moe_quant_f8_weights(w.data_ptr(), _TORCH_TO_MOE[w.dtype],
                                               mats, N, K, q.data_ptr(), s.data_ptr(),
                                               _stream(w.device)))
@@ -772,8 +779,7 @@ def moe_quant_f8_weights(w: torch.Tensor) -> tuple:
 
 
 def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
-                out: torch.Tensor | None = None,
-                workspace: torch.Tensor | None = None) -> torch.Tensor:
+                out: torch.Tensor | None = None) -> torch.Tensor:
     """out [.., N] = x . w^T of 8-bit rows x = (codes [.., K], scales [..,
     ceil(K / 128)]) and weights w = (codes [N, K], scales [ceil(N / 128),
     ceil(K / 128)]), as moe_quant_f8 and moe_quant_f8_weights give them; K a
@@ -783,37 +789,31 @@ def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
     f8 = torch.float8_e4m3fn
     if xq.dtype != f8 or wq.dtype != f8 or xs.dtype != torch.float32 or ws.dtype != torch.float32:
         raise ValueError("x and w are (float8_e4m3fn codes, float32 scales)")
-    if xq.dim() < 1 or wq.dim() != 2 or xq.shape[-1] != wq.shape[1]:
+    if xq.dim() < 1 or xs.dim() < 1 or wq.dim() != 2 or xq.shape[-1] != wq.shape[1]:
         raise ValueError(f"codes {tuple(xq.shape)} and {tuple(wq.shape)} must be "
                          "[.., K] and [N, K]")
     N, K = wq.shape
     if K < 16 or K % 16:
         raise ValueError(f"K={K} must be a positive multiple of 16")
-    if tuple(xs.shape) != (*xq.shape[:-1], _blocks(K)) \
-            or tuple(ws.shape) != (_blocks(N), _blocks(K)):
+    if xs.shape[:-1] != xq.shape[:-1] or xs.shape[-1] != _blocks(K) \
+            or ws.shape != (_blocks(N), _blocks(K)):
         raise ValueError(f"scales {tuple(xs.shape)} and {tuple(ws.shape)} do not match "
                          f"codes {tuple(xq.shape)} and {tuple(wq.shape)}")
-    if any(t.device != xq.device for t in (xs, wq, ws)):
+    dev = xq.device
+    if xs.device != dev or wq.device != dev or ws.device != dev:
         raise ValueError("x, w and their scales must be on one device")
-    L = library()
-    shape = (*xq.shape[:-1], N)
-    M = xq.numel() // K
-    with _on(xq.device):
+    shape = xq.shape[:-1] + (N,)
+    with _on(dev):
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=xq.device)
-        if out.dtype not in _TORCH_TO_MOE or tuple(out.shape) != shape \
-                or not out.is_contiguous() or out.device != xq.device:
+            out = torch.empty(shape, dtype=out_dtype, device=dev)
+        if out.dtype not in _TORCH_TO_MOE or out.shape != shape \
+                or not out.is_contiguous() or out.device != dev:
             raise ValueError(f"out must be a contiguous float32/bfloat16/float16 "
-                             f"{shape} tensor on x's device")
-        nbytes = L.moe_gemm_f8_workspace_bytes(M, N, K)
-        if nbytes == 0:
-            raise MoeError(MOE_EINVAL, moe_last_error())
-        if workspace is None or workspace.numel() < nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=xq.device)
-        xq, xs, wq, ws = (t.contiguous() for t in (xq, xs, wq, ws))
-        _check(L.moe_gemm_f8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-                             M, N, K, out.data_ptr(), _TORCH_TO_MOE[out.dtype],
-                             workspace.data_ptr(), nbytes, _stream(xq.device)))
+                             f"{tuple(shape)} tensor on x's device")
+        xq, xs, wq, ws = xq.contiguous(), xs.contiguous(), wq.contiguous(), ws.contiguous()
+        _check(library().moe_gemm_f8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(),
+                                     ws.data_ptr(), xq.numel() // K, N, K, out.data_ptr(),
+                                     _TORCH_TO_MOE[out.dtype], _stream(dev)))
     return out
 
 
@@ -894,10 +894,9 @@ def moe_norm(residual: torch.Tensor, block: torch.Tensor | None = None,
         out = residual if block is None else torch.empty_like(residual)
         x = s = None
         if weight is not None:
-            x = torch.empty(residual.shape, dtype=x_dtype, device=residual.device)
+            x = torch.empty_like(residual, dtype=x_dtype)
             if f8:
-                s = torch.empty(d.T, _blocks(d.D), dtype=torch.float32,
-                                device=residual.device)
+                s = residual.new_empty((d.T, _blocks(d.D)), dtype=torch.float32)
         _check(library().moe_norm_forward(
             ctypes.byref(d), residual.data_ptr(), _ptr(block), _ptr(post_weight),
             _ptr(gate), _ptr(weight), out.data_ptr(), _ptr(x), _ptr(s),

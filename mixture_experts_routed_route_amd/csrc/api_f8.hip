@@ -26,10 +26,9 @@ moe_status launched(hipError_t e, const char* where) {
 // 256 rows of codes stay below 2 GiB
 constexpr int kF8MaxK = 1 << 22;
 
-// The layer's workspace: quantised x, the SwiGLU outputs in f32 and
-// quantised, the pairs' unweighted outputs, the work lists.
+// The layer's workspace: quantised x, the SwiGLU outputs, the pairs' unweighted outputs, the work lists.
 struct F8Layout {
-  size_t x8, xs, h, h8, hs, y, full_tiles, sk1, sk4, fat_slot, fat_list, meta, bytes;
+  size_t x8, xs, h8, hs, y, full_tiles, sk1, sk4, fat_slot, fat_list, meta, bytes;
   int cap_tiles, cap_sk1, cap_sk4;
 };
 
@@ -44,8 +43,8 @@ F8Layout f8_layout(const moe_plan_desc& d, int D, int F, int xdt) {
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   L.x8 = take((size_t)d.T * D);
   L.xs = take((size_t)d.T * (D / 128) * 4);
-  L.h = take(P * F * 4);
-  L.h8 = take(P * F);
+  // codes, or a decode-shaped call's f32 values
+  L.h8 = take(P * F * (d.T <= kDecodeT ? 4 : 1));
   L.hs = take(P * (F / 128) * 4);
   L.y = take(P * D * (xdt == MOE_F16 ? 2 : 4));
   L.full_tiles = take((size_t)L.cap_tiles * 8);
@@ -64,16 +63,20 @@ size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt) {
   return f8_layout(d, D, F, xdt).bytes;
 }
 
-// 0 quantise x, 1 classify, 2 / 3 gate/up of groups of <= 16 / 17..64 rows,
-// 4 gate/up tile, 5 quantise the groups' h, 6 / 7 down of the groups, 8 down
-// tile, 9 combine
+// A plan's experts of more rows than this take the tile: its 64-row tiles
+// read 256 weight rows once for all rows, where a stream of thin groups reads
+// them again for every 16 rows.
+constexpr int kF8StreamRows = 16;
+// ... unless the plan holds few pairs an expert: then the tiles would leave
+// most compute units idle, and their launches are saved.
+constexpr int kF8StreamT = 256, kF8StreamPairs = 32;
+
+// 0 quantise x, 1 classify, 2 gate/up of thin groups, 3 gate/up tile, 4 down
+// of thin groups, 5 down tile, 6 combine
 int moe::f8_step_phase(int step) {
-  static const int ph[kF8Steps] = {1, 0, 3, 14, 2, 1, 5, 15, 4, 6};
+  static const int ph[kF8Steps] = {1, 0, 3, 2, 5, 4, 6};
   return ph[step];
 }
-
-// Experts of more rows than this take the tile.
-constexpr int kF8ThinRows = 64;
 
 hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s) {
   const moe_plan_desc& d = p.desc;
@@ -81,40 +84,43 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   char* b = l.ws;
   const int64_t P = (int64_t)d.T * d.k + (int64_t)d.n_shared * d.T;
   const int n_exp = d.E + d.n_shared;
-  const bool decode = p.decode;
+  // decode-shaped calls: the plan's own groups, and the strips quantise x and
+  // h themselves
+  const bool raw = p.decode && f8_strip_raw_fits(d.T, std::max(l.D, l.F));
+  const bool tiles = d.T > kF8StreamRows &&
+      (d.T > kF8StreamT || P > (int64_t)kF8StreamPairs * n_exp);
+  const bool down = step >= 4;
   F8Args g{};
-  g.pair_token = p.pair_token;
-  g.offsets = p.offsets;
-  g.meta = decode ? p.dmeta : (const int32_t*)(b + L.meta);
-  g.clamp = l.o.swiglu_limit;
-  const bool down = step >= 6;
   g.mode = down ? 2 : 1;
   g.K = down ? l.F : l.D;
   g.N = down ? l.D : l.F;
-  g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
-  g.As = (const float*)(b + (down ? L.hs : L.xs));
   g.B0 = (const uint8_t*)(down ? l.wd : l.wg);
   g.B0s = down ? l.wds : l.wgs;
   g.B1 = (const uint8_t*)l.wu;
   g.B1s = l.wus;
+  g.pair_token = p.pair_token;
+  g.offsets = p.offsets;
+  g.clamp = l.o.swiglu_limit;
   g.odt = l.xdt == MOE_F16 ? MOE_F16 : MOE_F32;
-  const int32_t* sk1 = decode ? p.dlist : (const int32_t*)(b + L.sk1);
-  const int32_t* sk4 = (const int32_t*)(b + L.sk4);
-  // an expert holds at most T pairs
-  const bool some4 = !decode && d.T > 16, some_tile = !decode && d.T > kF8ThinRows;
-  const int groups1 = (int)std::min<int64_t>(n_exp, P);
+  g.meta = raw ? p.dmeta : (const int32_t*)(b + L.meta);
+  g.adt = MOE_F8B128;
+  g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
+  g.As = (const float*)(b + (down ? L.hs : L.xs));
+  g.out = b + (down ? L.y : L.h8);
+  g.out_s = (float*)(b + L.hs);
   switch (step) {
     case 0:
+      if (raw) return hipSuccess;
       return launch_quant_rows(l.x, l.xdt, d.T, l.D, b + L.x8, (float*)(b + L.xs), s);
     case 1: {
-      if (decode) return hipSuccess;
+      if (raw) return hipSuccess;
       ClassifyArgs ca{};
       ca.counts = p.counts;
       ca.n_exp = n_exp;
       ca.mode = 1;
-      ca.S = kF8ThinRows;
+      ca.S = tiles ? kF8StreamRows : 1e30;
       // too few tiles for one round of the compute units: experts of up to
-      // 256 rows go to the strips, 64 rows a group
+      // 256 rows join the thin groups
       ca.full_nnb = l.F / 128;
       ca.full_fill = l.ncu;
       ca.full_tiles = (int32_t*)(b + L.full_tiles);
@@ -127,38 +133,38 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       ca.meta = (int32_t*)(b + L.meta);
       return launch_classify(ca, s);
     }
-    case 2: case 3: case 6: case 7: {
-      const bool wide = step == 3 || step == 7;
-      if (wide && !some4) return hipSuccess;
-      g.out = b + (down ? L.y : L.h);
-      g.list = wide ? sk4 : sk1;
-      g.meta_index = wide ? kMetaSk4 : kMetaSk1;
-      g.max_groups = wide ? L.cap_sk4 : groups1;
-      return launch_f8_strip(g, wide ? 4 : 1, l.ncu, s);
-    }
-    case 4: case 8:
-      if (!some_tile) return hipSuccess;
-      g.out = b + (down ? L.y : L.h8);
-      g.out_s = (float*)(b + L.hs);
+    case 2: case 4:
+      if (raw) {
+        g.A = (const uint8_t*)(down ? b + L.h8 : l.x);
+        g.adt = down ? MOE_F32 : l.xdt;
+        g.lds_rows = d.T;
+        g.list = p.dlist;
+        g.meta_index = kMetaSk1;
+        g.max_groups = (int)std::min<int64_t>(n_exp, P);
+        return launch_f8_strip(g, l.ncu, s);
+      }
+      g.list = (const int32_t*)(b + L.sk1);
+      g.list4 = (const int32_t*)(b + L.sk4);
+      {
+        // parts of 16 rows: one group of <= 16 rows an expert, and of the
+        // others at least 17 rows for each four parts; beside tiles only the
+        // experts of fewer than ncu tiles x columns, sixteen parts each
+        int64_t parts = P / 4;
+        if (tiles) parts = std::min<int64_t>(parts, 16 * (l.ncu / (l.F / 128) + 1));
+        g.max_groups = (int)std::min<int64_t>(P, n_exp + parts);
+      }
+      return launch_f8_stream(g, s);
+    case 3: case 5:
+      if (!tiles) return hipSuccess;
       g.list = (const int32_t*)(b + L.full_tiles);
       g.meta_index = kMetaFullTiles;
       g.max_groups = L.cap_tiles;
       // an f16 layer's gate/up sums stay exact: a code of h that moves by a
       // step weighs more than f16's rounding of y
       return launch_f8_tile(g, !down && l.xdt == MOE_F16, s);
-    case 5: {
-      const float* h = (const float*)(b + L.h);
-      hipError_t e = launch_quant_groups(h, l.F, b + L.h8, (float*)(b + L.hs), sk1,
-                                         g.meta + kMetaSk1, groups1, 16, s);
-      if (e != hipSuccess || !some4) return e;
-      return launch_quant_groups(h, l.F, b + L.h8, (float*)(b + L.hs), sk4,
-                                 g.meta + kMetaSk4, L.cap_sk4, 64, s);
-    }
-    case 9:
+    default:
       return launch_combine(b + L.y, l.xdt == MOE_F16, p.tok2pair, p.w, p.offsets, d.T,
                             l.D, d.k, d.n_shared, d.E, l.ydt, l.y, s);
-    default:
-      return hipSuccess;
   }
 }
 
@@ -171,7 +177,7 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
 // a last round that few tiles share: 13312 x 4096 x 4096 takes 3 rounds and
 // a tail, not 4.
 static bool f8_split(F8Args* g, bool f32, int ncu) {
-  if (g->M <= kF8ThinRows) return false;
+  if (g->M <= 64) return false;
   const double c256 = f32 ? 4.1 : 2.1, c128 = f32 ? 1.95 : 1.5, c64 = f32 ? 1.25 : 0.87;
   const int64_t nnb = (g->N + 255) / 256, nk = (g->K + 127) / 128;
   auto rounds = [&](int64_t tiles) { return (double)((tiles * nnb + ncu - 1) / ncu); };
@@ -236,32 +242,20 @@ moe_status moe_quant_f8_weights(const void* w, int32_t dtype, int64_t mats,
                   "weight quantiser");
 }
 
-size_t moe_gemm_f8_workspace_bytes(int64_t M, int32_t N, int32_t K) {
-  if (M < 0 || N < 0 || K < 16 || K % 16 || K > kF8MaxK) {
-    set_error(MOE_EINVAL, "M and N must be >= 0 and K=%d a multiple of 16 in 16..%d", K, kF8MaxK);
-    return 0;
-  }
-  return 256;
-}
-
 moe_status moe_gemm_f8(const void* x, const float* x_scales, const void* w,
                        const float* w_scales, int64_t M, int32_t N, int32_t K,
-                       void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
-                       void* stream) {
+                       void* out, int32_t out_dtype, void* stream) {
   if (!plain_type(out_dtype))
     return set_error(MOE_EUNSUPPORTED, "output dtype %d: f32, bf16 or f16 only", out_dtype);
-  const size_t need = moe_gemm_f8_workspace_bytes(M, N, K);
-  if (need == 0) return MOE_EINVAL;
+  if (M < 0 || N < 0 || K < 16 || K % 16 || K > kF8MaxK)
+    return set_error(MOE_EINVAL, "M and N must be >= 0 and K=%d a multiple of 16 in 16..%d",
+                     K, kF8MaxK);
   const bool any = M > 0 && N > 0;
   if (any && (!x || !x_scales || !w || !w_scales || !out))
     return set_error(MOE_EINVAL, "x, w, their scales and out must be non-NULL");
   if (!aligned16(x) || !aligned16(x_scales) || !aligned16(w) || !aligned16(w_scales) ||
       !aligned16(out))
     return set_error(MOE_EINVAL, "pointers must be 16-byte aligned");
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
-    return set_error(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
-  if (ws_bytes < need)
-    return set_error(MOE_EWORKSPACE, "product workspace %zu bytes < %zu needed", ws_bytes, need);
   if (M > (int64_t)INT32_MAX)
     return set_error(MOE_EUNSUPPORTED, "M=%lld must be below 2^31", (long long)M);
   if (!any) return MOE_OK;
@@ -269,14 +263,14 @@ moe_status moe_gemm_f8(const void* x, const float* x_scales, const void* w,
   const moe_status st = current_cus(&ncu);
   if (st != MOE_OK) return st;
   F8Args g{};
-  g.M = M; g.N = N; g.K = K;
+  g.M = M; g.N = N; g.K = K; g.adt = MOE_F8B128;
   g.A = (const uint8_t*)x; g.As = x_scales;
   g.B0 = (const uint8_t*)w; g.B0s = w_scales;
   g.out = out; g.odt = out_dtype;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool f32 = out_dtype == MOE_F32;
   if (f8_split(&g, f32, ncu)) return launched(launch_f8_tile(g, f32, s), "8-bit product");
-  return launched(launch_f8_strip(g, M <= 16 ? 1 : 4, ncu, s), "8-bit product");
+  return launched(launch_f8_strip(g, ncu, s), "8-bit product");
 }
 
 // ---- norms --------------------------------------------------------------------

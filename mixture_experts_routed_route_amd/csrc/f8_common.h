@@ -38,12 +38,20 @@ __device__ __forceinline__ floatx4 block_product(const Codes& a, const Codes& b)
   return p;
 }
 
-// 32 codes of a row from k: two 16-byte pieces, zeros past the row's end (a
-// row ends on a piece, K being a multiple of 16).
-__device__ __forceinline__ v8i32 load_codes(const uint8_t* row, int k, int K) {
+// A lane group's 32 codes of a block of a row: 16-byte pieces q and q + 4, so
+// that the four groups read 64 neighbouring bytes at once. `row` points at
+// piece q of the row's first block, k is the block's start; pieces past the
+// row's end (a row ends on a piece, K being a multiple of 16) are zeros.
+__device__ __forceinline__ v8i32 load_codes(const uint8_t* row, int q, int k, int K) {
   uint4 lo = {0u, 0u, 0u, 0u}, hi = lo;
-  if (k < K) lo = ldg16(row + k);
-  if (k + 16 < K) hi = ldg16(row + k + 16);
+  if (k + q * 16 < K) lo = ldg16(row + k);
+  if (k + q * 16 + 64 < K) hi = ldg16(row + k + 64);
+  return v8i32{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
+               (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+// the same within a whole block
+__device__ __forceinline__ v8i32 load_codes(const uint8_t* at) {
+  const uint4 lo = ldg16(at), hi = ldg16(at + 64);
   return v8i32{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }

@@ -19,25 +19,42 @@
 
 namespace moe {
 
-// Strips: a workgroup of four waves takes 16 weight rows (gate/up: 16 of
-// each matrix) against up to 16 RB rows of one group, each wave every
-// fourth block of K, operands straight from memory to registers (each
-// weight code is used by one wave only); the four partial sums meet in LDS.
-template <int MODE, int RB>
+// Strips: a wave takes 16 weight rows (gate/up: 16 of each matrix) against
+// up to 16 RB rows of one group, weight operands straight from memory to
+// registers (each weight code is used by one wave only; four blocks of K of
+// loads in flight a wave). A workgroup of four waves takes 4 / ks strips, ks
+// waves sharing one's blocks of K, their partial sums meeting in LDS: ks = 4
+// from 16 blocks on, 2 from 8, else 1, so that a wave streams at least four
+// blocks and short rows do not leave workgroups of a few KB.
+//
+// SRC 0 (plain products) reads quantised rows. SRC 1 (decode-shaped plans)
+// reads the rows as they are (x in its type, or h in f32) and quantises the
+// group's into LDS first, every workgroup for itself: for so few rows this
+// costs less than a launch that quantises them once.
+constexpr int kStripLds = 32768;   // bytes of rows a workgroup may hold (SRC 1)
+
+template <int MODE, int RB, int SRC>
 __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
   constexpr int WF = MODE == 1 ? 2 : 1;
+  constexpr int U = 1;
   __shared__ float part[3][WF][RB][256];
+  extern __shared__ __attribute__((aligned(16))) char rows_lds[];   // SRC 1
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lr = lane & 15, kq = (lane >> 4) * 32;
+  const int lr = lane & 15, lq = lane >> 4;
   const int K = a.K, N = a.N;
   const int nkb = (K + 127) / 128, nnb = (N + 127) / 128;
+  const int ks = nkb >= 16 ? 4 : nkb >= 8 ? 2 : 1, spw = 4 / ks;
+  const int kw = wave & (ks - 1);          // this wave's share of K
   const int strips = (N + 15) / 16;
+  const int sblocks = (strips + spw - 1) / spw;
   const int64_t groups = MODE == 0 ? (a.M + 16 * RB - 1) / (16 * RB) : a.meta[a.meta_index];
-  const int64_t items = groups * strips;
+  const int64_t items = groups * sblocks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t gi = it / strips;
-    const int n0 = (int)(it - gi * strips) * 16;
+    const int64_t gi = it / sblocks;
+    // a strip past the last repeats it and stores nothing
+    const int strip = (int)(it - gi * sblocks) * spw + wave / ks;
+    const int n0 = min(strip, strips - 1) * 16;
     int64_t row0;
     int rows, e = 0;
     if (MODE == 0) {
@@ -54,66 +71,105 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
     const float* ws[WF];
 #pragma unroll
     for (int f = 0; f < WF; ++f) {
-      w[f] = (f ? a.B1 : a.B0) + ((size_t)e * N + n) * K;
+      w[f] = (f ? a.B1 : a.B0) + ((size_t)e * N + n) * K + lq * 16;
       ws[f] = (f ? a.B1s : a.B0s) + ((size_t)e * nnb + (n0 >> 7)) * nkb;
     }
+    v8i32 wv[U][WF];
+    auto load_weights = [&](int kb0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int f = 0; f < WF; ++f) wv[u][f] = load_codes(w[f], lq, (kb0 + u * ks) * 128, K);
+    };
+    load_weights(kw);
     const uint8_t* x[RB];
     const float* xs[RB];
+    if constexpr (SRC == 0) {
 #pragma unroll
-    for (int t = 0; t < RB; ++t) {
-      int64_t r = row0 + min(16 * t + lr, rows - 1);
-      if (MODE == 1) r = a.pair_token[r];
-      x[t] = a.A + (size_t)r * K;
-      xs[t] = a.As + (size_t)r * nkb;
+      for (int t = 0; t < RB; ++t) {
+        int64_t r = row0 + min(16 * t + lr, rows - 1);
+        if (MODE == 1) r = a.pair_token[r];
+        x[t] = a.A + (size_t)r * K + lq * 16;
+        xs[t] = a.As + (size_t)r * nkb;
+      }
+    } else {
+      // 16 lanes a block; rows 16 bytes apart beyond their codes, so that a
+      // fragment's 16 rows lie on banks of their own
+      const int nb = K / 128;
+      float* const sl = reinterpret_cast<float*>(rows_lds + a.lds_rows * (K + 16));
+      for (int i = threadIdx.x >> 4; i < rows * nb; i += 16) {
+        const int r = i / nb, b = i - r * nb, k = b * 128 + (threadIdx.x & 15) * 8;
+        const int64_t src = MODE == 1 ? (int64_t)a.pair_token[row0 + r] : row0 + r;
+        float v[8];
+        raw8_to_f32(load_raw8(a.A, a.adt, (size_t)src * K + k), a.adt, v);
+        const F8Scale sc = f8_scale(max16(mag_max8(v)));
+        *reinterpret_cast<uint2*>(rows_lds + r * (K + 16) + k) = f8_pack8(v, sc.inv);
+        if ((threadIdx.x & 15) == 0) sl[r * nb + b] = sc.s;
+      }
+      __syncthreads();
+      x[0] = reinterpret_cast<const uint8_t*>(rows_lds) + min(lr, rows - 1) * (K + 16) + lq * 16;
+      xs[0] = sl + min(lr, rows - 1) * nb;
     }
     floatx4 acc[WF][RB];
 #pragma unroll
     for (int f = 0; f < WF; ++f)
 #pragma unroll
       for (int t = 0; t < RB; ++t) acc[f][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int kb = wave; kb < nkb; kb += 4) {
-      const int k = kb * 128 + kq;
-      v8i32 wv[WF], xv[RB];
+    for (int kb0 = kw; kb0 < nkb; kb0 += U * ks) {
+      if (kb0 != kw) load_weights(kb0);
+      v8i32 xv[U][RB];
+      float sx[U][RB], sw[U][WF];
 #pragma unroll
-      for (int f = 0; f < WF; ++f) wv[f] = load_codes(w[f], k, K);
+      for (int u = 0; u < U; ++u) {
+        const int kb = kb0 + u * ks, kc = min(kb, nkb - 1);
 #pragma unroll
-      for (int t = 0; t < RB; ++t) xv[t] = load_codes(x[t], k, K);
-      Codes wc[WF];
+        for (int t = 0; t < RB; ++t) {
+          xv[u][t] = load_codes(x[t], lq, kb * 128, K);
+          sx[u][t] = xs[t][kc];
+        }
 #pragma unroll
-      for (int f = 0; f < WF; ++f) wc[f] = widen(wv[f]);
+        for (int f = 0; f < WF; ++f) sw[u][f] = ws[f][kc];
+      }
 #pragma unroll
-      for (int t = 0; t < RB; ++t) {
-        const float sx = xs[t][kb];
-        const Codes xc = widen(xv[t]);
+      for (int u = 0; u < U; ++u) {
+        if (kb0 + u * ks >= nkb) break;   // uniform in the wave
+        Codes wc[WF];
 #pragma unroll
-        for (int f = 0; f < WF; ++f) {
-          const floatx4 p = block_product(wc[f], xc);
-          const float sc = sx * ws[f][kb];
+        for (int f = 0; f < WF; ++f) wc[f] = widen(wv[u][f]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[f][t][q] = fmaf(p[q], sc, acc[f][t][q]);
+        for (int t = 0; t < RB; ++t) {
+          const Codes xc = widen(xv[u][t]);
+#pragma unroll
+          for (int f = 0; f < WF; ++f) {
+            const floatx4 p = block_product(wc[f], xc);
+            const float sc = sx[u][t] * sw[u][f];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[f][t][q] = fmaf(p[q], sc, acc[f][t][q]);
+          }
         }
       }
     }
-    if (wave) {
-#pragma unroll
-      for (int f = 0; f < WF; ++f)
-#pragma unroll
-        for (int t = 0; t < RB; ++t)
-          *reinterpret_cast<floatx4*>(&part[wave - 1][f][t][lane * 4]) = acc[f][t];
-    }
-    __syncthreads();
-    if (!wave) {
-#pragma unroll
-      for (int t = 0; t < RB; ++t) {
+    if (ks > 1) {
+      if (kw) {
 #pragma unroll
         for (int f = 0; f < WF; ++f)
 #pragma unroll
-          for (int s = 0; s < 3; ++s)
-            acc[f][t] += *reinterpret_cast<floatx4*>(&part[s][f][t][lane * 4]);
+          for (int t = 0; t < RB; ++t)
+            *reinterpret_cast<floatx4*>(&part[wave - wave / ks - 1][f][t][lane * 4]) = acc[f][t];
+      }
+      __syncthreads();
+    }
+    if (!kw && strip < strips) {
+      const int p0 = wave - wave / ks;   // the first of the strip's ks - 1 parts
+#pragma unroll
+      for (int t = 0; t < RB; ++t) {
+        for (int s = 0; s < ks - 1; ++s)
+#pragma unroll
+          for (int f = 0; f < WF; ++f)
+            acc[f][t] += *reinterpret_cast<floatx4*>(&part[p0 + s][f][t][lane * 4]);
         const int r = 16 * t + lr;
         if (r >= rows) continue;
-        const int nc = n0 + (lane >> 4) * 4;
+        const int nc = n0 + lq * 4;
         float v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -128,24 +184,187 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
         }
       }
     }
-    __syncthreads();
+    __syncthreads();   // LDS is free for the next item
   }
 }
 
-hipError_t launch_f8_strip(const F8Args& a, int rb, int ncu, hipStream_t s) {
-  const int64_t groups = a.mode == 0 ? (a.M + 16 * rb - 1) / (16 * rb) : a.max_groups;
-  const int64_t items = groups * ((a.N + 15) / 16);
-  if (items == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>(items, (int64_t)ncu * 16)), block(256);
-  if (rb == 1) {
-    if (a.mode == 0) hipLaunchKernelGGL((f8_strip_kernel<0, 1>), grid, block, 0, s, a);
-    else if (a.mode == 1) hipLaunchKernelGGL((f8_strip_kernel<1, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((f8_strip_kernel<2, 1>), grid, block, 0, s, a);
-  } else {
-    if (a.mode == 0) hipLaunchKernelGGL((f8_strip_kernel<0, 4>), grid, block, 0, s, a);
-    else if (a.mode == 1) hipLaunchKernelGGL((f8_strip_kernel<1, 4>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((f8_strip_kernel<2, 4>), grid, block, 0, s, a);
+// Streams: the groups of a plan's thin experts (up to 16 rows at a time),
+// quantised rows. A workgroup of eight waves walks eight strips of 16 weight
+// rows (gate/up: 16 of each matrix, so a scale block of 128 features, which
+// it quantises itself; down: 128 columns), ks waves sharing a strip's blocks
+// of K, so that a workgroup's loads run through its weights in pieces of
+// whole rows: a wave that walked its rows alone, 128 bytes of 16 rows at a
+// time, got 3.8 TB/s from memory. The rows' fragments stay in registers over
+// all strips where K <= 128 ks NX.
+template <int MODE, int NX>
+__global__ __launch_bounds__(512, 4) void f8_stream_kernel(F8Args a, int ks) {
+  constexpr int WF = MODE == 1 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) float red[2][8][WF][256];
+  __shared__ uint32_t mx[8][16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int K = a.K, N = a.N, nkb = K / 128, nnb = N / 128;
+  // items: groups of 17..64 rows in four parts of 16, then those of <= 16
+  const int n4 = a.meta[kMetaSk4] * 4, n1 = a.meta[kMetaSk1];
+  const int gi = blockIdx.x / nnb, cb = blockIdx.x - gi * nnb;
+  if (gi >= n4 + n1) return;
+  const int32_t* g = gi < n4 ? a.list4 + 4 * (gi >> 2) : a.list + 4 * (gi - n4);
+  const int part = gi < n4 ? (gi & 3) * 16 : 0;
+  const int e = g[0], rows = min(16, g[2] - part), row0 = g[3] + part;
+  if (rows <= 0) return;   // the whole workgroup, before any barrier
+  const int kw = wave & (ks - 1), ws = wave / ks, sw = 8 / ks;
+  const int nch = (nkb + ks * NX - 1) / (ks * NX);   // chunks of K a strip
+  const int steps = ks * nch;                        // ks batches of sw strips
+
+  const size_t wbase = ((size_t)e * N + cb * 128 + lr) * K + lq * 16;
+  const uint8_t* w0 = a.B0 + wbase;
+  const uint8_t* w1 = MODE == 1 ? a.B1 + wbase : nullptr;
+  v8i32 w[NX][WF];
+  auto load_weights = [&](int st, int i) {
+    const int it = nch == 1 ? st : st / nch, ch = st - it * nch;
+    const int kb = min((ch * NX + i) * ks + kw, nkb - 1);
+    const size_t off = (size_t)((it * sw + ws) * 16) * K + kb * 128;
+    w[i][0] = load_codes(w0 + off);
+    if (MODE == 1) w[i][WF - 1] = load_codes(w1 + off);
+  };
+  int64_t xr = row0 + min(lr, rows - 1);
+#pragma unroll
+  for (int i = 0; i < NX; ++i) load_weights(0, i);
+  if (MODE == 1) xr = a.pair_token[xr];
+  const uint8_t* x = a.A + (size_t)xr * K + lq * 16;
+  const float* xs = a.As + (size_t)xr * nkb;
+  const float* s0 = a.B0s + ((size_t)e * nnb + cb) * nkb;
+  const float* s1 = MODE == 1 ? a.B1s + ((size_t)e * nnb + cb) * nkb : nullptr;
+  v8i32 xv[NX];
+  float sc[NX][WF];
+  auto load_rows = [&](int ch) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int kb = min((ch * NX + i) * ks + kw, nkb - 1);
+      xv[i] = load_codes(x + kb * 128);
+      const float sx = xs[kb];
+      sc[i][0] = sx * s0[kb];
+      if (MODE == 1) sc[i][WF - 1] = sx * s1[kb];
+    }
+  };
+  floatx4 acc[WF];
+  floatx4 mine[WF];   // the strip this wave finishes: strip `wave`
+  for (int st = 0; st < steps; ++st) {
+    const int it = nch == 1 ? st : st / nch, ch = st - it * nch;
+    if (nch > 1 || st == 0) load_rows(ch);
+    if (ch == 0) {
+#pragma unroll
+      for (int f = 0; f < WF; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const bool any = (ch * NX + i) * ks + kw < nkb;   // uniform in the wave
+      if (any) {
+        const Codes xc = widen(xv[i]);
+#pragma unroll
+        for (int f = 0; f < WF; ++f) {
+          const floatx4 p = block_product(widen(w[i][f]), xc);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[f][q] = fmaf(p[q], sc[i][f], acc[f][q]);
+        }
+      }
+      // the next step's weights into the registers just read: in flight over
+      // the sums below
+      if (st + 1 < steps) load_weights(st + 1, i);
+    }
+    if (ch < nch - 1) continue;
+    // the ks partial sums of each strip meet in the wave of the strip's
+    // number; a half of `red` is written again two barriers later
+    float (*const half)[WF][256] = red[it & 1];
+#pragma unroll
+    for (int f = 0; f < WF; ++f) *reinterpret_cast<floatx4*>(&half[wave][f][lane * 4]) = acc[f];
+    asm volatile("" ::: "memory");
+    wait_vm_lgkm0<63>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (wave / sw == it) {
+      const int p0 = (wave - it * sw) * ks;
+#pragma unroll
+      for (int f = 0; f < WF; ++f) {
+        mine[f] = *reinterpret_cast<const floatx4*>(&half[p0][f][lane * 4]);
+        for (int k = 1; k < ks; ++k)
+          mine[f] += *reinterpret_cast<const floatx4*>(&half[p0 + k][f][lane * 4]);
+      }
+    }
   }
+  const size_t row = (size_t)(row0 + lr);
+  const int n0 = cb * 128 + wave * 16 + lq * 4;
+  if constexpr (MODE == 1) {
+    float h[4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      h[q] = swiglu(mine[0][q], mine[WF - 1][q], a.clamp);
+      m = max(m, mag_bits(h[q]));
+    }
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if (lq == 0) mx[wave][lr] = m;
+    __syncthreads();
+    m = mx[0][lr];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) m = max(m, mx[w][lr]);
+    if (lr < rows) {
+      const F8Scale fs = f8_scale(m);
+      int o = 0;
+      o = __builtin_amdgcn_cvt_pk_fp8_f32(h[0] * fs.inv, h[1] * fs.inv, o, false);
+      o = __builtin_amdgcn_cvt_pk_fp8_f32(h[2] * fs.inv, h[3] * fs.inv, o, true);
+      *reinterpret_cast<int*>(static_cast<uint8_t*>(a.out) + row * N + n0) = o;
+      if (wave == 0 && lq == 0) a.out_s[row * nnb + cb] = fs.s;
+    }
+  } else if (lr < rows) {
+    const float v[4] = {mine[0][0], mine[0][1], mine[0][2], mine[0][3]};
+    store_out4(a.out, a.odt, row * N + n0, v);
+  }
+}
+
+template <int MODE, int NX>
+static void run_stream(const F8Args& a, int ks, unsigned grid, hipStream_t s) {
+  hipLaunchKernelGGL((f8_stream_kernel<MODE, NX>), dim3(grid), dim3(512), 0, s, a, ks);
+}
+
+hipError_t launch_f8_stream(const F8Args& a, hipStream_t s) {
+  const int64_t grid = (int64_t)a.max_groups * (a.N / 128);
+  if (grid == 0) return hipSuccess;
+  // the most waves a strip that leave each a block or more; two or three
+  // blocks a wave and chunk
+  const int nkb = a.K / 128;
+  int ks = 8;
+  while (ks > 1 && nkb < 2 * ks) ks >>= 1;
+  const bool three = (nkb + ks * 2 - 1) / (ks * 2) * 2 > (nkb + ks * 3 - 1) / (ks * 3) * 3 - 1;
+  if (a.mode == 1) run_stream<1, 2>(a, ks, (unsigned)grid, s);
+  else if (three) run_stream<2, 3>(a, ks, (unsigned)grid, s);
+  else run_stream<2, 2>(a, ks, (unsigned)grid, s);
+  return hipGetLastError();
+}
+
+static size_t strip_lds(int rows, int K) { return (size_t)rows * (K + 16 + K / 128 * 4); }
+
+bool f8_strip_raw_fits(int rows, int K) { return rows <= 16 && strip_lds(rows, K) <= kStripLds; }
+
+template <int MODE, int RB, int SRC>
+static void run_strip(const F8Args& a, unsigned grid, hipStream_t s) {
+  const size_t lds = SRC ? strip_lds(a.lds_rows, a.K) : 0;
+  hipLaunchKernelGGL((f8_strip_kernel<MODE, RB, SRC>), dim3(grid), dim3(256), lds, s, a);
+}
+
+hipError_t launch_f8_strip(const F8Args& a, int ncu, hipStream_t s) {
+  const int rb = a.mode == 0 && a.M > 16 ? 4 : 1;
+  const int64_t groups = a.mode == 0 ? (a.M + 16 * rb - 1) / (16 * rb) : a.max_groups;
+  const int nkb = (a.K + 127) / 128, spw = nkb >= 16 ? 1 : nkb >= 8 ? 2 : 4;
+  const int64_t items = groups * (((a.N + 15) / 16 + spw - 1) / spw);
+  if (items == 0) return hipSuccess;
+  const unsigned grid = (unsigned)std::min<int64_t>(items, (int64_t)ncu * 16);
+  if (a.mode == 0 && rb == 1) run_strip<0, 1, 0>(a, grid, s);
+  else if (a.mode == 0) run_strip<0, 4, 0>(a, grid, s);
+  else if (a.mode == 1) run_strip<1, 1, 1>(a, grid, s);
+  else run_strip<2, 1, 1>(a, grid, s);
   return hipGetLastError();
 }
 

@@ -310,13 +310,6 @@ hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
 hipError_t launch_quant_weights(const void* w, int dt, int64_t mats, int N,
                                 int K, void* q, float* s, hipStream_t st);
 
-// The rows of a plan's groups (expert, row0, rows, first pair), *n_groups of
-// them (at most max_groups, at most group_rows rows each): f32 rows of pairs
-// [P, F] to codes and scales.
-hipError_t launch_quant_groups(const float* h, int F, void* q, float* s,
-                               const int32_t* list, const int32_t* n_groups,
-                               int max_groups, int group_rows, hipStream_t st);
-
 // One product on e4m3 rows: out[row, n] = sum_b As[row, b] Bs[n / 128, b]
 // sum_{k in block b} A[row, k] B[n, k].
 struct F8Args {
@@ -327,21 +320,29 @@ struct F8Args {
   int tiles256;             // ... this many tiles of 256 rows, then
   int tail_tiles, tail_rows;// tiles of tail_rows (128 or 64)
   int K, N;                 // reduction; output width (gate/up: features)
-  const uint8_t* A;         // [rows, K]
+  const uint8_t* A;         // [rows, K] codes, or (strips over a plan, groups
+                            // of at most lds_rows rows) values of type adt
   const float* As;          // [rows, ceil(K / 128)]
+  int adt, lds_rows;        // adt MOE_F8B128: codes and scales
   const uint8_t* B0; const float* B0s;   // weights and their block scales
   const uint8_t* B1; const float* B1s;   // gate/up: W_up
   const int32_t* pair_token;
   const int32_t* offsets;   // [n_exp + 1]
   const int32_t* list;      // strip: (expert, row0, rows, first pair) groups
+  const int32_t* list4;     // stream: the groups of 17..64 rows (list: <= 16)
   const int32_t* meta; int meta_index;
   int max_groups;           // most groups the list can hold
   void* out; int odt;       // plain and down: [rows, N]; gate/up: strip f32
-                            // [P, N], tile codes [P, N] ...
+                            // [P, N], stream and tile codes [P, N] ...
   float* out_s;             // ... with scales [P, N / 128]
   float clamp;
 };
-hipError_t launch_f8_strip(const F8Args& a, int rb, int ncu, hipStream_t s);
+hipError_t launch_f8_strip(const F8Args& a, int ncu, hipStream_t s);
+// modes 1 and 2 over both lists of a plan's thin groups; max_groups counts
+// the groups of <= 16 rows and four parts for each of the others
+hipError_t launch_f8_stream(const F8Args& a, hipStream_t s);
+// whether strips may take groups of `rows` rows of K values unquantised
+bool f8_strip_raw_fits(int rows, int K);
 // list: (expert, row0) tiles of kFullBM rows, max_groups of them at most.
 // prec 0: codes in the 8-bit matrix unit; 1: widened to f16
 hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s);
@@ -367,7 +368,7 @@ struct F8Layer {
 };
 size_t f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt);
 // steps of the layer in order; `phase` is the index moe_phase_times reports
-constexpr int kF8Steps = 10;
+constexpr int kF8Steps = 7;
 int f8_step_phase(int step);
 hipError_t launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s);
 

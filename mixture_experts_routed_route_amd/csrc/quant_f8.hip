@@ -32,36 +32,6 @@ hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
   return hipGetLastError();
 }
 
-// Groups of pairs: the same on the rows of a plan's thin groups, a workgroup
-// a block column of 128 and 16 rows.
-__global__ __launch_bounds__(256) void quant_groups_kernel(
-    const float* __restrict__ h, int F, uint8_t* __restrict__ q, float* __restrict__ s,
-    const int32_t* __restrict__ list, const int32_t* __restrict__ n_groups, int g0) {
-  const int gi = g0 + blockIdx.y;
-  if (gi >= *n_groups) return;
-  const int r = blockIdx.z * 16 + (threadIdx.x >> 4);
-  if (r >= list[4 * gi + 2]) return;   // whole groups of 16 lanes
-  const size_t row = (size_t)(list[4 * gi + 3] + r);
-  const size_t at = row * F + blockIdx.x * 128 + (threadIdx.x & 15) * 8;
-  float v[8];
-  raw8_to_f32(load_raw8(h, MOE_F32, at), MOE_F32, v);
-  const F8Scale sc = f8_scale(max16(mag_max8(v)));
-  *reinterpret_cast<uint2*>(q + at) = f8_pack8(v, sc.inv);
-  if ((threadIdx.x & 15) == 0) s[row * (F / 128) + blockIdx.x] = sc.s;
-}
-
-hipError_t launch_quant_groups(const float* h, int F, void* q, float* s,
-                               const int32_t* list, const int32_t* n_groups,
-                               int max_groups, int group_rows, hipStream_t st) {
-  // a grid's second extent holds 65535 groups; a launch a piece
-  for (int g0 = 0; g0 < max_groups; g0 += 65535) {
-    const int n = max_groups - g0 < 65535 ? max_groups - g0 : 65535;
-    hipLaunchKernelGGL(quant_groups_kernel, dim3(F / 128, n, group_rows / 16), dim3(256), 0, st,
-                       h, F, (uint8_t*)q, s, list, n_groups, g0);
-  }
-  return hipGetLastError();
-}
-
 // Weights: a workgroup takes one 128 x 128 block, 16 rows a pass with 16
 // lanes a row, all of it in registers between the maximum and the codes.
 __global__ __launch_bounds__(256) void quant_weights_kernel(
