@@ -821,7 +821,15 @@ def _rows_like(t, like, name: str):
     if t.dtype not in _TORCH_TO_MOE or t.shape != like.shape or t.device != like.device:
         raise ValueError(f"{name} must be a float32/bfloat16/float16 tensor of shape "
                          f"{tuple(like.shape)} on the residual's device")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _norm_vec(v, D, like, dtype):
+    if v.dtype not in _TORCH_TO_MOE or (dtype is not None and v.dtype != dtype) \
+            or v.dim() != 1 or v.shape[0] != D or v.device != like.device:
+        raise ValueError(f"weight and post_weight must be [{D}] tensors of one "
+                         "type (float32/bfloat16/float16) on the residual's device")
+    return v if v.is_contiguous() else v.contiguous()
 
 
 def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
@@ -832,36 +840,39 @@ def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
     T, D = residual.shape
     if D < 8 or D % 8 or D > MOE_NORM_MAX_D:
         raise ValueError(f"D={D} must be a multiple of 8 in 8..{MOE_NORM_MAX_D}")
-    if block is None and (post_weight is not None or gate is not None):
-        raise ValueError("post_weight and gate need a block")
-    if block is None and weight is None:
-        raise ValueError("neither a block nor a weight: nothing to do")
-    residual = residual.contiguous()
-    if block is not None:
-        block = _rows_like(block, residual, "block")
-    vecs = [v for v in (weight, post_weight) if v is not None]
-    for v in vecs:
-        if v.dtype not in _TORCH_TO_MOE or v.dtype != vecs[0].dtype \
-                or tuple(v.shape) != (D,) or v.device != residual.device:
-            raise ValueError(f"weight and post_weight must be [{D}] tensors of one "
-                             "type (float32/bfloat16/float16) on the residual's device")
+    if not residual.is_contiguous():
+        residual = residual.contiguous()
+    udt = wdt = gdt = MOE_F32
     kind = MOE_GATE_NONE
+    if block is None:
+        if post_weight is not None or gate is not None:
+            raise ValueError("post_weight and gate need a block")
+        if weight is None:
+            raise ValueError("neither a block nor a weight: nothing to do")
+    else:
+        block = _rows_like(block, residual, "block")
+        udt = _TORCH_TO_MOE[block.dtype]
+    if weight is not None:
+        weight = _norm_vec(weight, D, residual, None)
+        wdt = _TORCH_TO_MOE[weight.dtype]
+    if post_weight is not None:
+        post_weight = _norm_vec(post_weight, D, residual,
+                                None if weight is None else weight.dtype)
+        wdt = _TORCH_TO_MOE[post_weight.dtype]
     if gate is not None:
-        if tuple(gate.shape) == (D,):
+        if gate.dim() == 1 and gate.shape[0] == D:
             kind = MOE_GATE_CHANNEL
-        elif tuple(gate.shape) == (T, 1):
+        elif gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] == 1:
             kind = MOE_GATE_TOKEN
         if kind == MOE_GATE_NONE or gate.dtype not in _TORCH_TO_MOE \
                 or gate.device != residual.device:
             raise ValueError(f"gate must be [{D}] (per channel) or [{T}, 1] (per token), "
                              "float32/bfloat16/float16, on the residual's device")
-        gate = gate.contiguous()
-    weight, post_weight = (None if v is None else v.contiguous()
-                           for v in (weight, post_weight))
-    code = lambda t: MOE_F32 if t is None else _TORCH_TO_MOE[t.dtype]  # noqa: E731
-    d = NormDesc(T, D, code(residual), code(block), x_dtype,
-                 _TORCH_TO_MOE[vecs[0].dtype] if vecs else MOE_F32, code(gate), kind,
-                 MOE_NORM_UNIT_OFFSET if unit_offset else 0, float(alpha), float(eps))
+        if not gate.is_contiguous():
+            gate = gate.contiguous()
+        gdt = _TORCH_TO_MOE[gate.dtype]
+    d = NormDesc(T, D, _TORCH_TO_MOE[residual.dtype], udt, x_dtype, wdt, gdt, kind,
+                 MOE_NORM_UNIT_OFFSET if unit_offset else 0, alpha, eps)
     return d, residual, block, weight, post_weight, gate
 
 
