@@ -25,6 +25,12 @@ template <int TPR> struct RowShape {
   static constexpr int kThreads = TPR * kRows;
 };
 
+__device__ __forceinline__ float load_one(const void* p, int dt, size_t i) {
+  if (dt == MOE_F32) return static_cast<const float*>(p)[i];
+  if (dt == MOE_BF16) return (float)static_cast<const __bf16*>(p)[i];
+  return (float)static_cast<const _Float16*>(p)[i];
+}
+
 __device__ __forceinline__ float param(float v, int unit) { return unit ? 1.f + v : v; }
 
 }  // namespace
@@ -77,11 +83,7 @@ __global__ __launch_bounds__(RowShape<TPR>::kThreads) void norm_forward_kernel(N
     }
     float gt = a.alpha;
     if (a.g && a.gate_token) {
-      float one;
-      if (a.gdt == MOE_F32) one = static_cast<const float*>(a.g)[row];
-      else if (a.gdt == MOE_BF16) one = (float)static_cast<const __bf16*>(a.g)[row];
-      else one = (float)static_cast<const _Float16*>(a.g)[row];
-      gt *= one;
+      gt *= load_one(a.g, a.gdt, row);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -144,7 +146,7 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
   if (a.D <= 512) return run_norm_forward<64, 1>(a, s);
   if (a.D <= 1024) return run_norm_forward<64, 2>(a, s);
   if (a.D <= 2048) return run_norm_forward<256, 1>(a, s);
-  if (a.D <= 4096) return run_norm_forward<256, 2>(a, s);
+  if (a.D <= 4096) return run_norm_forward<512, 1>(a, s);
   if (a.D <= 8192) return run_norm_forward<512, 2>(a, s);
   return run_norm_forward<1024, 2>(a, s);
 }
@@ -157,46 +159,88 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
 //   dz  = alpha g d,  dg += alpha d z
 // and with v = u inv_u, tp = dz p, mp = mean(tp v):
 //   du  = inv_u (tp - v mp),  dp += dz v      (without a post-norm du = dz)
-// The inverse norms are recomputed from r' and u, which are read anyway. A
-// workgroup walks rows gridDim.x apart and holds its partial sums of dw, dp
-// and a channel gate's dg in registers; it writes them once, [3][grid][D],
-// and a second launch adds the workgroups' partials in order (no atomics:
-// the same bits from run to run).
-template <int TPR, int NV>
-__global__ __launch_bounds__(RowShape<TPR>::kThreads) void norm_backward_kernel(NormBwdArgs a) {
-  __shared__ float sh[2][5 * 16];
+// d is linear in dr', t and r', so with a = alpha g p the second norm's sum
+// of a u d is s3 + inv (s4 - inv^2 s1 / D s5) of the sums of a u dr', a u t
+// and a u r': all six sums of a row are known after one pass and one barrier,
+// and everything behind it is elementwise. The inverse norms are recomputed
+// from r' and u, which are read anyway. A workgroup walks rows (R at a time),
+// the parameters in LDS, the next row's loads in flight, its partial sums of
+// dw, dp and a channel gate's dg in registers; it writes them once,
+// [3][grid][D], and a second launch adds the workgroups' partials in order
+// (no atomics: the same bits from run to run).
+// LP: the parameters in LDS; rows of more than 8192 values read them again
+// for every row.
+template <int TPR, int R, int NV, bool LP>
+__global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_backward_kernel(NormBwdArgs a) {
+  constexpr int W = TPR / 64;   // waves a row
+  extern __shared__ __attribute__((aligned(16))) float par[];   // [3][cols]: w, p, g
+  __shared__ float sh[2][R][6 * W];
+  __shared__ float fold[R > 1 ? (R - 1) * TPR * 8 : 1];
+  constexpr int cols = TPR * NV * 8;
   const int t = threadIdx.x % TPR;
   const int sub = threadIdx.x / TPR;
-  constexpr int R = RowShape<TPR>::kRows;
   const float invD = 1.f / (float)a.D;
+  const bool gate_ch = a.g && !a.gate_token;
+  // eight of the parameters k (0 w, 1 p, 2 a channel gate) from channel c;
+  // ones where there is none
+  auto read_params = [&](int k, int c, float (&v)[8]) {
+    const void* src = k == 0 ? a.w : k == 1 ? a.p : gate_ch ? a.g : nullptr;
+    const int dt = k == 2 ? a.gdt : a.wdt;
+    if (src) raw8_to_f32(load_raw8(src, dt, c), dt, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = !src ? 1.f : k == 2 ? v[j] : param(v[j], a.unit);
+  };
+  auto params = [&](int k, int c, float (&v)[8]) {
+    if (LP) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = par[k * cols + c + j];
+    } else {
+      read_params(k, c, v);
+    }
+  };
+  if (LP) {
+    for (int c = threadIdx.x * 8; c < a.D; c += TPR * R * 8) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        float v[8];
+        read_params(k, c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) par[k * cols + c + j] = v[j];
+      }
+    }
+  }
   float dw[NV][8], dp[NV][8], dg[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = dp[i][j] = dg[i][j] = 0.f;
-  const bool gate_ch = a.g && !a.gate_token;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * R + sub; row < a.T; row += (int64_t)gridDim.x * R) {
-    // Between two rows' uses of one half of sh lies a barrier that every wave
-    // reaches after its reads: the second sum's where there is a block, else
-    // the next row's (the halves then take turns).
-    float* const sh0 = sh[a.u ? 0 : turn];
-    turn ^= 1;
-    const size_t base = (size_t)row * a.D;
-    Raw8 r8[NV], x8[NV], u8[NV], e8[NV];
+  struct Row { Raw8 r[NV], x[NV], u[NV], e[NV]; };
+  auto load_row = [&](Row& q, int64_t row) {
+    const size_t base = (size_t)min(row, (int64_t)a.T - 1) * a.D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + t) * 8;
       if (c < a.D) {
         if (a.w) {
-          r8[i] = load_raw8(a.r, a.rdt, base + c);
-          x8[i] = load_raw8(a.dx, a.dxdt, base + c);
+          q.r[i] = load_raw8(a.r, a.rdt, base + c);
+          q.x[i] = load_raw8(a.dx, a.dxdt, base + c);
         }
-        if (a.u) u8[i] = load_raw8(a.u, a.udt, base + c);
-        if (a.dr) e8[i] = load_raw8(a.dr, a.rdt, base + c);
+        if (a.u) q.u[i] = load_raw8(a.u, a.udt, base + c);
+        if (a.dr) q.e[i] = load_raw8(a.dr, a.rdt, base + c);
       }
     }
-    float sum[3] = {0.f, 0.f, 0.f};   // r'^2, t r', u^2
+  };
+  // the same number of turns for every row group: the sums hold barriers
+  const int64_t step = (int64_t)gridDim.x * R;
+  const int64_t first = (int64_t)blockIdx.x * R;
+  Row q;
+  if (first < a.T) load_row(q, first + sub);
+  __syncthreads();   // the parameters
+  int turn = 0;
+  for (int64_t row0 = first; row0 < a.T; row0 += step) {
+    const int64_t row = row0 + sub;
+    const bool live = row < a.T;
+    const size_t base = (size_t)min(row, (int64_t)a.T - 1) * a.D;
     float r[NV][8], dx[NV][8], u[NV][8], d[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -205,92 +249,104 @@ __global__ __launch_bounds__(RowShape<TPR>::kThreads) void norm_backward_kernel(
       for (int j = 0; j < 8; ++j) r[i][j] = dx[i][j] = u[i][j] = d[i][j] = 0.f;
       if (c < a.D) {
         if (a.w) {
-          raw8_to_f32(r8[i], a.rdt, r[i]);
-          raw8_to_f32(x8[i], a.dxdt, dx[i]);
-          float wv[8];
-          raw8_to_f32(load_raw8(a.w, a.wdt, c), a.wdt, wv);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
-            sum[1] = fmaf(dx[i][j] * param(wv[j], a.unit), r[i][j], sum[1]);
-          }
+          raw8_to_f32(q.r[i], a.rdt, r[i]);
+          raw8_to_f32(q.x[i], a.dxdt, dx[i]);
         }
-        if (a.u) raw8_to_f32(u8[i], a.udt, u[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[2] = fmaf(u[i][j], u[i][j], sum[2]);
-        if (a.dr) raw8_to_f32(e8[i], a.rdt, d[i]);
+        if (a.u) raw8_to_f32(q.u[i], a.udt, u[i]);
+        if (a.dr) raw8_to_f32(q.e[i], a.rdt, d[i]);
       }
     }
-    row_sums<TPR>(sum, sh0);
+    if (row0 + step < a.T) load_row(q, row0 + step + sub);
+    float gt = 1.f;
+    if (a.g && a.gate_token) gt = load_one(a.g, a.gdt, min(row, (int64_t)a.T - 1));
+    float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // r'^2, t r', u^2, a u (dr', t, r')
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + t) * 8;
+      if (c < a.D) {
+        float wv[8], pv[8], gv[8];
+        params(0, c, wv);
+        params(1, c, pv);
+        params(2, c, gv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float tt = dx[i][j] * wv[j];
+          const float au = a.alpha * gv[j] * pv[j] * u[i][j];
+          sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
+          sum[1] = fmaf(tt, r[i][j], sum[1]);
+          sum[2] = fmaf(u[i][j], u[i][j], sum[2]);
+          sum[3] = fmaf(au, d[i][j], sum[3]);
+          sum[4] = fmaf(au, tt, sum[4]);
+          sum[5] = fmaf(au, r[i][j], sum[5]);
+        }
+      }
+    }
+    // the halves of sh take turns: a row's reads lie between its barrier and
+    // the next row's, after which the half is written again
+    row_sums<TPR>(sum, sh[turn][sub]);
+    turn ^= 1;
     const float inv = rsqrtf(sum[0] * invD + a.eps);
     const float m = sum[1] * inv * inv * invD;   // mean(t n) inv
     const float inv_u = a.p ? rsqrtf(sum[2] * invD + a.eps) : 1.f;
-    float gt = a.alpha;
-    if (a.g && a.gate_token) {
-      if (a.gdt == MOE_F32) gt *= static_cast<const float*>(a.g)[row];
-      else if (a.gdt == MOE_BF16) gt *= (float)static_cast<const __bf16*>(a.g)[row];
-      else gt *= (float)static_cast<const _Float16*>(a.g)[row];
-    }
-    float s2[2] = {0.f, 0.f};   // tp u, d z
+    const float aud = a.w ? sum[3] + inv * (sum[4] - m * sum[5]) : sum[3];
+    const float mp = gt * inv_u * aud * invD;
+    if (a.dg_token && t == 0 && live) a.dg_token[row] = inv_u * aud;
+    if (!live) continue;   // past its barrier
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + t) * 8;
       if (c < a.D) {
         if (a.w) {
           float wv[8];
-          raw8_to_f32(load_raw8(a.w, a.wdt, c), a.wdt, wv);
+          params(0, c, wv);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             dw[i][j] = fmaf(dx[i][j], r[i][j] * inv, dw[i][j]);
-            d[i][j] += inv * (dx[i][j] * param(wv[j], a.unit) - r[i][j] * m);
+            d[i][j] += inv * (dx[i][j] * wv[j] - r[i][j] * m);
           }
         }
         store8(a.dr_out, a.rdt, base + c, d[i]);
         if (a.u) {
-          float pv[8], gv[8];
-          if (a.p) raw8_to_f32(load_raw8(a.p, a.wdt, c), a.wdt, pv);
-          if (gate_ch) raw8_to_f32(load_raw8(a.g, a.gdt, c), a.gdt, gv);
+          float o[8], pv[8], gv[8];
+          params(1, c, pv);
+          params(2, c, gv);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float v = u[i][j] * inv_u;
-            const float pj = a.p ? param(pv[j], a.unit) : 1.f;
-            if (gate_ch) dg[i][j] = fmaf(a.alpha * d[i][j], v * pj, dg[i][j]);
-            if (a.gate_token) s2[1] = fmaf(d[i][j], v * pj, s2[1]);
-            const float dz = gt * d[i][j] * (gate_ch ? gv[j] : 1.f);
+            const float v = u[i][j] * inv_u, ad = a.alpha * d[i][j];
+            const float pj = pv[j], gj = gv[j];
+            dg[i][j] = fmaf(ad, v * pj, dg[i][j]);
+            const float dz = gt * ad * gj;
             dp[i][j] = fmaf(dz, v, dp[i][j]);
-            d[i][j] = dz * pj;
-            s2[0] = fmaf(d[i][j], v, s2[0]);
+            o[j] = a.p ? inv_u * (dz * pj - v * mp) : dz;
           }
-        }
-      }
-    }
-    if (a.u) {
-      row_sums<TPR>(s2, sh[1]);
-      const float mp = a.p ? s2[0] * invD : 0.f;
-      if (a.dg_token && t == 0) a.dg_token[row] = a.alpha * s2[1];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * 8;
-        if (c < a.D) {
-          float o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j] = a.p ? inv_u * (d[i][j] - u[i][j] * inv_u * mp) : d[i][j];
           store8(a.du, a.udt, base + c, o);
         }
       }
     }
   }
-  // this row slot's partials: slot blockIdx.x * R + sub of grid * R
-  const size_t slots = (size_t)gridDim.x * R;
-  const size_t slot = (size_t)blockIdx.x * R + sub;
+  // the workgroup's partials: its row groups' sums in order, then one slot
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + t) * 8;
-    if (c < a.D) {
-      if (a.w) store8(a.part, MOE_F32, slot * a.D + c, dw[i]);
-      if (a.p) store8(a.part, MOE_F32, (slots + slot) * a.D + c, dp[i]);
-      if (gate_ch) store8(a.part, MOE_F32, (2 * slots + slot) * a.D + c, dg[i]);
+  for (int k = 0; k < 3; ++k) {
+    float (*const v)[8] = k == 0 ? dw : k == 1 ? dp : dg;
+    if (!(k == 0 ? a.w != nullptr : k == 1 ? a.p != nullptr : gate_ch)) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + t) * 8;
+      if constexpr (R > 1) {
+        __syncthreads();
+        if (sub) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fold[(j * (R - 1) + sub - 1) * TPR + t] = v[i][j];
+        }
+        __syncthreads();
+        if (!sub) {
+          for (int s = 0; s < R - 1; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] += fold[(j * (R - 1) + s) * TPR + t];
+        }
+      }
+      if (c < a.D && !sub)
+        store8(a.part, MOE_F32, ((size_t)k * gridDim.x + blockIdx.x) * a.D + c, v[i]);
     }
   }
 }
@@ -298,61 +354,62 @@ __global__ __launch_bounds__(RowShape<TPR>::kThreads) void norm_backward_kernel(
 // out[c] = the slots' partials of column c, added in a fixed order: 16
 // threads take every 16th slot, then their sums in order. blockIdx.y picks
 // the vector.
-__global__ __launch_bounds__(256) void norm_columns_kernel(
+__global__ __launch_bounds__(1024) void norm_columns_kernel(
     const float* __restrict__ part, int slots, int D, float* o0, float* o1, float* o2) {
-  __shared__ float sh[16][17];
+  __shared__ float sh[16][64];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
-  const int c = blockIdx.x * 16 + (threadIdx.x & 15);
-  const int g = threadIdx.x >> 4;
+  const int l = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + l;
   float s = 0.f;
-  if (c < D)
-    for (int k = g; k < slots; k += 16) s += part[((size_t)blockIdx.y * slots + k) * D + c];
-  sh[g][threadIdx.x & 15] = s;
+  if (c < D) {
+    const float* p = part + (size_t)blockIdx.y * slots * D + c;
+#pragma unroll 4
+    for (int k = g; k < slots; k += 16) s += p[(size_t)k * D];
+  }
+  sh[g][l] = s;
   __syncthreads();
   if (g == 0 && c < D) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v += sh[k][threadIdx.x & 15];
+    for (int k = 0; k < 16; ++k) v += sh[k][l];
     out[c] = v;
   }
 }
 
 namespace {
 
-struct BwdShape { int grid, slots; };
-constexpr int kBwdGrid = 512;   // two workgroups a compute unit
-BwdShape bwd_shape(int T, int D) {
-  const int rows = D <= 1024 ? 4 : 1;
-  const int64_t need = ((int64_t)T + rows - 1) / rows;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(need, kBwdGrid));
-  return {grid, grid * rows};
+// Workgroups of the backward, each leaving one slot of partials: as many as
+// the compute units hold at once, two each (four of the 256-thread ones would
+// fit, with twice the partials), one of the widest rows.
+int bwd_slots(int T, int D) {
+  const int rows = D <= 512 ? 4 : D <= 2048 ? 2 : 1;
+  const int most = D <= 4096 ? 512 : 256;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + rows - 1) / rows, most));
 }
 
 }  // namespace
 
-size_t norm_backward_part_floats(int T, int D) {
-  return (size_t)3 * bwd_shape(T, D).slots * D;
-}
+size_t norm_backward_part_floats(int T, int D) { return (size_t)3 * bwd_slots(T, D) * D; }
 
-template <int TPR, int NV>
+template <int TPR, int R, int NV, bool LP = true>
 static void run_norm_backward(const NormBwdArgs& a, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((norm_backward_kernel<TPR, NV>), dim3(grid),
-                     dim3(RowShape<TPR>::kThreads), 0, s, a);
+  hipLaunchKernelGGL((norm_backward_kernel<TPR, R, NV, LP>), dim3(grid), dim3(TPR * R),
+                     LP ? 3 * TPR * NV * 8 * sizeof(float) : 0, s, a);
 }
 
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s) {
-  const BwdShape sh = bwd_shape(a.T, a.D);
-  if (a.D <= 512) run_norm_backward<64, 1>(a, sh.grid, s);
-  else if (a.D <= 1024) run_norm_backward<64, 2>(a, sh.grid, s);
-  else if (a.D <= 2048) run_norm_backward<256, 1>(a, sh.grid, s);
-  else if (a.D <= 4096) run_norm_backward<256, 2>(a, sh.grid, s);
-  else if (a.D <= 8192) run_norm_backward<512, 2>(a, sh.grid, s);
-  else run_norm_backward<1024, 2>(a, sh.grid, s);
+  const int slots = bwd_slots(a.T, a.D);
+  if (a.D <= 512) run_norm_backward<64, 4, 1>(a, slots, s);
+  else if (a.D <= 1024) run_norm_backward<128, 2, 1>(a, slots, s);
+  else if (a.D <= 2048) run_norm_backward<256, 2, 1>(a, slots, s);
+  else if (a.D <= 4096) run_norm_backward<512, 1, 1>(a, slots, s);
+  else if (a.D <= 8192) run_norm_backward<512, 1, 2>(a, slots, s);
+  else run_norm_backward<1024, 1, 2, false>(a, slots, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_columns_kernel, dim3((a.D + 15) / 16, 3), dim3(256), 0, s, a.part,
-                     sh.slots, a.D, a.dw, a.p ? a.dp : nullptr, a.dg_channel);
+  hipLaunchKernelGGL(norm_columns_kernel, dim3((a.D + 63) / 64, 3), dim3(1024), 0, s, a.part,
+                     slots, a.D, a.dw, a.p ? a.dp : nullptr, a.dg_channel);
   return hipGetLastError();
 }
 

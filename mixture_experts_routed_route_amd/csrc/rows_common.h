@@ -107,29 +107,49 @@ __device__ __forceinline__ uint2 f8_pack8(const float (&v)[8], float inv) {
   return uint2{o[0], o[1]};
 }
 
+// Lane exchanges within a row of 16 lanes by DPP (a few cycles; a shuffle
+// goes through the LDS): neighbours, pairs, mirrored halves, mirrored row.
+// After the four every lane holds the row's result.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
 // the largest magnitude over 16 neighbouring lanes (16 x 8 values: a block)
 __device__ __forceinline__ uint32_t max16(uint32_t m) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-  return m;
+  m = max(m, dpp<kDppXor1>(m));
+  m = max(m, dpp<kDppXor2>(m));
+  m = max(m, dpp<kDppHalfMirror>(m));
+  return max(m, dpp<kDppMirror>(m));
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v = dpp_add<kDppXor1>(v);
+  v = dpp_add<kDppXor2>(v);
+  v = dpp_add<kDppHalfMirror>(v);
+  v = dpp_add<kDppMirror>(v);
+  auto row = [&](int r) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * r));
+  };
+  return (row(0) + row(1)) + (row(2) + row(3));
 }
 
 // Sums of N values over the TPR threads of a row, the same bits in every
-// thread. sh: N * TPR / 64 floats per row group, used once between barriers
-// (the caller alternates between two).
+// thread. sh: the row group's own N * TPR / 64 floats, used once between
+// barriers (the caller alternates between two). Every thread of the
+// workgroup takes part.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* sh) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = (threadIdx.x % TPR) >> 6, lane = threadIdx.x & 63;
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) sh[i * W + wave] = v[i];
