@@ -90,6 +90,16 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   const bool tiles = d.T > kF8StreamRows &&
       (d.T > kF8StreamT || P > (int64_t)kF8StreamPairs * n_exp);
   const bool down = step >= 4;
+  // one token: two launches, the second with the pairs' sum
+  if (d.T == 1 && !(l.o.flags & MOE_OPT_TILED_DECODE) &&
+      f8_one_fits(l.D, l.F, d.k, d.n_shared)) {
+    if (step != 2 && step != 4) return hipSuccess;
+    const F8OneArgs one{l.x, l.xdt, (const uint8_t*)l.wg, (const uint8_t*)l.wu,
+                        (const uint8_t*)l.wd, l.wgs, l.wus, l.wds, p.ids, p.tok2pair,
+                        p.offsets, p.w, (float*)(b + L.h8), l.y, l.ydt, l.D, l.F, d.k,
+                        d.E, d.n_shared, l.o.swiglu_limit};
+    return down ? launch_f8_one_down(one, s) : launch_f8_one_gateup(one, s);
+  }
   F8Args g{};
   g.mode = down ? 2 : 1;
   g.K = down ? l.F : l.D;

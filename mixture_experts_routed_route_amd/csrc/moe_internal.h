@@ -347,6 +347,24 @@ bool f8_strip_raw_fits(int rows, int K);
 // prec 0: codes in the 8-bit matrix unit; 1: widened to f16
 hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s);
 
+// One-token calls on MOE_F8B128 weights (gemv_f8.hip).
+struct F8OneArgs {
+  const void* x; int xdt;   // [D]
+  const uint8_t* wg; const uint8_t* wu; const uint8_t* wd;
+  const float* wgs; const float* wus; const float* wds;
+  const int32_t* ids;       // [k] the token's experts (plan)
+  const int32_t* tok2pair;  // [k] their pair rows, -1 if dropped
+  const int32_t* offsets;   // [E + n_shared + 1]
+  const float* w;           // [k] routing weights
+  float* h;                 // [P, F] SwiGLU outputs
+  void* y; int ydt;         // [D]
+  int D, F, k, E, n_shared;
+  float clamp;
+};
+bool f8_one_fits(int D, int F, int k, int n_shared);
+hipError_t launch_f8_one_gateup(const F8OneArgs& a, hipStream_t s);
+hipError_t launch_f8_one_down(const F8OneArgs& a, hipStream_t s);
+
 // The layer on MOE_F8B128 weights (api_f8.hip): its device workspace and its
 // launches, on a plan's arrays.
 struct F8Plan {

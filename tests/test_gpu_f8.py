@@ -188,6 +188,20 @@ def test_layer_against_f64(dt, T, D, F, E, k, shared, cf):
     _check(wl, ws, torch.float32)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,F,E,k,shared,cf", [
+    (128, 128, 1, 1, 0, 0.0), (640, 256, 16, 6, 1, 0.0), (2048, 768, 12, 8, 1, 0.0),
+    (256, 4096, 8, 3, 0, 0.0), (8192, 128, 4, 2, 1, 0.0), (256, 128, 40, 17, 0, 0.0),
+    (128, 2048, 16, 15, 1, 0.0), (128, 4096, 18, 15, 1, 0.0)])
+def test_one_token(dt, D, F, E, k, shared, cf):
+    """T = 1: the two-launch path, the shapes it leaves to the strips (more
+    than 16 pairs, rows past its LDS), and the strips themselves."""
+    wl, ws = _layer(1, D, F, E, k, dt, shared, cf, seed=D + F + k)
+    for y_dtype in (torch.float32, DT[dt]):
+        _check(wl, ws, y_dtype)
+        _check(wl, ws, y_dtype, moe.make_options(flags=moe.MOE_OPT_TILED_DECODE))
+
+
 def test_layer_skewed_and_clamped():
     """One expert takes most rows, two take none, and the clamp binds."""
     bias = torch.tensor([8.0, 0.0, -40.0, 1.0, -40.0, 0.5])
