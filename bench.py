@@ -90,6 +90,11 @@ def parse():
                          "workloads; default the prefill one)")
     ap.add_argument("--router", action="store_true",
                     help="time moe_route (router map + plan + statistics)")
+    ap.add_argument("--block", action="store_true",
+                    help="time one layer step on 8-bit weights: norm, router "
+                         "and plan, experts, the norms between two blocks "
+                         "with the next rows quantised, the next block's "
+                         "8-bit projection (T defaults to 4096)")
     ap.add_argument("--copy-calibration", type=int, default=0, metavar="MIB",
                     help="also run one plain elementwise copy of MIB MiB "
                          "(dst = src * 1 in f32: MIB MiB read, MIB MiB "
@@ -140,6 +145,8 @@ def main():
         return bench_router(args, dev, torch, moe, W)
     if args.backward:
         return bench_backward(args, dev, torch, moe, W)
+    if args.block:
+        return bench_block(args, dev, torch, moe)
     wl = W.config(args.config, capacity_factor=args.capacity_factor, T=args.T,
                   pairs_per_expert=args.pairs_per_expert, w_dtype=args.weights)
     T, D, F, E, k, ns = (wl[n] for n in ("T", "D", "F", "E", "k", "n_shared"))
@@ -533,6 +540,76 @@ def bench_router(args, dev, torch, moe, W):
         "hardware": hardware(torch),
     }
     print(json.dumps(out), flush=True)
+
+
+def bench_block(args, dev, torch, moe):
+    """One layer step on 8-bit weights (the prefill layer's sizes): x =
+    norm(r); plan = route(x); y = experts(x); r, rows = norms around the
+    block, the rows quantised; out = the next block's projection of them.
+    Each part is also timed alone, with events around calls of its own."""
+    T = args.T or 4096
+    D, F, E, k, N = 2048, 768, 128, 8, 2048
+    g = torch.Generator(device=dev).manual_seed(0)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    bf = torch.bfloat16
+    r, w_router = rn(T, D), (rn(E, D) * D ** -0.5).to(bf)
+    w1, w2, post, gate = ((1 + 0.1 * rn(D)).to(bf) for _ in range(4))
+    weights = [moe.moe_quant_f8_weights((rn(E, n, c) * c ** -0.5).to(bf))
+               for n, c in ((F, D), (F, D), (D, F))]
+    proj = moe.moe_quant_f8_weights((rn(N, D) * D ** -0.5).to(bf))
+
+    def step():
+        _, x = moe.moe_norm(r, weight=w1)
+        plan, _, _ = moe.moe_route(x, w_router, k)
+        y = moe.moe_forward(plan, x, *weights)
+        r2, rows = moe.moe_norm(r, y, w2, post, gate, alpha=0.5,
+                                x_dtype=torch.float8_e4m3fn)
+        return x, plan, y, rows, moe.moe_gemm_f8(rows, proj)
+
+    def timed(f, n):
+        for _ in range(args.warmup):
+            f()
+        torch.cuda.synchronize()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(n):
+            f()
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b) / n
+
+    x, plan, y, rows, _ = step()
+    torch.cuda.synchronize()
+    parts = {
+        "norm": timed(lambda: moe.moe_norm(r, weight=w1), args.steps),
+        "route": timed(lambda: moe.moe_route(x, w_router, k), args.steps),
+        "experts": timed(lambda: moe.moe_forward(plan, x, *weights), args.steps),
+        "norms_around": timed(lambda: moe.moe_norm(
+            r, y, w2, post, gate, alpha=0.5, x_dtype=torch.float8_e4m3fn), args.steps),
+        "projection": timed(lambda: moe.moe_gemm_f8(rows, proj), args.steps)}
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        step()
+    torch.cuda.synchronize()
+    ms = (time.perf_counter() - t0) * 1e3 / args.steps
+    flops = T * (6.0 * D * F * k + 2.0 * D * E + 2.0 * D * N)
+    print(json.dumps({
+        "metric": "layer step TFLOP/s on 8-bit weights (experts, router and "
+                  "projection products)",
+        "value": round(flops / (ms * 1e-3) / 1e12, 3), "unit": "TFLOP/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(ms, 4), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "f8 (e4m3, blocks of 128)",
+        "data": "synthetic (seeded)",
+        "config": {"workload": "layer_step_f8", "T": T, "d_model": D, "d_ff": F,
+                   "experts": E, "top_k": k, "projection": N,
+                   "parallelism": "single GPU"},
+        "tokens_per_s": round(T / (ms * 1e-3), 1),
+        "part_ms": {n: round(v, 4) for n, v in parts.items()},
+        "hardware": hardware(torch)}))
 
 
 def bench_backward(args, dev, torch, moe, W):

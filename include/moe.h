@@ -82,8 +82,12 @@ typedef enum {
      * the quotients and the product rounded to f32, the code to nearest
      * even. A block that holds a NaN or an infinity has a scale of NaN or
      * infinity and stands for NaN. As weights of moe_forward (bf16 / f16
-     * x), the layer quantises x's rows and the SwiGLU output (f32, per pair
-     * and 128 features) and multiplies codes. */
+     * x; scales 16-byte aligned), the layer quantises x's rows and the
+     * SwiGLU output (f32, per pair and 128 features) and multiplies codes:
+     * experts of at most 16 rows, and decode-shaped calls, with sums in f32
+     * throughout; experts of more rows as moe_gemm_f8 does for a 16-bit
+     * output (a bf16 layer's products and an f16 layer's down) or an F32 one
+     * (an f16 layer's gate/up). */
     MOE_F8B128 = 6
 } moe_dtype;
 
@@ -160,7 +164,11 @@ typedef struct {
  *                     compute unit; the second launch also sums the pairs
  *                     into y in the combine's order and precision (phases
  *                     3 and 5 of moe_phase_times; 6 is not used).
- *                     MOE_OPT_TILED_DECODE keeps such calls on the tile. */
+ *                     MOE_OPT_TILED_DECODE keeps such calls on the tile.
+ * A layer on MOE_F8B128 weights takes swiglu_limit, the phase flags and
+ * MOE_OPT_TILED_DECODE (its one-token launches then give way to the strips of
+ * other decode-shaped calls); its routes go by rules of their own, and the
+ * other options are not read. */
 typedef struct {
     float swiglu_limit;
     float splitk_max_pairs;
@@ -336,7 +344,7 @@ moe_status moe_forward(const moe_plan *plan, const void *x, int32_t x_dtype,
  *                [K / 32][N][32] (NULL without a fat route); fat_slots is
  *                the number of slots the workspace holds.
  * Returns MOE_EINVAL on a NULL plan, ws or out, or sizes the workspace query
- * refuses. */
+ * refuses, MOE_EUNSUPPORTED for 8-bit weights. */
 typedef struct {
     const void *h, *h_lo;
     int64_t h_ld;
@@ -500,8 +508,10 @@ moe_status moe_norm_backward(const moe_norm_desc *desc,
  * 14 gate/up split-K groups of 17..64 rows, 15 down groups of 17..64 rows
  * (moe_forward); 7 router kernel, 8 plan, 9 routing statistics
  * (moe_route); 10 recompute, 11 data gradients, 12 weight gradients,
- * 13 routing-weight gradients (moe_backward). Synchronises on the recorded
- * events. reset != 0 clears afterwards. */
+ * 13 routing-weight gradients (moe_backward). On 8-bit weights: 1 x's rows
+ * quantised, 2 / 4 the products on tiles, 3 / 5 those of thin groups and
+ * decode-shaped calls, 0 and 6 as above (a step that a call does without
+ * takes no time). Synchronises on the recorded events. reset != 0 clears afterwards. */
 #define MOE_N_PHASES 16
 moe_status moe_phase_times(double *ms, int32_t n, int64_t *calls,
                            int32_t reset);

@@ -4,7 +4,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "moe_internal.h"
+#include "f8_internal.h"
 
 using namespace moe;
 

@@ -11,7 +11,7 @@
 #include <string>
 #include <vector>
 
-#include "moe_internal.h"
+#include "f8_internal.h"
 
 using namespace moe;
 

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "f8_internal.h"
 
 namespace moe {
 
