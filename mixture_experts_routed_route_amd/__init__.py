@@ -737,6 +737,11 @@ def _on(device):
     return torch.cuda.device(device)
 
 
+def _c_int(name: str, n: int):
+    if n > 2**31 - 1:
+        raise ValueError(f"{name}={n} must be below 2^31")
+
+
 def moe_quant_f8(x: torch.Tensor) -> tuple:
     """Rows [.., K] (float32, bfloat16 or float16; K a multiple of 8) as 8-bit
     blocks: (codes float8_e4m3fn [.., K], scales float32 [.., ceil(K / 128)]),
@@ -746,6 +751,7 @@ def moe_quant_f8(x: torch.Tensor) -> tuple:
     K = x.shape[-1]
     if K < 8 or K % 8:
         raise ValueError(f"K={K} must be a positive multiple of 8")
+    _c_int("K", K)
     with _on(x.device):
         x = x.contiguous()
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
@@ -765,6 +771,8 @@ def moe_quant_f8_weights(w: torch.Tensor) -> tuple:
     N, K = w.shape[-2:]
     if K < 8 or K % 8:
         raise ValueError(f"K={K} must be a positive multiple of 8")
+    _c_int("K", K)
+    _c_int("N", N)
     mats = 1
     for n in w.shape[:-2]:
         mats *= n
@@ -795,6 +803,8 @@ def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
     N, K = wq.shape
     if K < 16 or K % 16:
         raise ValueError(f"K={K} must be a positive multiple of 16")
+    _c_int("K", K)
+    _c_int("N", N)
     if xs.shape[:-1] != xq.shape[:-1] or xs.shape[-1] != _blocks(K) \
             or ws.shape != (_blocks(N), _blocks(K)):
         raise ValueError(f"scales {tuple(xs.shape)} and {tuple(ws.shape)} do not match "
@@ -840,6 +850,7 @@ def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
     T, D = residual.shape
     if D < 8 or D % 8 or D > MOE_NORM_MAX_D:
         raise ValueError(f"D={D} must be a multiple of 8 in 8..{MOE_NORM_MAX_D}")
+    _c_int("T", T)
     if not residual.is_contiguous():
         residual = residual.contiguous()
     udt = wdt = gdt = MOE_F32

@@ -207,7 +207,8 @@ __global__ __launch_bounds__(512, 4) void f8_stream_kernel(F8Args a, int ks) {
   const int K = a.K, N = a.N, nkb = K / 128, nnb = N / 128;
   // items: groups of 17..64 rows in four parts of 16, then those of <= 16
   const int n4 = a.meta[kMetaSk4] * 4, n1 = a.meta[kMetaSk1];
-  const int gi = blockIdx.x / nnb, cb = blockIdx.x - gi * nnb;
+  const uint32_t item = wide_block();
+  const int gi = item / (uint32_t)nnb, cb = item - gi * (uint32_t)nnb;
   if (gi >= n4 + n1) return;
   const int32_t* g = gi < n4 ? a.list4 + 4 * (gi >> 2) : a.list + 4 * (gi - n4);
   const int part = gi < n4 ? (gi & 3) * 16 : 0;
@@ -325,8 +326,8 @@ __global__ __launch_bounds__(512, 4) void f8_stream_kernel(F8Args a, int ks) {
 }
 
 template <int MODE, int NX>
-static void run_stream(const F8Args& a, int ks, unsigned grid, hipStream_t s) {
-  hipLaunchKernelGGL((f8_stream_kernel<MODE, NX>), dim3(grid), dim3(512), 0, s, a, ks);
+static void run_stream(const F8Args& a, int ks, int64_t grid, hipStream_t s) {
+  hipLaunchKernelGGL((f8_stream_kernel<MODE, NX>), wide_grid(grid), dim3(512), 0, s, a, ks);
 }
 
 hipError_t launch_f8_stream(const F8Args& a, hipStream_t s) {
@@ -338,9 +339,9 @@ hipError_t launch_f8_stream(const F8Args& a, hipStream_t s) {
   int ks = 8;
   while (ks > 1 && nkb < 2 * ks) ks >>= 1;
   const bool three = (nkb + ks * 2 - 1) / (ks * 2) * 2 > (nkb + ks * 3 - 1) / (ks * 3) * 3 - 1;
-  if (a.mode == 1) run_stream<1, 2>(a, ks, (unsigned)grid, s);
-  else if (three) run_stream<2, 3>(a, ks, (unsigned)grid, s);
-  else run_stream<2, 2>(a, ks, (unsigned)grid, s);
+  if (a.mode == 1) run_stream<1, 2>(a, ks, grid, s);
+  else if (three) run_stream<2, 3>(a, ks, grid, s);
+  else run_stream<2, 2>(a, ks, grid, s);
   return hipGetLastError();
 }
 

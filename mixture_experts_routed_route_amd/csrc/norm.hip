@@ -39,7 +39,7 @@ template <int TPR, int NV>
 __global__ __launch_bounds__(RowShape<TPR>::kThreads) void norm_forward_kernel(NormArgs a) {
   __shared__ float sh[2 * 16];
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RowShape<TPR>::kRows + threadIdx.x / TPR;
+  const int64_t row = (int64_t)wide_block() * RowShape<TPR>::kRows + threadIdx.x / TPR;
   if (row >= a.T) return;   // whole waves, and whole workgroups where TPR > 64
   const size_t base = (size_t)row * a.D;
   Raw8 rr[NV], ur[NV];
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(RowShape<TPR>::kThreads) void norm_forward_kernel(N
 template <int TPR, int NV>
 static hipError_t run_norm_forward(const NormArgs& a, hipStream_t s) {
   constexpr int R = RowShape<TPR>::kRows;
-  hipLaunchKernelGGL((norm_forward_kernel<TPR, NV>), dim3((unsigned)(((int64_t)a.T + R - 1) / R)),
+  hipLaunchKernelGGL((norm_forward_kernel<TPR, NV>), wide_grid(((int64_t)a.T + R - 1) / R),
                      dim3(RowShape<TPR>::kThreads), 0, s, a);
   return hipGetLastError();
 }

@@ -10,7 +10,7 @@ namespace moe {
 __global__ __launch_bounds__(256) void quant_rows_kernel(
     const void* __restrict__ x, int dt, uint32_t n_blocks, uint32_t nb, int K,
     uint8_t* __restrict__ q, float* __restrict__ s) {
-  const uint32_t g = blockIdx.x * 16u + (threadIdx.x >> 4);
+  const uint32_t g = wide_block() * 16u + (threadIdx.x >> 4);
   if (g >= n_blocks) return;   // whole groups of 16 lanes
   const uint32_t row = g / nb, b = g - row * nb;
   const int k = (int)(b * 128u) + (threadIdx.x & 15) * 8;
@@ -27,7 +27,7 @@ hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
   const int64_t nb = (K + 127) / 128;
   const int64_t n = rows * nb;
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(quant_rows_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, st,
+  hipLaunchKernelGGL(quant_rows_kernel, wide_grid((n + 15) / 16), dim3(256), 0, st,
                      x, dt, (uint32_t)n, (uint32_t)nb, K, (uint8_t*)q, s);
   return hipGetLastError();
 }
@@ -35,10 +35,11 @@ hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
 // Weights: a workgroup takes one 128 x 128 block, 16 rows a pass with 16
 // lanes a row, all of it in registers between the maximum and the codes.
 __global__ __launch_bounds__(256) void quant_weights_kernel(
-    const void* __restrict__ w, int dt, uint32_t nn, uint32_t nk, int N, int K,
-    uint8_t* __restrict__ q, float* __restrict__ s) {
+    const void* __restrict__ w, int dt, uint32_t n_blocks, uint32_t nn, uint32_t nk, int N,
+    int K, uint8_t* __restrict__ q, float* __restrict__ s) {
   __shared__ uint32_t mx[4];
-  const uint32_t blk = blockIdx.x;
+  const uint32_t blk = wide_block();
+  if (blk >= n_blocks) return;   // whole workgroups
   const uint32_t kb = blk % nk, t = blk / nk;
   const uint32_t rb = t % nn, mat = t / nn;
   const int k = (int)kb * 128 + (threadIdx.x & 15) * 8;
@@ -76,8 +77,8 @@ hipError_t launch_quant_weights(const void* w, int dt, int64_t mats, int N,
   const int64_t nn = (N + 127) / 128, nk = (K + 127) / 128;
   const int64_t n = mats * nn * nk;
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(quant_weights_kernel, dim3((unsigned)n), dim3(256), 0, st, w, dt,
-                     (uint32_t)nn, (uint32_t)nk, N, K, (uint8_t*)q, s);
+  hipLaunchKernelGGL(quant_weights_kernel, wide_grid(n), dim3(256), 0, st, w, dt,
+                     (uint32_t)n, (uint32_t)nn, (uint32_t)nk, N, K, (uint8_t*)q, s);
   return hipGetLastError();
 }
 

@@ -8,6 +8,15 @@
 
 namespace moe {
 
+// A launch holds fewer than 2^32 threads along x: more than 2^20 workgroups
+// go into rows of that many, and a kernel asks for its number here (those
+// past the last return).
+inline dim3 wide_grid(int64_t n) {
+  const unsigned x = (unsigned)(n < (1 << 20) ? n : 1 << 20);
+  return dim3(x, (unsigned)((n + x - 1) / x));
+}
+__device__ __forceinline__ uint32_t wide_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // 8 values as loaded: f32 fills both words, 16-bit types the first. The type
 // is uniform over a launch, so the branches are scalar.
 struct Raw8 { uint4 a, b; };

@@ -196,6 +196,25 @@ def test_binding_refuses_tensors():
             moe.moe_norm_backward(*args, **kw)
 
 
+def test_binding_refuses_sizes_past_an_int():
+    """Sizes of 2^31 and more, which the C call would read modulo 2^32."""
+    n = 2 ** 31
+    wide = torch.zeros(1).expand(1, n + 16)
+    tall = torch.zeros(8).expand(n, 8)
+    for call in (lambda: moe.moe_quant_f8(wide), lambda: moe.moe_quant_f8_weights(wide),
+                 lambda: moe.moe_quant_f8_weights(tall), lambda: moe.moe_norm(tall, weight=torch.ones(8)),
+                 lambda: moe.moe_norm_backward(tall, None, tall, weight=torch.ones(8))):
+        with pytest.raises(ValueError, match="below 2\\^31"):
+            call()
+    q, s = torch.zeros(1, dtype=F8), torch.zeros(1)
+    a, sa = q.expand(4, 2 ** 32 + 16), s.expand(4, 2 ** 25 + 1)
+    w, sw = q.expand(2, 2 ** 32 + 16), s.expand(1, 2 ** 25 + 1)
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        moe.moe_gemm_f8((a, sa), (w, sw))
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        moe.moe_gemm_f8((q.expand(4, 16), s.expand(4, 1)), (q.expand(n, 16), s.expand(2 ** 24, 1)))
+
+
 def test_constants_match_the_header():
     import os
     import re

@@ -85,6 +85,26 @@ def test_quant_weights_bit_exact(dt, n, N, K):
     assert q2.shape == (N, K) and torch.equal(s2.cpu(), rs[0])
 
 
+@pytest.mark.parametrize("kind", ["rows", "weights"])
+def test_quant_many_short_blocks(kind):
+    """More workgroups than a launch holds along one axis (2^32 threads):
+    the same eight values and their negatives, row after row."""
+    n = (1 << 28) + 48 if kind == "rows" else (1 << 24) + 3
+    v = torch.tensor([1.0, -0.3, 0.01, 0.0, 7.0, -2.5, 0.6, 3.0])
+    x = torch.empty(n, 8, dtype=torch.bfloat16, device="cuda")
+    x[:] = v.to(x)
+    x[1::2] *= -1
+    if kind == "rows":
+        q, s = moe.moe_quant_f8(x)
+    else:
+        q, s = (t.view(n, -1) for t in moe.moe_quant_f8_weights(x.view(n, 1, 8)))
+    rq, rs = R.quant_rows(x[:2].cpu())
+    assert bool((s == rs[0].cuda()).all())
+    q = q.view(torch.int64)
+    pair = rq.view(torch.int64).cuda()
+    assert bool((q[::2] == pair[0]).all()) and bool((q[1::2] == pair[1]).all())
+
+
 def _product(M, N, K, out, seed=0):
     a = R.quant_rows(_rows(M, K, "bf16", seed))
     w = R.quant_weights((_rows(N, K, "f32", seed + 1, wide=False) * K ** -0.5)[None])
@@ -202,6 +222,13 @@ def test_one_token(dt, D, F, E, k, shared, cf):
         _check(wl, ws, y_dtype, moe.make_options(flags=moe.MOE_OPT_TILED_DECODE))
 
 
+@pytest.mark.parametrize("T,D,F,k", [(16, 2048, 128, 2), (9, 256, 4096, 1), (2, 16384, 128, 2)])
+def test_few_tokens_of_wide_rows(T, D, F, k):
+    """Decode-shaped calls whose rows are too wide for the strips' LDS."""
+    wl, ws = _layer(T, D, F, 4, k, "bf16", 1, seed=T + D)
+    _check(wl, ws, torch.float32)
+
+
 def test_layer_skewed_and_clamped():
     """One expert takes most rows, two take none, and the clamp binds."""
     bias = torch.tensor([8.0, 0.0, -40.0, 1.0, -40.0, 0.5])
@@ -274,3 +301,30 @@ def test_graph_replays_and_streams():
         _, y2, z2 = step()
     side.synchronize()
     assert torch.equal(y2, y) and torch.equal(z2, z)
+
+
+def test_two_calls_at_once():
+    """Products, layers and quantisers on two streams at the same time, with
+    the same weights: each as it is alone."""
+    wl, ws = _layer(300, 256, 384, 8, 2, "bf16", 1, seed=12)
+    dev = {n: tuple(t.cuda() for t in v) for n, v in ws.items()}
+    proj = tuple(t[0].cuda() for t in R.quant_weights(torch.randn(1, 512, 256) * 0.1))
+    xs = [wl["x"].cuda(), wl["x"].flip(0).contiguous().cuda()]
+    lg = [wl["logits"].cuda(), wl["logits"].flip(0).contiguous().cuda()]
+
+    def step(i):
+        p = moe.moe_plan_create(lg[i], 2, 0.0, 1)
+        y = moe.moe_forward(p, xs[i], dev["w_gate"], dev["w_up"], dev["w_down"], y_dtype=torch.bfloat16)
+        return p, y, moe.moe_gemm_f8(moe.moe_quant_f8(y), proj)
+
+    alone = [step(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                runs.append((i, step(i)))
+    torch.cuda.synchronize()
+    for i, (_, y, z) in runs:
+        assert torch.equal(y, alone[i][1]) and torch.equal(z, alone[i][2])

@@ -99,6 +99,16 @@ def test_forward_parts_and_in_place():
     assert st == moe.MOE_OK and torch.equal(r, full) and torch.equal(x1, x2)
 
 
+def test_forward_many_rows():
+    """More workgroups than a launch holds along one axis (2^32 threads)."""
+    T = (1 << 26) + 5
+    r = torch.full((T, 8), 2.0, dtype=torch.bfloat16, device="cuda")
+    r[-1] = -4.0
+    out, x = moe.moe_norm(r, r, weight=torch.full((8,), 3.0, dtype=torch.bfloat16, device="cuda"), eps=0.0)
+    assert bool((out[:-1] == 4.0).all()) and bool((out[-1] == -8.0).all())
+    assert bool((x[:-1] == 3.0).all()) and bool((x[-1] == -3.0).all())
+
+
 def test_forward_special_rows():
     """A row of zeros norms to zeros; NaN and infinities stay in their rows."""
     v = _inputs(6, 256, "f32", "f32", "f32", True, "none", False, seed=5)
