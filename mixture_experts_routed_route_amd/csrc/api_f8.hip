@@ -32,7 +32,7 @@ struct F8Layout {
   int cap_tiles, cap_sk1, cap_sk4;
 };
 
-F8Layout f8_layout(const moe_plan_desc& d, int D, int F, int xdt) {
+F8Layout f8_layout(const moe_plan_desc& d, int D, int F) {
   F8Layout L{};
   const size_t P = (size_t)d.T * d.k + (size_t)d.n_shared * d.T;
   const int n_exp = d.E + d.n_shared;
@@ -46,7 +46,8 @@ F8Layout f8_layout(const moe_plan_desc& d, int D, int F, int xdt) {
   // codes, or a decode-shaped call's f32 values
   L.h8 = take(P * F * (d.T <= kDecodeT ? 4 : 1));
   L.hs = take(P * (F / 128) * 4);
-  L.y = take(P * D * (xdt == MOE_F16 ? 2 : 4));
+  // f32: a rounding of every pair to f16 would weigh as much as y's own
+  L.y = take(P * D * 4);
   L.full_tiles = take((size_t)L.cap_tiles * 8);
   L.sk1 = take((size_t)L.cap_sk1 * 16);
   L.sk4 = take((size_t)L.cap_sk4 * 16);
@@ -59,8 +60,8 @@ F8Layout f8_layout(const moe_plan_desc& d, int D, int F, int xdt) {
 
 }  // namespace
 
-size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt) {
-  return f8_layout(d, D, F, xdt).bytes;
+size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F) {
+  return f8_layout(d, D, F).bytes;
 }
 
 // A plan's experts of more rows than this take the tile: its 64-row tiles
@@ -80,7 +81,7 @@ int moe::f8_step_phase(int step) {
 
 hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s) {
   const moe_plan_desc& d = p.desc;
-  const F8Layout L = f8_layout(d, l.D, l.F, l.xdt);
+  const F8Layout L = f8_layout(d, l.D, l.F);
   char* b = l.ws;
   const int64_t P = (int64_t)d.T * d.k + (int64_t)d.n_shared * d.T;
   const int n_exp = d.E + d.n_shared;
@@ -111,7 +112,7 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   g.pair_token = p.pair_token;
   g.offsets = p.offsets;
   g.clamp = l.o.swiglu_limit;
-  g.odt = l.xdt == MOE_F16 ? MOE_F16 : MOE_F32;
+  g.odt = MOE_F32;
   g.meta = raw ? p.dmeta : (const int32_t*)(b + L.meta);
   g.adt = MOE_F8B128;
   g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
@@ -173,7 +174,7 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       // step weighs more than f16's rounding of y
       return launch_f8_tile(g, !down && l.xdt == MOE_F16, s);
     default:
-      return launch_combine(b + L.y, l.xdt == MOE_F16, p.tok2pair, p.w, p.offsets, d.T,
+      return launch_combine(b + L.y, false, p.tok2pair, p.w, p.offsets, d.T,
                             l.D, d.k, d.n_shared, d.E, l.ydt, l.y, s);
   }
 }

@@ -91,7 +91,7 @@ struct F8Layer {
   char* ws;
   moe_options o;
 };
-size_t f8_layer_bytes(const moe_plan_desc& d, int D, int F, int xdt);
+size_t f8_layer_bytes(const moe_plan_desc& d, int D, int F);
 // steps of the layer in order; `phase` is the index moe_phase_times reports
 constexpr int kF8Steps = 7;
 int f8_step_phase(int step);

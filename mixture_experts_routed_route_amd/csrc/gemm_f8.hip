@@ -21,11 +21,12 @@ namespace moe {
 
 // Strips: a wave takes 16 weight rows (gate/up: 16 of each matrix) against
 // up to 16 RB rows of one group, weight operands straight from memory to
-// registers (each weight code is used by one wave only; four blocks of K of
-// loads in flight a wave). A workgroup of four waves takes 4 / ks strips, ks
-// waves sharing one's blocks of K, their partial sums meeting in LDS: ks = 4
-// from 16 blocks on, 2 from 8, else 1, so that a wave streams at least four
-// blocks and short rows do not leave workgroups of a few KB.
+// registers (each weight code is used by one wave only). A workgroup of four
+// waves takes 4 / ks strips, ks waves sharing one's blocks of K, their partial
+// sums meeting in LDS: ks = 4 from 16 blocks on, 2 from 8, else 1, so that a
+// wave streams at least four blocks and short rows do not leave workgroups of
+// a few KB. A wave holds one block of loads at a time: the up to eight
+// workgroups of a CU cover one another's waits.
 //
 // SRC 0 (plain products) reads quantised rows. SRC 1 (decode-shaped plans)
 // reads the rows as they are (x in its type, or h in f32) and quantises the
@@ -36,7 +37,6 @@ constexpr int kStripLds = 32768;   // bytes of rows a workgroup may hold (SRC 1)
 template <int MODE, int RB, int SRC>
 __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
   constexpr int WF = MODE == 1 ? 2 : 1;
-  constexpr int U = 1;
   __shared__ float part[3][WF][RB][256];
   extern __shared__ __attribute__((aligned(16))) char rows_lds[];   // SRC 1
   const int lane = threadIdx.x & 63;
@@ -74,12 +74,10 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
       w[f] = (f ? a.B1 : a.B0) + ((size_t)e * N + n) * K + lq * 16;
       ws[f] = (f ? a.B1s : a.B0s) + ((size_t)e * nnb + (n0 >> 7)) * nkb;
     }
-    v8i32 wv[U][WF];
-    auto load_weights = [&](int kb0) {
+    v8i32 wv[WF];
+    auto load_weights = [&](int kb) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int f = 0; f < WF; ++f) wv[u][f] = load_codes(w[f], lq, (kb0 + u * ks) * 128, K);
+      for (int f = 0; f < WF; ++f) wv[f] = load_codes(w[f], lq, kb * 128, K);
     };
     load_weights(kw);
     const uint8_t* x[RB];
@@ -115,37 +113,29 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
     for (int f = 0; f < WF; ++f)
 #pragma unroll
       for (int t = 0; t < RB; ++t) acc[f][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int kb0 = kw; kb0 < nkb; kb0 += U * ks) {
-      if (kb0 != kw) load_weights(kb0);
-      v8i32 xv[U][RB];
-      float sx[U][RB], sw[U][WF];
+    for (int kb = kw; kb < nkb; kb += ks) {
+      if (kb != kw) load_weights(kb);
+      v8i32 xv[RB];
+      float sx[RB], sw[WF];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int kb = kb0 + u * ks, kc = min(kb, nkb - 1);
-#pragma unroll
-        for (int t = 0; t < RB; ++t) {
-          xv[u][t] = load_codes(x[t], lq, kb * 128, K);
-          sx[u][t] = xs[t][kc];
-        }
-#pragma unroll
-        for (int f = 0; f < WF; ++f) sw[u][f] = ws[f][kc];
+      for (int t = 0; t < RB; ++t) {
+        xv[t] = load_codes(x[t], lq, kb * 128, K);
+        sx[t] = xs[t][kb];
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (kb0 + u * ks >= nkb) break;   // uniform in the wave
-        Codes wc[WF];
+      for (int f = 0; f < WF; ++f) sw[f] = ws[f][kb];
+      Codes wc[WF];
 #pragma unroll
-        for (int f = 0; f < WF; ++f) wc[f] = widen(wv[u][f]);
+      for (int f = 0; f < WF; ++f) wc[f] = widen(wv[f]);
 #pragma unroll
-        for (int t = 0; t < RB; ++t) {
-          const Codes xc = widen(xv[u][t]);
+      for (int t = 0; t < RB; ++t) {
+        const Codes xc = widen(xv[t]);
 #pragma unroll
-          for (int f = 0; f < WF; ++f) {
-            const floatx4 p = block_product(wc[f], xc);
-            const float sc = sx[u][t] * sw[u][f];
+        for (int f = 0; f < WF; ++f) {
+          const floatx4 p = block_product(wc[f], xc);
+          const float sc = sx[t] * sw[f];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[f][t][q] = fmaf(p[q], sc, acc[f][t][q]);
-          }
+          for (int q = 0; q < 4; ++q) acc[f][t][q] = fmaf(p[q], sc, acc[f][t][q]);
         }
       }
     }

@@ -618,7 +618,7 @@ size_t moe_forward_workspace_bytes(const moe_plan* p, int32_t D, int32_t F,
     return 0;
   }
   const moe_options o = opt ? *opt : defaults();
-  if (w_dtype == MOE_F8B128) return f8_layer_bytes(p->desc, D, F, x_dtype);
+  if (w_dtype == MOE_F8B128) return f8_layer_bytes(p->desc, D, F);
   return fwd_layout(p->desc, D, F, x_dtype, w_dtype, o).bytes;
 }
 
@@ -650,7 +650,7 @@ moe_status moe_forward(const moe_plan* p, const void* x, int32_t x_dtype,
     return fail(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
   const bool f8 = wdt == MOE_F8B128;
   FwdLayout L{};
-  if (f8) L.bytes = f8_layer_bytes(d, D, F, x_dtype);
+  if (f8) L.bytes = f8_layer_bytes(d, D, F);
   else L = fwd_layout(d, D, F, x_dtype, wdt, o);
   const size_t Pmax_rows = (size_t)d.T * d.k + (size_t)d.n_shared * d.T;
   const size_t lim31 = ((size_t)1 << 31) - 1;

@@ -183,9 +183,8 @@ def _check(wl, ws, y_dtype, options=None):
     v = moe.moe_plan_get_views(p)
     ids, w = v["topk_id"].cpu().long(), v["topk_w"].cpu()
     keep = v["tok2pair"].cpu() >= 0
-    pair = torch.float16 if wl["x"].dtype == torch.float16 else torch.float32
     ref, bound = R.layer(wl["x"], ws["w_gate"], ws["w_up"], ws["w_down"], ids, w, keep,
-                         wl["E"], wl["n_shared"], wl["swiglu_limit"], y_dtype, pair)
+                         wl["E"], wl["n_shared"], wl["swiglu_limit"], y_dtype, torch.float32)
     err = (y.cpu().double() - ref).abs()
     assert bool((err <= bound).all()), float((err / bound).max())
     # In the norm: a code that moves to a neighbour changes its value by at
