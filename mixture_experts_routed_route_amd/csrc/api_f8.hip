@@ -66,11 +66,19 @@ size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F) {
 
 // A plan's experts of more rows than this take the tile: its 64-row tiles
 // read 256 weight rows once for all rows, where a stream of thin groups reads
-// them again for every 16 rows.
+// them again for every 16 rows. With 32 (64) instead of 16, 512 uniform tokens
+// on 128 experts, top-8, D 2048, F 768 take 266 (332) us, not 190; 4096 skewed
+// ones 516 (530), not 447.
 constexpr int kF8StreamRows = 16;
-// ... unless the plan holds few pairs an expert: then the tiles would leave
-// most compute units idle, and their launches are saved.
-constexpr int kF8StreamT = 256, kF8StreamPairs = 32;
+// ... in plans of at least so many pairs an expert and more than so many in
+// all. Below, the tiles' two launches wait for a few workgroups' walks along
+// K: us with tiles / with streams alone at the same D and F: 160 tokens on
+// 128 experts (10 pairs an expert) 172 / 150, 224 (14) 174 / 175, 256 (16)
+// 178 / 200; 32 tokens on 16 experts (16, 256 pairs) 68 / 47, 128 on 8 (32)
+// 42 / 47, 256 on 8 (64) 49 / 55; 1024 skewed ones, top-1 of 128 (8), 103 / 82.
+constexpr int kF8TilePairs = 16, kF8TileAll = 256;
+// Above so many tokens always: one expert may hold them all.
+constexpr int kF8StreamT = 1024;
 
 // 0 quantise x, 1 classify, 2 gate/up of thin groups, 3 gate/up tile, 4 down
 // of thin groups, 5 down tile, 6 combine
@@ -88,8 +96,8 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   // decode-shaped calls: the plan's own groups, and the strips quantise x and
   // h themselves
   const bool raw = p.decode && f8_strip_raw_fits(d.T, std::max(l.D, l.F));
-  const bool tiles = d.T > kF8StreamRows &&
-      (d.T > kF8StreamT || P > (int64_t)kF8StreamPairs * n_exp);
+  const bool tiles = d.T > kF8StreamT ||
+      (d.T > kF8StreamRows && P >= (int64_t)kF8TilePairs * n_exp && P > kF8TileAll);
   const bool down = step >= 4;
   // one token: two launches, the second with the pairs' sum
   if (d.T == 1 && !(l.o.flags & MOE_OPT_TILED_DECODE) &&
@@ -130,10 +138,6 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       ca.n_exp = n_exp;
       ca.mode = 1;
       ca.S = tiles ? kF8StreamRows : 1e30;
-      // too few tiles for one round of the compute units: experts of up to
-      // 256 rows join the thin groups
-      ca.full_nnb = l.F / 128;
-      ca.full_fill = l.ncu;
       ca.full_tiles = (int32_t*)(b + L.full_tiles);
       ca.sk1 = (int32_t*)(b + L.sk1);
       ca.sk4 = (int32_t*)(b + L.sk4);
@@ -156,14 +160,9 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       }
       g.list = (const int32_t*)(b + L.sk1);
       g.list4 = (const int32_t*)(b + L.sk4);
-      {
-        // parts of 16 rows: one group of <= 16 rows an expert, and of the
-        // others at least 17 rows for each four parts; beside tiles only the
-        // experts of fewer than ncu tiles x columns, sixteen parts each
-        int64_t parts = P / 4;
-        if (tiles) parts = std::min<int64_t>(parts, 16 * (l.ncu / (l.F / 128) + 1));
-        g.max_groups = (int)std::min<int64_t>(P, n_exp + parts);
-      }
+      // parts of 16 rows: one group of <= 16 rows an expert, and of the
+      // others (none beside tiles) at least 17 rows for each four parts
+      g.max_groups = (int)std::min<int64_t>(P, n_exp + (tiles ? 0 : P / 4));
       return launch_f8_stream(g, s);
     case 3: case 5:
       if (!tiles) return hipSuccess;

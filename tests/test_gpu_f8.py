@@ -237,6 +237,16 @@ def test_layer_skewed_and_clamped():
     _check(wl, ws, torch.float32)
 
 
+@pytest.mark.parametrize("T,E,k", [(200, 64, 1), (1024, 80, 1), (90, 128, 8), (1030, 128, 1)])
+def test_layer_few_pairs_an_expert(T, E, k):
+    """Few pairs an expert, most of them one expert's: streams alone up to
+    1024 tokens (groups of 64 rows and a rest), tiles above."""
+    bias = torch.zeros(E)
+    bias[5] = 6.0
+    wl, ws = _layer(T, 256, 128, E, k, "bf16", 0, 0.0, seed=T, bias=bias)
+    _check(wl, ws, torch.bfloat16)
+
+
 def test_layer_determinism_and_noalloc():
     wl, ws = _layer(33, 256, 256, 8, 2, "bf16", 1, seed=3)
     p, y = _run(wl, ws, torch.float32)
