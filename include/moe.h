@@ -509,9 +509,9 @@ moe_status moe_norm_backward(const moe_norm_desc *desc,
  * (moe_forward); 7 router kernel, 8 plan, 9 routing statistics
  * (moe_route); 10 recompute, 11 data gradients, 12 weight gradients,
  * 13 routing-weight gradients (moe_backward). On 8-bit weights: 1 x's rows
- * quantised, 2 / 4 the products on tiles, 3 / 5 those of thin groups and
- * decode-shaped calls, 0 and 6 as above (a step that a call does without
- * takes no time). Synchronises on the recorded events. reset != 0 clears afterwards. */
+ * quantised and the groups listed, 2 / 4 the products on tiles, 3 / 5 those of
+ * thin groups and decode-shaped calls, 6 as above (a step that a call does
+ * without takes no time). Synchronises on the recorded events. reset != 0 clears afterwards. */
 #define MOE_N_PHASES 16
 moe_status moe_phase_times(double *ms, int32_t n, int64_t *calls,
                            int32_t reset);

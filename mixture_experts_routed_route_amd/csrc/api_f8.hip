@@ -28,8 +28,8 @@ constexpr int kF8MaxK = 1 << 22;
 
 // The layer's workspace: quantised x, the SwiGLU outputs, the pairs' unweighted outputs, the work lists.
 struct F8Layout {
-  size_t x8, xs, h8, hs, y, full_tiles, sk1, sk4, fat_slot, fat_list, meta, bytes;
-  int cap_tiles, cap_sk1, cap_sk4;
+  size_t x8, xs, h8, hs, y, tiles, parts, meta, bytes;
+  int cap_tiles, cap_parts;
 };
 
 F8Layout f8_layout(const moe_plan_desc& d, int D, int F) {
@@ -37,8 +37,7 @@ F8Layout f8_layout(const moe_plan_desc& d, int D, int F) {
   const size_t P = (size_t)d.T * d.k + (size_t)d.n_shared * d.T;
   const int n_exp = d.E + d.n_shared;
   L.cap_tiles = n_exp + (int)(P / kFullBM) + 1;
-  L.cap_sk1 = n_exp;
-  L.cap_sk4 = n_exp + (int)(P / kSkRows) + 1;
+  L.cap_parts = (int)std::min<size_t>(P, n_exp + P / 16);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   L.x8 = take((size_t)d.T * D);
@@ -48,12 +47,9 @@ F8Layout f8_layout(const moe_plan_desc& d, int D, int F) {
   L.hs = take(P * (F / 128) * 4);
   // f32: a rounding of every pair to f16 would weigh as much as y's own
   L.y = take(P * D * 4);
-  L.full_tiles = take((size_t)L.cap_tiles * 8);
-  L.sk1 = take((size_t)L.cap_sk1 * 16);
-  L.sk4 = take((size_t)L.cap_sk4 * 16);
-  L.fat_slot = take((size_t)n_exp * 4);
-  L.fat_list = take((size_t)n_exp * 4);
-  L.meta = take(kMetaCount * 4);
+  L.tiles = take((size_t)L.cap_tiles * 8);
+  L.parts = take((size_t)L.cap_parts * 16);
+  L.meta = take(kF8MetaCount * 4);
   L.bytes = o;
   return L;
 }
@@ -80,10 +76,10 @@ constexpr int kF8TilePairs = 16, kF8TileAll = 256;
 // Above so many tokens always: one expert may hold them all.
 constexpr int kF8StreamT = 1024;
 
-// 0 quantise x, 1 classify, 2 gate/up of thin groups, 3 gate/up tile, 4 down
-// of thin groups, 5 down tile, 6 combine
+// 0 quantise x and list the groups, 1 gate/up of thin groups, 2 gate/up tile,
+// 3 down of thin groups, 4 down tile, 5 combine
 int moe::f8_step_phase(int step) {
-  static const int ph[kF8Steps] = {1, 0, 3, 2, 5, 4, 6};
+  static const int ph[kF8Steps] = {1, 3, 2, 5, 4, 6};
   return ph[step];
 }
 
@@ -98,11 +94,11 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   const bool raw = p.decode && f8_strip_raw_fits(d.T, std::max(l.D, l.F));
   const bool tiles = d.T > kF8StreamT ||
       (d.T > kF8StreamRows && P >= (int64_t)kF8TilePairs * n_exp && P > kF8TileAll);
-  const bool down = step >= 4;
+  const bool down = step >= 3;
   // one token: two launches, the second with the pairs' sum
   if (d.T == 1 && !(l.o.flags & MOE_OPT_TILED_DECODE) &&
       f8_one_fits(l.D, l.F, d.k, d.n_shared)) {
-    if (step != 2 && step != 4) return hipSuccess;
+    if (step != 1 && step != 3) return hipSuccess;
     const F8OneArgs one{l.x, l.xdt, (const uint8_t*)l.wg, (const uint8_t*)l.wu,
                         (const uint8_t*)l.wd, l.wgs, l.wus, l.wds, p.ids, p.tok2pair,
                         p.offsets, p.w, (float*)(b + L.h8), l.y, l.ydt, l.D, l.F, d.k,
@@ -121,53 +117,38 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
   g.offsets = p.offsets;
   g.clamp = l.o.swiglu_limit;
   g.odt = MOE_F32;
-  g.meta = raw ? p.dmeta : (const int32_t*)(b + L.meta);
   g.adt = MOE_F8B128;
   g.A = (const uint8_t*)(b + (down ? L.h8 : L.x8));
   g.As = (const float*)(b + (down ? L.hs : L.xs));
   g.out = b + (down ? L.y : L.h8);
   g.out_s = (float*)(b + L.hs);
   switch (step) {
-    case 0:
+    case 0: {
       if (raw) return hipSuccess;
-      return launch_quant_rows(l.x, l.xdt, d.T, l.D, b + L.x8, (float*)(b + L.xs), s);
-    case 1: {
-      if (raw) return hipSuccess;
-      ClassifyArgs ca{};
-      ca.counts = p.counts;
-      ca.n_exp = n_exp;
-      ca.mode = 1;
-      ca.S = tiles ? kF8StreamRows : 1e30;
-      ca.full_tiles = (int32_t*)(b + L.full_tiles);
-      ca.sk1 = (int32_t*)(b + L.sk1);
-      ca.sk4 = (int32_t*)(b + L.sk4);
-      ca.offsets = p.offsets;
-      ca.pair_token = p.pair_token;
-      ca.fat_slot = (int32_t*)(b + L.fat_slot);
-      ca.fat_list = (int32_t*)(b + L.fat_list);
-      ca.meta = (int32_t*)(b + L.meta);
-      return launch_classify(ca, s);
+      return launch_f8_prepare({l.x, l.xdt, d.T, l.D, (uint8_t*)(b + L.x8), (float*)(b + L.xs),
+                                p.counts, p.offsets, n_exp, tiles ? kF8StreamRows : d.T,
+                                (int32_t*)(b + L.parts), (int32_t*)(b + L.tiles),
+                                (int32_t*)(b + L.meta)}, s);
     }
-    case 2: case 4:
+    case 1: case 3:
       if (raw) {
         g.A = (const uint8_t*)(down ? b + L.h8 : l.x);
         g.adt = down ? MOE_F32 : l.xdt;
         g.lds_rows = d.T;
         g.list = p.dlist;
-        g.meta_index = kMetaSk1;
+        g.groups = p.dmeta + kMetaSk1;
         g.max_groups = (int)std::min<int64_t>(n_exp, P);
         return launch_f8_strip(g, l.ncu, s);
       }
-      g.list = (const int32_t*)(b + L.sk1);
-      g.list4 = (const int32_t*)(b + L.sk4);
-      // parts of 16 rows: one group of <= 16 rows an expert, and of the
-      // others (none beside tiles) at least 17 rows for each four parts
-      g.max_groups = (int)std::min<int64_t>(P, n_exp + (tiles ? 0 : P / 4));
+      g.list = (const int32_t*)(b + L.parts);
+      g.groups = (const int32_t*)(b + L.meta) + kF8Parts;
+      // beside tiles an expert has one part at most
+      g.max_groups = tiles ? (int)std::min<int64_t>(P, n_exp) : L.cap_parts;
       return launch_f8_stream(g, s);
-    case 3: case 5:
+    case 2: case 4:
       if (!tiles) return hipSuccess;
-      g.list = (const int32_t*)(b + L.full_tiles);
-      g.meta_index = kMetaFullTiles;
+      g.list = (const int32_t*)(b + L.tiles);
+      g.groups = (const int32_t*)(b + L.meta) + kF8Tiles;
       g.max_groups = L.cap_tiles;
       // an f16 layer's gate/up sums stay exact: a code of h that moves by a
       // step weighs more than f16's rounding of y

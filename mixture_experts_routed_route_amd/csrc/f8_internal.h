@@ -17,6 +17,19 @@ hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
 hipError_t launch_quant_weights(const void* w, int dt, int64_t mats, int N,
                                 int K, void* q, float* s, hipStream_t st);
 
+// A layer's first launch: x's rows quantised, the plan's groups listed.
+enum F8Meta : int32_t { kF8Parts = 0, kF8Tiles = 1, kF8MetaCount = 2 };
+struct F8PrepareArgs {
+  const void* x; int xdt; int T, D;
+  uint8_t* q; float* s;
+  const int32_t* counts; const int32_t* offsets; int n_exp;
+  int thin_rows;            // experts of up to so many rows: parts
+  int32_t* parts;           // (expert, row0, rows <= 16, first pair)
+  int32_t* tiles;           // (expert, row0) tiles of kFullBM rows
+  int32_t* meta;            // [kF8MetaCount] their numbers
+};
+hipError_t launch_f8_prepare(const F8PrepareArgs& a, hipStream_t st);
+
 // One product on e4m3 rows: out[row, n] = sum_b As[row, b] Bs[n / 128, b]
 // sum_{k in block b} A[row, k] B[n, k].
 struct F8Args {
@@ -35,9 +48,10 @@ struct F8Args {
   const uint8_t* B1; const float* B1s;   // gate/up: W_up
   const int32_t* pair_token;
   const int32_t* offsets;   // [n_exp + 1]
-  const int32_t* list;      // strip: (expert, row0, rows, first pair) groups
-  const int32_t* list4;     // stream: the groups of 17..64 rows (list: <= 16)
-  const int32_t* meta; int meta_index;
+  const int32_t* list;      // strip and stream: (expert, row0, rows, first
+                            // pair) groups of at most 16 rows; tile: (expert,
+                            // row0)
+  const int32_t* groups;    // device: the list's length
   int max_groups;           // most groups the list can hold
   void* out; int odt;       // plain and down: [rows, N]; gate/up: strip f32
                             // [P, N], stream and tile codes [P, N] ...
@@ -45,8 +59,7 @@ struct F8Args {
   float clamp;
 };
 hipError_t launch_f8_strip(const F8Args& a, int ncu, hipStream_t s);
-// modes 1 and 2 over both lists of a plan's thin groups; max_groups counts
-// the groups of <= 16 rows and four parts for each of the others
+// modes 1 and 2 over a plan's parts
 hipError_t launch_f8_stream(const F8Args& a, hipStream_t s);
 // whether strips may take groups of `rows` rows of K values unquantised
 bool f8_strip_raw_fits(int rows, int K);
@@ -93,7 +106,7 @@ struct F8Layer {
 };
 size_t f8_layer_bytes(const moe_plan_desc& d, int D, int F);
 // steps of the layer in order; `phase` is the index moe_phase_times reports
-constexpr int kF8Steps = 7;
+constexpr int kF8Steps = 6;
 int f8_step_phase(int step);
 hipError_t launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipStream_t s);
 

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
   const int kw = wave & (ks - 1);          // this wave's share of K
   const int strips = (N + 15) / 16;
   const int sblocks = (strips + spw - 1) / spw;
-  const int64_t groups = MODE == 0 ? (a.M + 16 * RB - 1) / (16 * RB) : a.meta[a.meta_index];
+  const int64_t groups = MODE == 0 ? (a.M + 16 * RB - 1) / (16 * RB) : *a.groups;
   const int64_t items = groups * sblocks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t gi = it / sblocks;
@@ -195,15 +195,11 @@ __global__ __launch_bounds__(512, 4) void f8_stream_kernel(F8Args a, int ks) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int K = a.K, N = a.N, nkb = K / 128, nnb = N / 128;
-  // items: groups of 17..64 rows in four parts of 16, then those of <= 16
-  const int n4 = a.meta[kMetaSk4] * 4, n1 = a.meta[kMetaSk1];
   const uint32_t item = wide_block();
   const int gi = item / (uint32_t)nnb, cb = item - gi * (uint32_t)nnb;
-  if (gi >= n4 + n1) return;
-  const int32_t* g = gi < n4 ? a.list4 + 4 * (gi >> 2) : a.list + 4 * (gi - n4);
-  const int part = gi < n4 ? (gi & 3) * 16 : 0;
-  const int e = g[0], rows = min(16, g[2] - part), row0 = g[3] + part;
-  if (rows <= 0) return;   // the whole workgroup, before any barrier
+  if (gi >= *a.groups) return;   // the whole workgroup, before any barrier
+  const int32_t* g = a.list + 4 * (size_t)gi;
+  const int e = g[0], rows = g[2], row0 = g[3];
   const int kw = wave & (ks - 1), ws = wave / ks, sw = 8 / ks;
   const int nch = (nkb + ks * NX - 1) / (ks * NX);   // chunks of K a strip
   const int steps = ks * nch;                        // ks batches of sw strips

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
     const int m = blockIdx.x >> 3;
     ti = m / NNB * 8 + (blockIdx.x & 7);
     nb = m % NNB;
-    if (ti >= a.meta[a.meta_index]) return;
+    if (ti >= *a.groups) return;
   }
   int e = 0, rows;
   int64_t row0;
