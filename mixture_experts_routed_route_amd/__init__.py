@@ -481,12 +481,13 @@ def _check_weight_shapes(plan, w_gate, w_up, w_down, D: int, F: int):
         N, K = want[name]
         if _is_f8(w):
             data, scales = w
-            if data.dim() != 3 or tuple(data.shape[1:]) != (N, K):
+            shape = data.shape
+            if shape != (shape[0], N, K):
                 raise ValueError(f"{name} codes must be [n, {N}, {K}], "
-                                 f"got {tuple(data.shape)}")
-            if tuple(scales.shape) != (data.shape[0], _blocks(N), _blocks(K)):
+                                 f"got {tuple(shape)}")
+            if scales.shape != (shape[0], _blocks(N), _blocks(K)):
                 raise ValueError(f"{name} scales {tuple(scales.shape)} do not "
-                                 f"match its codes {tuple(data.shape)}")
+                                 f"match its codes {tuple(shape)}")
             f = data.dtype
         elif isinstance(w, (tuple, list)):
             data, params = w
@@ -534,27 +535,27 @@ def moe_forward(plan: Plan, x: torch.Tensor, w_gate, w_up, w_down,
     if Dw != D:
         raise ValueError(f"weights have d_model {Dw}, x has {D}")
     _check_weight_shapes(plan, w_gate, w_up, w_down, D, F)
-    o = options or moe_options_default()
-    wg, keep_g = _weight(w_gate, x.device)
-    wu, keep_u = _weight(w_up, x.device)
-    wd, keep_d = _weight(w_down, x.device)
+    o = ctypes.byref(options or moe_options_default())
+    dev = x.device
+    wg, keep_g = _weight(w_gate, dev)
+    wu, keep_u = _weight(w_up, dev)
+    wd, keep_d = _weight(w_down, dev)
     xdt = _TORCH_TO_MOE[x.dtype]
-    nbytes = L.moe_forward_workspace_bytes(plan.handle, D, F, xdt, wg.dtype,
-                                           ctypes.byref(o))
+    nbytes = L.moe_forward_workspace_bytes(plan.handle, D, F, xdt, wg.dtype, o)
     if nbytes == 0:
         raise MoeError(MOE_EUNSUPPORTED, moe_last_error())
     if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        nbytes = workspace.numel()
     if out is None:
-        out = torch.empty(T, D, dtype=y_dtype, device=x.device)
+        out = torch.empty(T, D, dtype=y_dtype, device=dev)
     if out.dtype not in (torch.float32, x.dtype) or out.shape != (T, D) \
             or not out.is_contiguous():
         raise ValueError("out must be a contiguous [T, D] f32 or x-dtype tensor")
     _check(L.moe_forward(plan.handle, x.data_ptr(), xdt, wg, wu, wd, D, F,
                          out.data_ptr(), _TORCH_TO_MOE[out.dtype],
-                         workspace.data_ptr(),
-                         workspace.numel(), ctypes.byref(o),
-                         _stream(x.device)))
+                         workspace.data_ptr(), nbytes, o, _stream(dev)))
     return out
 
 
