@@ -168,38 +168,107 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
 // dw, dp and a channel gate's dg in registers; it writes them once,
 // [3][grid][D], and a second launch adds the workgroups' partials in order
 // (no atomics: the same bits from run to run).
+// Every load and store of the walk is a buffer instruction that is always
+// there: what a type, a missing tensor, a short row or a row past the last
+// leaves out lies past its buffer's end (loads give 0, stores write nothing).
+// One counter orders loads and stores, and with branches between them the
+// wait for a row's loads would cover the stores of the row before.
 // LP: the parameters in LDS; rows of more than 8192 values read them again
-// for every row.
+// for every row (and have no registers for the next row's loads).
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+constexpr int kPastEnd = (int)0x80000000u;
+
+// eight values, f32 or 16-bit, as loaded
+struct Wide8 { u32x4 a, b; };
+
+__device__ __forceinline__ void wide_to_f32(const Wide8& w, int dt, float (&v)[8]) {
+  if (dt == MOE_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(w.a[i]);
+      v[4 + i] = __uint_as_float(w.b[i]);
+    }
+  } else if (dt == MOE_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w.a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w.a[i] & 0xFFFF0000u);
+    }
+  } else {
+    const half8 h = __builtin_bit_cast(half8, w.a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+  }
+}
+
+__device__ __forceinline__ Wide8 wide_from_f32(const float (&v)[8], int dt) {
+  Wide8 w;
+  if (dt == MOE_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w.a[i] = __float_as_uint(v[i]);
+      w.b[i] = __float_as_uint(v[4 + i]);
+    }
+  } else if (dt == MOE_BF16) {
+    bf16x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = (__bf16)v[i];
+    w.a = w.b = __builtin_bit_cast(u32x4, o);
+  } else {
+    half8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = (_Float16)v[i];
+    w.a = w.b = __builtin_bit_cast(u32x4, o);
+  }
+  return w;
+}
+
 template <int TPR, int R, int NV, bool LP>
 __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_backward_kernel(NormBwdArgs a) {
   constexpr int W = TPR / 64;   // waves a row
-  extern __shared__ __attribute__((aligned(16))) float par[];   // [3][cols]: w, p, g
+  extern __shared__ __attribute__((aligned(16))) float par[];   // [3][cols]: w, p, alpha p g
   __shared__ float sh[2][R][6 * W];
   __shared__ float fold[R > 1 ? (R - 1) * TPR * 8 : 1];
   constexpr int cols = TPR * NV * 8;
   const int t = threadIdx.x % TPR;
-  const int sub = threadIdx.x / TPR;
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);   // whole waves
   const float invD = 1.f / (float)a.D;
   const bool gate_ch = a.g && !a.gate_token;
-  // eight of the parameters k (0 w, 1 p, 2 a channel gate) from channel c;
-  // ones where there is none
+  const uint32_t u_values = a.u ? (uint32_t)a.D : 0u, w_values = a.w ? (uint32_t)a.D : 0u;
+  // eight of the parameters k (0 w, 1 p, 2 alpha times a channel gate) from
+  // channel c; ones where there is none, zeros past the row
   auto read_params = [&](int k, int c, float (&v)[8]) {
     const void* src = k == 0 ? a.w : k == 1 ? a.p : gate_ch ? a.g : nullptr;
     const int dt = k == 2 ? a.gdt : a.wdt;
-    if (src) raw8_to_f32(load_raw8(src, dt, c), dt, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = !src ? 1.f : k == 2 ? v[j] : param(v[j], a.unit);
+    for (int j = 0; j < 8; ++j) v[j] = c < a.D ? 1.f : 0.f;
+    if (src && c < a.D) {
+      raw8_to_f32(load_raw8(src, dt, c), dt, v);
+      if (k != 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = param(v[j], a.unit);
+      }
+    }
+    if (k == 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= a.alpha;
+    }
   };
-  auto params = [&](int k, int c, float (&v)[8]) {
+  // parameters h .. h + 3 of a thread's eight: four at a time, the loops over
+  // halves kept apart, so that no more of them take registers
+  auto params = [&](int k, int c, int h, float (&v)[4]) {
     if (LP) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = par[k * cols + c + j];
+      for (int j = 0; j < 4; ++j) v[j] = par[k * cols + c + h + j];
     } else {
-      read_params(k, c, v);
+      float w[8];
+      read_params(k, c, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = w[h + j];
     }
   };
   if (LP) {
-    for (int c = threadIdx.x * 8; c < a.D; c += TPR * R * 8) {
+    for (int c = threadIdx.x * 8; c < cols; c += TPR * R * 8) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         float v[8];
@@ -214,64 +283,87 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = dp[i][j] = dg[i][j] = 0.f;
-  struct Row { Raw8 r[NV], x[NV], u[NV], e[NV]; };
+  // a row of a tensor of `values` values a row (0: none)
+  auto row_of = [&](const void* p, int dt, int64_t row, uint32_t values) {
+    const int sz = dt == MOE_F32 ? 4 : 2;
+    const bool live = row < a.T;
+    return make_rsrc(static_cast<const char*>(p) + (size_t)(live ? row : 0) * a.D * sz,
+                     live ? values * sz : 0u);
+  };
+  auto load8 = [&](__amdgpu_buffer_rsrc_t rs, int dt, int i) {
+    const int off = (i * TPR + t) * (dt == MOE_F32 ? 32 : 16);
+    Wide8 w;
+    w.a = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+    w.b = __builtin_amdgcn_raw_buffer_load_b128(rs, dt == MOE_F32 ? off + 16 : kPastEnd, 0, 0);
+    return w;
+  };
+  auto put8 = [&](__amdgpu_buffer_rsrc_t rs, int dt, int i, const float (&v)[8]) {
+    const int off = (i * TPR + t) * (dt == MOE_F32 ? 32 : 16);
+    const Wide8 w = wide_from_f32(v, dt);
+    __builtin_amdgcn_raw_buffer_store_b128(w.a, rs, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(w.b, rs, dt == MOE_F32 ? off + 16 : kPastEnd, 0, 0);
+  };
+  struct Row { Wide8 r[NV], x[NV], u[NV], e[NV]; uint32_t g32, g16; };
+  const uint32_t gate_sz = !a.g || !a.gate_token ? 0u : a.gdt == MOE_F32 ? 4u : 2u;
   auto load_row = [&](Row& q, int64_t row) {
-    const size_t base = (size_t)min(row, (int64_t)a.T - 1) * a.D;
+    const bool live = row < a.T;
+    const __amdgpu_buffer_rsrc_t rg =
+        make_rsrc(static_cast<const char*>(a.g) + (size_t)(live ? row : 0) * gate_sz,
+                  live ? gate_sz : 0u);
+    q.g32 = __builtin_amdgcn_raw_buffer_load_b32(rg, 0, 0, 0);
+    q.g16 = __builtin_amdgcn_raw_buffer_load_b16(rg, 0, 0, 0);
+    const __amdgpu_buffer_rsrc_t rr = row_of(a.r, a.rdt, row, w_values);
+    const __amdgpu_buffer_rsrc_t rx = row_of(a.dx, a.dxdt, row, w_values);
+    const __amdgpu_buffer_rsrc_t ru = row_of(a.u, a.udt, row, u_values);
+    const __amdgpu_buffer_rsrc_t re = row_of(a.dr, a.rdt, row, a.dr ? (uint32_t)a.D : 0u);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * 8;
-      if (c < a.D) {
-        if (a.w) {
-          q.r[i] = load_raw8(a.r, a.rdt, base + c);
-          q.x[i] = load_raw8(a.dx, a.dxdt, base + c);
-        }
-        if (a.u) q.u[i] = load_raw8(a.u, a.udt, base + c);
-        if (a.dr) q.e[i] = load_raw8(a.dr, a.rdt, base + c);
-      }
+      q.r[i] = load8(rr, a.rdt, i);
+      q.x[i] = load8(rx, a.dxdt, i);
+      q.u[i] = load8(ru, a.udt, i);
+      q.e[i] = load8(re, a.rdt, i);
     }
   };
   // the same number of turns for every row group: the sums hold barriers
   const int64_t step = (int64_t)gridDim.x * R;
   const int64_t first = (int64_t)blockIdx.x * R;
   Row q;
-  if (first < a.T) load_row(q, first + sub);
+  load_row(q, first + sub);
   __syncthreads();   // the parameters
   int turn = 0;
   for (int64_t row0 = first; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub;
     const bool live = row < a.T;
-    const size_t base = (size_t)min(row, (int64_t)a.T - 1) * a.D;
+    if (!LP && row0 != first) load_row(q, row);
     float r[NV][8], dx[NV][8], u[NV][8], d[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] = dx[i][j] = u[i][j] = d[i][j] = 0.f;
-      if (c < a.D) {
-        if (a.w) {
-          raw8_to_f32(q.r[i], a.rdt, r[i]);
-          raw8_to_f32(q.x[i], a.dxdt, dx[i]);
-        }
-        if (a.u) raw8_to_f32(q.u[i], a.udt, u[i]);
-        if (a.dr) raw8_to_f32(q.e[i], a.rdt, d[i]);
-      }
+      wide_to_f32(q.r[i], a.rdt, r[i]);
+      wide_to_f32(q.x[i], a.dxdt, dx[i]);
+      wide_to_f32(q.u[i], a.udt, u[i]);
+      wide_to_f32(q.e[i], a.rdt, d[i]);
     }
-    if (row0 + step < a.T) load_row(q, row0 + step + sub);
-    float gt = 1.f;
-    if (a.g && a.gate_token) gt = load_one(a.g, a.gdt, min(row, (int64_t)a.T - 1));
+    float gt = 1.f;   // a token's gate
+    if (gate_sz) {
+      gt = a.gdt == MOE_F32 ? __uint_as_float(q.g32)
+         : a.gdt == MOE_BF16 ? __uint_as_float(q.g16 << 16)
+                             : (float)__builtin_bit_cast(_Float16, (uint16_t)q.g16);
+    }
+    if (LP) load_row(q, row0 + step + sub);
     float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // r'^2, t r', u^2, a u (dr', t, r')
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + t) * 8;
-      if (c < a.D) {
-        float wv[8], pv[8], gv[8];
-        params(0, c, wv);
-        params(1, c, pv);
-        params(2, c, gv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float tt = dx[i][j] * wv[j];
-          const float au = a.alpha * gv[j] * pv[j] * u[i][j];
+      for (int h = 0; h < 8; h += 4) {
+        float wv[4], pv[4], gv[4];
+        params(0, c, h, wv);
+        params(1, c, h, pv);
+        params(2, c, h, gv);
+#pragma unroll
+        for (int j = h; j < h + 4; ++j) {
+          const float tt = dx[i][j] * wv[j - h];
+          const float au = gv[j - h] * pv[j - h] * u[i][j];
           sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
           sum[1] = fmaf(tt, r[i][j], sum[1]);
           sum[2] = fmaf(u[i][j], u[i][j], sum[2]);
@@ -279,6 +371,7 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
           sum[4] = fmaf(au, tt, sum[4]);
           sum[5] = fmaf(au, r[i][j], sum[5]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     // the halves of sh take turns: a row's reads lie between its barrier and
@@ -290,38 +383,44 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
     const float inv_u = a.p ? rsqrtf(sum[2] * invD + a.eps) : 1.f;
     const float aud = a.w ? sum[3] + inv * (sum[4] - m * sum[5]) : sum[3];
     const float mp = gt * inv_u * aud * invD;
-    if (a.dg_token && t == 0 && live) a.dg_token[row] = inv_u * aud;
-    if (!live) continue;   // past its barrier
+    __builtin_amdgcn_raw_buffer_store_b32(
+        __float_as_uint(inv_u * aud),
+        make_rsrc(a.dg_token + (live ? row : 0), live && a.dg_token ? 4u : 0u),
+        t == 0 ? 0 : kPastEnd, 0, 0);
+    const __amdgpu_buffer_rsrc_t rd = row_of(a.dr_out, a.rdt, row, (uint32_t)a.D);
+    const __amdgpu_buffer_rsrc_t ru = row_of(a.du, a.udt, row, u_values);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + t) * 8;
-      if (c < a.D) {
-        if (a.w) {
-          float wv[8];
-          params(0, c, wv);
+      float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            dw[i][j] = fmaf(dx[i][j], r[i][j] * inv, dw[i][j]);
-            d[i][j] += inv * (dx[i][j] * wv[j] - r[i][j] * m);
+      for (int h = 0; h < 8; h += 4) {
+        float wv[4], pv[4], gv[4];
+        params(0, c, h, wv);
+        params(1, c, h, pv);
+        params(2, c, h, gv);
+        // the zeros of a row past the last may have an infinite inverse norm
+        if (live) {
+          if (a.w) {
+#pragma unroll
+            for (int j = h; j < h + 4; ++j) {
+              dw[i][j] = fmaf(dx[i][j], r[i][j] * inv, dw[i][j]);
+              d[i][j] += inv * (dx[i][j] * wv[j - h] - r[i][j] * m);
+            }
           }
-        }
-        store8(a.dr_out, a.rdt, base + c, d[i]);
-        if (a.u) {
-          float o[8], pv[8], gv[8];
-          params(1, c, pv);
-          params(2, c, gv);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = u[i][j] * inv_u, ad = a.alpha * d[i][j];
-            const float pj = pv[j], gj = gv[j];
-            dg[i][j] = fmaf(ad, v * pj, dg[i][j]);
-            const float dz = gt * ad * gj;
+          for (int j = h; j < h + 4; ++j) {
+            const float v = u[i][j] * inv_u;
+            dg[i][j] = fmaf(a.alpha * d[i][j], v * pv[j - h], dg[i][j]);
+            const float dz = gt * gv[j - h] * d[i][j];
             dp[i][j] = fmaf(dz, v, dp[i][j]);
-            o[j] = a.p ? inv_u * (dz * pj - v * mp) : dz;
+            o[j] = a.p ? inv_u * (dz * pv[j - h] - v * mp) : dz;
           }
-          store8(a.du, a.udt, base + c, o);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      put8(rd, a.rdt, i, d[i]);
+      put8(ru, a.udt, i, o);
     }
   }
   // the workgroup's partials: its row groups' sums in order, then one slot
