@@ -479,11 +479,10 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(
 namespace {
 
 // Workgroups of the backward, each leaving one slot of partials: as many as
-// the compute units hold at once, two each (four of the 256-thread ones would
-// fit, with twice the partials), one of the widest rows.
+// the compute units hold at once, two of 256 threads or one of 512.
 int bwd_slots(int T, int D) {
-  const int rows = D <= 512 ? 4 : D <= 2048 ? 2 : 1;
-  const int most = D <= 4096 ? 512 : 256;
+  const int rows = D <= 2048 ? 4 : D <= 4096 ? 2 : 1;
+  const int most = D <= 1024 ? 512 : 256;
   return (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + rows - 1) / rows, most));
 }
 
@@ -499,10 +498,14 @@ static void run_norm_backward(const NormBwdArgs& a, int grid, hipStream_t s) {
 
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s) {
   const int slots = bwd_slots(a.T, a.D);
+  // 16 values a thread where a row has 64 threads for them: fewer threads
+  // share a row's sums, with twice the loads in flight each. 8 a thread took
+  // 4096 x 2048 f32 in 51 us, not 48; 8192 x 1024 bf16 in 32, not 29; 8192 x
+  // 4096 bf16 in 104, not 99.
   if (a.D <= 512) run_norm_backward<64, 4, 1>(a, slots, s);
-  else if (a.D <= 1024) run_norm_backward<128, 2, 1>(a, slots, s);
-  else if (a.D <= 2048) run_norm_backward<256, 2, 1>(a, slots, s);
-  else if (a.D <= 4096) run_norm_backward<512, 1, 1>(a, slots, s);
+  else if (a.D <= 1024) run_norm_backward<64, 4, 2>(a, slots, s);
+  else if (a.D <= 2048) run_norm_backward<128, 4, 2>(a, slots, s);
+  else if (a.D <= 4096) run_norm_backward<256, 2, 2>(a, slots, s);
   else if (a.D <= 8192) run_norm_backward<512, 1, 2>(a, slots, s);
   else run_norm_backward<1024, 1, 2, false>(a, slots, s);
   hipError_t e = hipGetLastError();
