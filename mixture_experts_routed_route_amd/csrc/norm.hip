@@ -173,8 +173,10 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
 // leaves out lies past its buffer's end (loads give 0, stores write nothing).
 // One counter orders loads and stores, and with branches between them the
 // wait for a row's loads would cover the stores of the row before.
-// LP: the parameters in LDS; rows of more than 8192 values read them again
-// for every row (and have no registers for the next row's loads).
+// HELD: the parameters in LDS, a row in registers between its sums and the
+// rest. Rows of more than 8192 values have room in neither: they read the
+// parameters for every row, and the row again after its sums (4096 x
+// 16384 bf16 in 764 us, 1037 if held; either way the compiler spills).
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kPastEnd = (int)0x80000000u;
 
@@ -223,7 +225,7 @@ __device__ __forceinline__ Wide8 wide_from_f32(const float (&v)[8], int dt) {
   return w;
 }
 
-template <int TPR, int R, int NV, bool LP>
+template <int TPR, int R, int NV, bool HELD>
 __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_backward_kernel(NormBwdArgs a) {
   constexpr int W = TPR / 64;   // waves a row
   extern __shared__ __attribute__((aligned(16))) float par[];   // [3][cols]: w, p, alpha p g
@@ -257,7 +259,7 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
   // parameters h .. h + 3 of a thread's eight: four at a time, the loops over
   // halves kept apart, so that no more of them take registers
   auto params = [&](int k, int c, int h, float (&v)[4]) {
-    if (LP) {
+    if (HELD) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = par[k * cols + c + h + j];
     } else {
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
       for (int j = 0; j < 4; ++j) v[j] = w[h + j];
     }
   };
-  if (LP) {
+  if (HELD) {
     for (int c = threadIdx.x * 8; c < cols; c += TPR * R * 8) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
@@ -303,57 +305,71 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
     __builtin_amdgcn_raw_buffer_store_b128(w.a, rs, off, 0, 0);
     __builtin_amdgcn_raw_buffer_store_b128(w.b, rs, dt == MOE_F32 ? off + 16 : kPastEnd, 0, 0);
   };
-  struct Row { Wide8 r[NV], x[NV], u[NV], e[NV]; uint32_t g32, g16; };
+  constexpr int NH = HELD ? NV : 1;
+  struct Row { Wide8 r[NH], x[NH], u[NH], e[NH]; uint32_t g32, g16; };
   const uint32_t gate_sz = !a.g || !a.gate_token ? 0u : a.gdt == MOE_F32 ? 4u : 2u;
-  auto load_row = [&](Row& q, int64_t row) {
+  auto load_gate = [&](Row& q, int64_t row) {
     const bool live = row < a.T;
     const __amdgpu_buffer_rsrc_t rg =
         make_rsrc(static_cast<const char*>(a.g) + (size_t)(live ? row : 0) * gate_sz,
                   live ? gate_sz : 0u);
     q.g32 = __builtin_amdgcn_raw_buffer_load_b32(rg, 0, 0, 0);
     q.g16 = __builtin_amdgcn_raw_buffer_load_b16(rg, 0, 0, 0);
+  };
+  // pieces i0 .. i0 + NH - 1
+  auto load_row = [&](Row& q, int64_t row, int i0) {
     const __amdgpu_buffer_rsrc_t rr = row_of(a.r, a.rdt, row, w_values);
     const __amdgpu_buffer_rsrc_t rx = row_of(a.dx, a.dxdt, row, w_values);
     const __amdgpu_buffer_rsrc_t ru = row_of(a.u, a.udt, row, u_values);
     const __amdgpu_buffer_rsrc_t re = row_of(a.dr, a.rdt, row, a.dr ? (uint32_t)a.D : 0u);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      q.r[i] = load8(rr, a.rdt, i);
-      q.x[i] = load8(rx, a.dxdt, i);
-      q.u[i] = load8(ru, a.udt, i);
-      q.e[i] = load8(re, a.rdt, i);
+    for (int i = 0; i < NH; ++i) {
+      q.r[i] = load8(rr, a.rdt, i0 + i);
+      q.x[i] = load8(rx, a.dxdt, i0 + i);
+      q.u[i] = load8(ru, a.udt, i0 + i);
+      q.e[i] = load8(re, a.rdt, i0 + i);
     }
   };
   // the same number of turns for every row group: the sums hold barriers
   const int64_t step = (int64_t)gridDim.x * R;
   const int64_t first = (int64_t)blockIdx.x * R;
   Row q;
-  load_row(q, first + sub);
+  load_gate(q, first + sub);
+  if (HELD) load_row(q, first + sub, 0);
   __syncthreads();   // the parameters
   int turn = 0;
   for (int64_t row0 = first; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub;
     const bool live = row < a.T;
-    if (!LP && row0 != first) load_row(q, row);
-    float r[NV][8], dx[NV][8], u[NV][8], d[NV][8];
+    float r[NH][8], dx[NH][8], u[NH][8], d[NH][8];
+    auto widen_row = [&]() {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      wide_to_f32(q.r[i], a.rdt, r[i]);
-      wide_to_f32(q.x[i], a.dxdt, dx[i]);
-      wide_to_f32(q.u[i], a.udt, u[i]);
-      wide_to_f32(q.e[i], a.rdt, d[i]);
-    }
+      for (int i = 0; i < NH; ++i) {
+        wide_to_f32(q.r[i], a.rdt, r[i]);
+        wide_to_f32(q.x[i], a.dxdt, dx[i]);
+        wide_to_f32(q.u[i], a.udt, u[i]);
+        wide_to_f32(q.e[i], a.rdt, d[i]);
+      }
+    };
+    if (HELD) widen_row();
     float gt = 1.f;   // a token's gate
     if (gate_sz) {
       gt = a.gdt == MOE_F32 ? __uint_as_float(q.g32)
          : a.gdt == MOE_BF16 ? __uint_as_float(q.g16 << 16)
                              : (float)__builtin_bit_cast(_Float16, (uint16_t)q.g16);
     }
-    if (LP) load_row(q, row0 + step + sub);
+    load_gate(q, row0 + step + sub);
+    if (HELD) load_row(q, row0 + step + sub, 0);
     float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // r'^2, t r', u^2, a u (dr', t, r')
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * 8;
+      const int n = HELD ? i : 0;
+      int c = (i * TPR + t) * 8;
+      if (!HELD) {
+        asm volatile("" : "+v"(c));   // the parameters here, not before the walk
+        load_row(q, row, i);
+        widen_row();
+      }
 #pragma unroll
       for (int h = 0; h < 8; h += 4) {
         float wv[4], pv[4], gv[4];
@@ -362,14 +378,14 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
         params(2, c, h, gv);
 #pragma unroll
         for (int j = h; j < h + 4; ++j) {
-          const float tt = dx[i][j] * wv[j - h];
-          const float au = gv[j - h] * pv[j - h] * u[i][j];
-          sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
-          sum[1] = fmaf(tt, r[i][j], sum[1]);
-          sum[2] = fmaf(u[i][j], u[i][j], sum[2]);
-          sum[3] = fmaf(au, d[i][j], sum[3]);
+          const float tt = dx[n][j] * wv[j - h];
+          const float au = gv[j - h] * pv[j - h] * u[n][j];
+          sum[0] = fmaf(r[n][j], r[n][j], sum[0]);
+          sum[1] = fmaf(tt, r[n][j], sum[1]);
+          sum[2] = fmaf(u[n][j], u[n][j], sum[2]);
+          sum[3] = fmaf(au, d[n][j], sum[3]);
           sum[4] = fmaf(au, tt, sum[4]);
-          sum[5] = fmaf(au, r[i][j], sum[5]);
+          sum[5] = fmaf(au, r[n][j], sum[5]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -391,7 +407,13 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
     const __amdgpu_buffer_rsrc_t ru = row_of(a.du, a.udt, row, u_values);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * 8;
+      const int n = HELD ? i : 0;
+      int c = (i * TPR + t) * 8;
+      if (!HELD) {
+        asm volatile("" : "+v"(c));   // the parameters here, not before the walk
+        load_row(q, row, i);
+        widen_row();
+      }
       float o[8];
 #pragma unroll
       for (int h = 0; h < 8; h += 4) {
@@ -404,22 +426,22 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
           if (a.w) {
 #pragma unroll
             for (int j = h; j < h + 4; ++j) {
-              dw[i][j] = fmaf(dx[i][j], r[i][j] * inv, dw[i][j]);
-              d[i][j] += inv * (dx[i][j] * wv[j - h] - r[i][j] * m);
+              dw[i][j] = fmaf(dx[n][j], r[n][j] * inv, dw[i][j]);
+              d[n][j] += inv * (dx[n][j] * wv[j - h] - r[n][j] * m);
             }
           }
 #pragma unroll
           for (int j = h; j < h + 4; ++j) {
-            const float v = u[i][j] * inv_u;
-            dg[i][j] = fmaf(a.alpha * d[i][j], v * pv[j - h], dg[i][j]);
-            const float dz = gt * gv[j - h] * d[i][j];
+            const float v = u[n][j] * inv_u;
+            dg[i][j] = fmaf(a.alpha * d[n][j], v * pv[j - h], dg[i][j]);
+            const float dz = gt * gv[j - h] * d[n][j];
             dp[i][j] = fmaf(dz, v, dp[i][j]);
             o[j] = a.p ? inv_u * (dz * pv[j - h] - v * mp) : dz;
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      put8(rd, a.rdt, i, d[i]);
+      put8(rd, a.rdt, i, d[n]);
       put8(ru, a.udt, i, o);
     }
   }
@@ -490,10 +512,10 @@ int bwd_slots(int T, int D) {
 
 size_t norm_backward_part_floats(int T, int D) { return (size_t)3 * bwd_slots(T, D) * D; }
 
-template <int TPR, int R, int NV, bool LP = true>
+template <int TPR, int R, int NV, bool HELD = true>
 static void run_norm_backward(const NormBwdArgs& a, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((norm_backward_kernel<TPR, R, NV, LP>), dim3(grid), dim3(TPR * R),
-                     LP ? 3 * TPR * NV * 8 * sizeof(float) : 0, s, a);
+  hipLaunchKernelGGL((norm_backward_kernel<TPR, R, NV, HELD>), dim3(grid), dim3(TPR * R),
+                     HELD ? 3 * TPR * NV * 8 * sizeof(float) : 0, s, a);
 }
 
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s) {
