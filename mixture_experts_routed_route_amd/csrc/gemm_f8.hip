@@ -23,16 +23,20 @@ namespace moe {
 // up to 16 RB rows of one group, weight operands straight from memory to
 // registers (each weight code is used by one wave only). A workgroup of four
 // waves takes 4 / ks strips, ks waves sharing one's blocks of K, their partial
-// sums meeting in LDS: ks = 4 from 16 blocks on, 2 from 8, else 1, so that a
-// wave streams at least four blocks and short rows do not leave workgroups of
-// a few KB. A wave holds one block of loads at a time: the up to eight
-// workgroups of a CU cover one another's waits.
+// sums meeting in LDS: as many as leave each a block (from 16 blocks on only,
+// 64 x 512 . 4096 x 512 took 9.1 us, not 5.9; from 64 on, 8 x 4096 . 1024 x
+// 4096 12.1, not 7.9). A wave holds one block of loads at a time: the up to
+// eight workgroups of a CU cover one another's waits. One row of 2048 values
+// by 4096 takes 4.8 us (1.7 TB/s of weights: a chain of loads, not their
+// rate).
 //
 // SRC 0 (plain products) reads quantised rows. SRC 1 (decode-shaped plans)
 // reads the rows as they are (x in its type, or h in f32) and quantises the
 // group's into LDS first, every workgroup for itself: for so few rows this
 // costs less than a launch that quantises them once.
 constexpr int kStripLds = 32768;   // bytes of rows a workgroup may hold (SRC 1)
+
+__host__ __device__ constexpr int strip_share(int nkb) { return nkb >= 4 ? 4 : nkb >= 2 ? 2 : 1; }
 
 template <int MODE, int RB, int SRC>
 __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
@@ -44,7 +48,7 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
   const int lr = lane & 15, lq = lane >> 4;
   const int K = a.K, N = a.N;
   const int nkb = (K + 127) / 128, nnb = (N + 127) / 128;
-  const int ks = nkb >= 16 ? 4 : nkb >= 8 ? 2 : 1, spw = 4 / ks;
+  const int ks = strip_share(nkb), spw = 4 / ks;
   const int kw = wave & (ks - 1);          // this wave's share of K
   const int strips = (N + 15) / 16;
   const int sblocks = (strips + spw - 1) / spw;
@@ -342,10 +346,15 @@ static void run_strip(const F8Args& a, unsigned grid, hipStream_t s) {
 }
 
 hipError_t launch_f8_strip(const F8Args& a, int ncu, hipStream_t s) {
-  const int rb = a.mode == 0 && a.M > 16 ? 4 : 1;
-  const int64_t groups = a.mode == 0 ? (a.M + 16 * rb - 1) / (16 * rb) : a.max_groups;
-  const int nkb = (a.K + 127) / 128, spw = nkb >= 16 ? 1 : nkb >= 8 ? 2 : 4;
-  const int64_t items = groups * (((a.N + 15) / 16 + spw - 1) / spw);
+  const int spw = 4 / strip_share((a.K + 127) / 128);
+  const int64_t sblocks = ((a.N + 15) / 16 + spw - 1) / spw;
+  // 64 rows a workgroup once 16 would make four workgroups a CU: weights are
+  // read a fourth as often, by fewer waves (us with 64 / 16 rows: 64 rows by
+  // 4096 x 4096 17.6 / 22.0, by 2048 x 1024 7.5 / 5.8; 128 by 1001 x 1040 7.7
+  // / 5.7; 517 by 1001 x 1040 10.4 / 10.7)
+  const int64_t groups16 = a.mode == 0 ? (a.M + 15) / 16 : a.max_groups;
+  const int rb = a.mode == 0 && a.M > 16 && groups16 * sblocks >= 4 * ncu ? 4 : 1;
+  const int64_t items = (groups16 + rb - 1) / rb * sblocks;
   if (items == 0) return hipSuccess;
   const unsigned grid = (unsigned)std::min<int64_t>(items, (int64_t)ncu * 16);
   if (a.mode == 0 && rb == 1) run_strip<0, 1, 0>(a, grid, s);
