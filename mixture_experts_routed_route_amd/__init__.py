@@ -756,7 +756,7 @@ def moe_quant_f8(x: torch.Tensor) -> tuple:
     with _on(x.device):
         x = x.contiguous()
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        s = x.new_empty((*x.shape[:-1], _blocks(K)), dtype=torch.float32)
+        s = torch.empty(*x.shape[:-1], _blocks(K), dtype=torch.float32, device=x.device)
         _check(library().moe_quant_f8(x.data_ptr(), _TORCH_TO_MOE[x.dtype],
                                       x.numel() // K, K, q.data_ptr(),
                                       s.data_ptr(), _stream(x.device)))
@@ -780,7 +780,8 @@ def moe_quant_f8_weights(w: torch.Tensor) -> tuple:
     with _on(w.device):
         w = w.contiguous()
         q = torch.empty_like(w, dtype=torch.float8_e4m3fn)
-        s = w.new_empty((*w.shape[:-2], _blocks(N), _blocks(K)), dtype=torch.float32)
+        s = torch.empty(*w.shape[:-2], _blocks(N), _blocks(K), dtype=torch.float32,
+                        device=w.device)
         _check(library().moe_quant_f8_weights(w.data_ptr(), _TORCH_TO_MOE[w.dtype],
                                               mats, N, K, q.data_ptr(), s.data_ptr(),
                                               _stream(w.device)))
@@ -795,36 +796,38 @@ def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
     multiple of 16. The result has ``out``'s type, or ``out_dtype``
     (float32, bfloat16 or float16)."""
     (xq, xs), (wq, ws) = x, w
-    f8 = torch.float8_e4m3fn
-    if xq.dtype != f8 or wq.dtype != f8 or xs.dtype != torch.float32 or ws.dtype != torch.float32:
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if xq.dtype != f8 or wq.dtype != f8 or xs.dtype != f32 or ws.dtype != f32:
         raise ValueError("x and w are (float8_e4m3fn codes, float32 scales)")
-    if xq.dim() < 1 or xs.dim() < 1 or wq.dim() != 2 or xq.shape[-1] != wq.shape[1]:
-        raise ValueError(f"codes {tuple(xq.shape)} and {tuple(wq.shape)} must be "
+    xshape, wshape = xq.shape, wq.shape
+    if len(xshape) < 1 or len(wshape) != 2 or xshape[-1] != wshape[1]:
+        raise ValueError(f"codes {tuple(xshape)} and {tuple(wshape)} must be "
                          "[.., K] and [N, K]")
-    N, K = wq.shape
+    N, K = wshape
     if K < 16 or K % 16:
         raise ValueError(f"K={K} must be a positive multiple of 16")
     _c_int("K", K)
     _c_int("N", N)
-    if xs.shape[:-1] != xq.shape[:-1] or xs.shape[-1] != _blocks(K) \
-            or ws.shape != (_blocks(N), _blocks(K)):
+    lead, nb = xshape[:-1], _blocks(K)
+    if xs.shape != (*lead, nb) or ws.shape != (_blocks(N), nb):
         raise ValueError(f"scales {tuple(xs.shape)} and {tuple(ws.shape)} do not match "
-                         f"codes {tuple(xq.shape)} and {tuple(wq.shape)}")
+                         f"codes {tuple(xshape)} and {tuple(wshape)}")
     dev = xq.device
     if xs.device != dev or wq.device != dev or ws.device != dev:
         raise ValueError("x, w and their scales must be on one device")
-    shape = xq.shape[:-1] + (N,)
     with _on(dev):
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=dev)
-        if out.dtype not in _TORCH_TO_MOE or out.shape != shape \
-                or not out.is_contiguous() or out.device != dev:
-            raise ValueError(f"out must be a contiguous float32/bfloat16/float16 "
-                             f"{tuple(shape)} tensor on x's device")
+            # sizes one by one: a torch.Size costs 1.5 us more
+            out = torch.empty(*lead, N, dtype=out_dtype, device=dev)
+        elif out.shape != (*lead, N) or not out.is_contiguous() or out.device != dev:
+            raise ValueError(f"out must be a contiguous {(*lead, N)} tensor on x's device")
+        odt = _TORCH_TO_MOE.get(out.dtype)
+        if odt is None:
+            raise ValueError("the result is float32, bfloat16 or float16")
         xq, xs, wq, ws = xq.contiguous(), xs.contiguous(), wq.contiguous(), ws.contiguous()
         _check(library().moe_gemm_f8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(),
                                      ws.data_ptr(), xq.numel() // K, N, K, out.data_ptr(),
-                                     _TORCH_TO_MOE[out.dtype], _stream(dev)))
+                                     odt, _stream(dev)))
     return out
 
 
@@ -832,15 +835,16 @@ def _rows_like(t, like, name: str):
     if t.dtype not in _TORCH_TO_MOE or t.shape != like.shape or t.device != like.device:
         raise ValueError(f"{name} must be a float32/bfloat16/float16 tensor of shape "
                          f"{tuple(like.shape)} on the residual's device")
-    return t if t.is_contiguous() else t.contiguous()
+    return t.contiguous()
 
 
 def _norm_vec(v, D, like, dtype):
-    if v.dtype not in _TORCH_TO_MOE or (dtype is not None and v.dtype != dtype) \
-            or v.dim() != 1 or v.shape[0] != D or v.device != like.device:
+    dt = v.dtype
+    if dt not in _TORCH_TO_MOE or (dtype is not None and dt != dtype) \
+            or v.shape != (D,) or v.device != like.device:
         raise ValueError(f"weight and post_weight must be [{D}] tensors of one "
                          "type (float32/bfloat16/float16) on the residual's device")
-    return v if v.is_contiguous() else v.contiguous()
+    return v.contiguous()
 
 
 def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
@@ -852,8 +856,7 @@ def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
     if D < 8 or D % 8 or D > MOE_NORM_MAX_D:
         raise ValueError(f"D={D} must be a multiple of 8 in 8..{MOE_NORM_MAX_D}")
     _c_int("T", T)
-    if not residual.is_contiguous():
-        residual = residual.contiguous()
+    residual = residual.contiguous()
     udt = wdt = gdt = MOE_F32
     kind = MOE_GATE_NONE
     if block is None:
@@ -872,16 +875,15 @@ def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
                                 None if weight is None else weight.dtype)
         wdt = _TORCH_TO_MOE[post_weight.dtype]
     if gate is not None:
-        if gate.dim() == 1 and gate.shape[0] == D:
+        if gate.shape == (D,):
             kind = MOE_GATE_CHANNEL
-        elif gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] == 1:
+        elif gate.shape == (T, 1):
             kind = MOE_GATE_TOKEN
         if kind == MOE_GATE_NONE or gate.dtype not in _TORCH_TO_MOE \
                 or gate.device != residual.device:
             raise ValueError(f"gate must be [{D}] (per channel) or [{T}, 1] (per token), "
                              "float32/bfloat16/float16, on the residual's device")
-        if not gate.is_contiguous():
-            gate = gate.contiguous()
+        gate = gate.contiguous()
         gdt = _TORCH_TO_MOE[gate.dtype]
     d = NormDesc(T, D, _TORCH_TO_MOE[residual.dtype], udt, x_dtype, wdt, gdt, kind,
                  MOE_NORM_UNIT_OFFSET if unit_offset else 0, alpha, eps)
@@ -907,22 +909,24 @@ def moe_norm(residual: torch.Tensor, block: torch.Tensor | None = None,
     ``x_dtype``, or, for float8_e4m3fn, is (codes, scales) as moe_gemm_f8
     takes them. Without block residual_out is residual itself; without weight
     x is None."""
-    f8 = x_dtype == torch.float8_e4m3fn
+    given, f8 = residual, x_dtype == torch.float8_e4m3fn
     if not f8 and x_dtype not in _TORCH_TO_MOE:
         raise ValueError("x_dtype must be float32, bfloat16, float16 or float8_e4m3fn")
     d, residual, block, weight, post_weight, gate = _norm_args(
         residual, block, weight, post_weight, gate, alpha, eps, unit_offset,
         MOE_F8B128 if f8 else _TORCH_TO_MOE[x_dtype])
     with _on(residual.device):
-        out = residual if block is None else torch.empty_like(residual)
+        out = given if block is None else torch.empty_like(residual)
         x = s = None
         if weight is not None:
             x = torch.empty_like(residual, dtype=x_dtype)
             if f8:
-                s = residual.new_empty((d.T, _blocks(d.D)), dtype=torch.float32)
+                T, D = residual.shape
+                s = torch.empty(T, _blocks(D), dtype=torch.float32, device=residual.device)
         _check(library().moe_norm_forward(
             ctypes.byref(d), residual.data_ptr(), _ptr(block), _ptr(post_weight),
-            _ptr(gate), _ptr(weight), out.data_ptr(), _ptr(x), _ptr(s),
+            _ptr(gate), _ptr(weight), None if block is None else out.data_ptr(),
+            _ptr(x), _ptr(s),
             _stream(residual.device)))
     return out, ((x, s) if f8 and x is not None else x)
 
@@ -957,21 +961,23 @@ def moe_norm_backward(residual_out: torch.Tensor, block: torch.Tensor | None,
         if nbytes == 0:
             raise MoeError(MOE_EINVAL, moe_last_error())
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=residual_out.device)
-        f32 = dict(dtype=torch.float32, device=residual_out.device)
+        f32, dev = torch.float32, residual_out.device
+        D = residual_out.shape[1]
         out = {"dresidual": torch.empty_like(residual_out)}
         if block is not None:
             out["dblock"] = torch.empty_like(block)
         if weight is not None:
-            out["dweight"] = torch.empty(d.D, **f32)
+            out["dweight"] = torch.empty(D, dtype=f32, device=dev)
         if post_weight is not None:
-            out["dpost_weight"] = torch.empty(d.D, **f32)
+            out["dpost_weight"] = torch.empty(D, dtype=f32, device=dev)
         if gate is not None:
-            out["dgate"] = torch.empty(gate.shape, **f32)
-        ptr = lambda name: _ptr(out.get(name))  # noqa: E731
+            out["dgate"] = torch.empty_like(gate, dtype=torch.float32)
+        get = out.get
         _check(L.moe_norm_backward(
             ctypes.byref(d), residual_out.data_ptr(), _ptr(block), _ptr(post_weight),
-            _ptr(gate), _ptr(weight), _ptr(dresidual_out), _ptr(dx), ptr("dresidual"),
-            ptr("dblock"), ptr("dpost_weight"), ptr("dgate"), ptr("dweight"),
+            _ptr(gate), _ptr(weight), _ptr(dresidual_out), _ptr(dx),
+            out["dresidual"].data_ptr(), _ptr(get("dblock")), _ptr(get("dpost_weight")),
+            _ptr(get("dgate")), _ptr(get("dweight")),
             workspace.data_ptr(), nbytes, _stream(residual_out.device)))
     return out
 

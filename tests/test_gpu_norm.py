@@ -99,6 +99,17 @@ def test_forward_parts_and_in_place():
     assert st == moe.MOE_OK and torch.equal(r, full) and torch.equal(x1, x2)
 
 
+def test_forward_of_a_view():
+    """A residual that is a view at an odd offset, without a block: it comes
+    back as it is."""
+    base = torch.randn(6, 72, device="cuda")
+    r = base[::2, 3:67]
+    w = torch.ones(64, device="cuda")
+    out, x = moe.moe_norm(r, weight=w, x_dtype=torch.float32)
+    assert out is r
+    assert torch.equal(x, moe.moe_norm(r.clone(), weight=w, x_dtype=torch.float32)[1])
+
+
 def test_forward_many_rows():
     """More workgroups than a launch holds along one axis (2^32 threads)."""
     T = (1 << 26) + 5
