@@ -33,8 +33,11 @@ namespace moe {
 // SRC 0 (plain products) reads quantised rows. SRC 1 (decode-shaped plans)
 // reads the rows as they are (x in its type, or h in f32) and quantises the
 // group's into LDS first, every workgroup for itself: for so few rows this
-// costs less than a launch that quantises them once.
-constexpr int kStripLds = 32768;   // bytes of rows a workgroup may hold (SRC 1)
+// costs less than a launch that quantises them once, and streams. us of a
+// layer so / so: 2 tokens, top-8 of 128, D 2048, F 768 25 / 43, 8 tokens 61 /
+// 64; 16 tokens, top-2 of 16, D 1536, F 256 21 / 31, top-4 at D 2048, F 768
+// (34 KB of rows) 31 / 35.
+constexpr int kStripLds = 49152;   // bytes of rows a workgroup may hold (SRC 1)
 
 __host__ __device__ constexpr int strip_share(int nkb) { return nkb >= 4 ? 4 : nkb >= 2 ? 2 : 1; }
 
@@ -188,8 +191,12 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
 // it quantises itself; down: 128 columns), ks waves sharing a strip's blocks
 // of K, so that a workgroup's loads run through its weights in pieces of
 // whole rows: a wave that walked its rows alone, 128 bytes of 16 rows at a
-// time, got 3.8 TB/s from memory. The rows' fragments stay in registers over
-// all strips where K <= 128 ks NX.
+// time, got half of the rate. The rows' fragments stay in registers over all
+// strips where K <= 128 ks NX. Bound by memory: 128 tokens on 129 experts, D
+// 2048, F 768, take 83 us for gate/up (406 MB, 4.9 TB/s) and 49 for down (203
+// MB, 4.1 TB/s; a workgroup lives for two steps, too few to hide its start).
+// Loads without a place in the caches (nontemporal) were 7 % slower, the next
+// step's loads a step earlier gained 2 us of down and lost 2 at K = 512.
 template <int MODE, int NX>
 __global__ __launch_bounds__(512, 4) void f8_stream_kernel(F8Args a, int ks) {
   constexpr int WF = MODE == 1 ? 2 : 1;
@@ -323,8 +330,10 @@ static void run_stream(const F8Args& a, int ks, int64_t grid, hipStream_t s) {
 hipError_t launch_f8_stream(const F8Args& a, hipStream_t s) {
   const int64_t grid = (int64_t)a.max_groups * (a.N / 128);
   if (grid == 0) return hipSuccess;
-  // the most waves a strip that leave each a block or more; two or three
-  // blocks a wave and chunk
+  // The most waves a strip that leave each two blocks or more (one or more: 56
+  // us, not 52, for the down stream of 128 tokens, K = 768), two or three
+  // blocks a wave and chunk, whichever leaves fewer idle (two at K = 768: 74
+  // us, not 52; six, and one wave a strip: 92).
   const int nkb = a.K / 128;
   int ks = 8;
   while (ks > 1 && nkb < 2 * ks) ks >>= 1;

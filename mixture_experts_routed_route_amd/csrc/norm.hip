@@ -10,7 +10,9 @@
 // of the threads that own it between the two sums, so the launch is bound
 // by HBM. A row takes 64 threads (four rows a workgroup) or a workgroup of
 // up to 1024, 8 or 16 values each, so that a thread's registers leave
-// several workgroups a CU, whose loads cover one another's sums.
+// several workgroups a CU, whose loads cover one another's sums. Forward: 13312
+// x 4096, f32 residual, f16 block and x, 120 us, 5.4 TB/s (a copy of 1 GiB runs
+// at 5.1, an addition in place at 5.9).
 #include <algorithm>
 
 #include "rows_common.h"
@@ -143,6 +145,11 @@ static hipError_t run_norm_forward(const NormArgs& a, hipStream_t s) {
 
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
+  // 8 values a thread where they fill 256 or 512 threads, 16 a thread else.
+  // 13312 x 4096 f32 residual and f16 block, us of the same bytes as rows of
+  // 1024 / 2048 / 4096 / 8192 values: this rule 126 / 122 / 123 / 131, twice
+  // the values a thread (half at 1024 and 8192) 122 / 129 / 130 / 129, four
+  // times - / 137 / 142 / 141.
   if (a.D <= 512) return run_norm_forward<64, 1>(a, s);
   if (a.D <= 1024) return run_norm_forward<64, 2>(a, s);
   if (a.D <= 2048) return run_norm_forward<256, 1>(a, s);
@@ -167,7 +174,9 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
 // the parameters in LDS, the next row's loads in flight, its partial sums of
 // dw, dp and a channel gate's dg in registers; it writes them once,
 // [3][grid][D], and a second launch adds the workgroups' partials in order
-// (no atomics: the same bits from run to run).
+// (no atomics: the same bits from run to run). 4096 x 2048 f32: 41 us and 4
+// for the columns, 201 MB at 4.4 TB/s; 8192 x 8192 bf16 170 us, 4.7 TB/s: the
+// walk's one barrier a row and the first and last rows' latency are left.
 // Every load and store of the walk is a buffer instruction that is always
 // there: what a type, a missing tensor, a short row or a row past the last
 // leaves out lies past its buffer's end (loads give 0, stores write nothing).

@@ -221,9 +221,10 @@ def test_one_token(dt, D, F, E, k, shared, cf):
         _check(wl, ws, y_dtype, moe.make_options(flags=moe.MOE_OPT_TILED_DECODE))
 
 
-@pytest.mark.parametrize("T,D,F,k", [(16, 2048, 128, 2), (9, 256, 4096, 1), (2, 16384, 128, 2)])
+@pytest.mark.parametrize("T,D,F,k", [(16, 2048, 128, 2), (9, 256, 4096, 1), (2, 16384, 128, 2),
+                                     (16, 4096, 128, 2), (12, 128, 4096, 3)])
 def test_few_tokens_of_wide_rows(T, D, F, k):
-    """Decode-shaped calls whose rows are too wide for the strips' LDS."""
+    """Decode-shaped calls whose rows fill the strips' LDS, or are too wide."""
     wl, ws = _layer(T, D, F, 4, k, "bf16", 1, seed=T + D)
     _check(wl, ws, torch.float32)
 
