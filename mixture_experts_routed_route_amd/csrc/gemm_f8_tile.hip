@@ -361,22 +361,65 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
         }
       }
     } else {
-      const bool vec = (N & 3) == 0;
+      if ((N & (a.odt == MOE_F32 ? 3 : 7)) == 0) {   // 16-byte stores
+        // Through LDS, 128 rows at a time, so that a store covers whole rows of
+        // the tile. Lanes hold four columns of 16 rows; stored from there, 64
+        // or 32 bytes a row, a bf16 product of 4096^3 took 68 us, not 65, and
+        // a 4096-token layer's down product (K = 768, f32) 128 us, not 119.
+        // Piece c (four columns) of row r lies at piece c ^ (r & 15).
+        float* const tile = reinterpret_cast<float*>(smem);   // [128][kTW]
+        auto at = [](int r, int c) { return r * kTW + ((c ^ (r & 15)) << 2); };
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const int r = (wt * TB + t) * 16 + lr;
-        if (r >= rows) continue;
+        for (int h = 0; h < (NT > 2 ? 2 : 1); ++h) {
+          fence();
+          wait_vm_lgkm0<63>();
+          __builtin_amdgcn_s_barrier();   // the stages, or the half before, have been read
+          fence();
+          if (NT <= 2 || wt >> 1 == h) {
 #pragma unroll
-        for (int i = 0; i < FW; ++i) {
-          const int n = n0 + (ww * FW + i) * 16 + lq * 4;
-          const size_t at = (size_t)(row0 + r) * N + n;
-          const float v[4] = {acc[i][t][0], acc[i][t][1], acc[i][t][2], acc[i][t][3]};
-          if (vec) {
-            if (n < N) store_out4(a.out, a.odt, at, v);
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+              for (int i = 0; i < FW; ++i)
+                *reinterpret_cast<floatx4*>(
+                    tile + at((wt * TB + t) * 16 + lr - 128 * h, (ww * FW + i) * 4 + lq)) = acc[i][t];
+          }
+          fence();
+          wait_vm_lgkm0<63>();
+          __builtin_amdgcn_s_barrier();
+          fence();
+          const int rh = min(128, rows - 128 * h);
+          const size_t r0 = (size_t)(row0 + 128 * h);
+          if (a.odt == MOE_F32) {
+#pragma unroll 4
+            for (int r = wave; r < rh; r += 8) {
+              const floatx4 v = *reinterpret_cast<const floatx4*>(tile + at(r, lane));
+              if (n0 + lane * 4 < N)
+                *reinterpret_cast<floatx4*>(static_cast<float*>(a.out) + (r0 + r) * N + n0 +
+                                            lane * 4) = v;
+            }
           } else {
+            const int c = lane & 31;
+#pragma unroll 4
+            for (int r = wave * 2 + (lane >> 5); r < rh; r += 16) {
+              const floatx4 x = *reinterpret_cast<const floatx4*>(tile + at(r, 2 * c));
+              const floatx4 y = *reinterpret_cast<const floatx4*>(tile + at(r, 2 * c + 1));
+              const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+              if (n0 + c * 8 < N) store8(a.out, a.odt, (r0 + r) * N + n0 + c * 8, v);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const int r = (wt * TB + t) * 16 + lr;
+          if (r >= rows) continue;
+#pragma unroll
+          for (int i = 0; i < FW; ++i) {
+            const int n = n0 + (ww * FW + i) * 16 + lq * 4;
+            const size_t at = (size_t)(row0 + r) * N + n;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (n + q < N) store_out1(a.out, a.odt, at + q, v[q]);
+              if (n + q < N) store_out1(a.out, a.odt, at + q, acc[i][t][q]);
           }
         }
       }
