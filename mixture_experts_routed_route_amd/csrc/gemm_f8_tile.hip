@@ -440,8 +440,7 @@ hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s) {
   const dim3 grid((unsigned)blocks), block(512);
   if (prec) {
     if (a.mode == 0) hipLaunchKernelGGL((f8_tile_kernel<0, 1>), grid, block, 0, s, a);
-    else if (a.mode == 1) hipLaunchKernelGGL((f8_tile_kernel<1, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((f8_tile_kernel<2, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((f8_tile_kernel<1, 1>), grid, block, 0, s, a);
   } else {
     if (a.mode == 0) hipLaunchKernelGGL((f8_tile_kernel<0, 0>), grid, block, 0, s, a);
     else if (a.mode == 1) hipLaunchKernelGGL((f8_tile_kernel<1, 0>), grid, block, 0, s, a);

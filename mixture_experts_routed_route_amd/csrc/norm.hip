@@ -322,8 +322,9 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
     const __amdgpu_buffer_rsrc_t rg =
         make_rsrc(static_cast<const char*>(a.g) + (size_t)(live ? row : 0) * gate_sz,
                   live ? gate_sz : 0u);
-    q.g32 = __builtin_amdgcn_raw_buffer_load_b32(rg, 0, 0, 0);
-    q.g16 = __builtin_amdgcn_raw_buffer_load_b16(rg, 0, 0, 0);
+    // the one of the other size lies past the end as a whole
+    q.g32 = __builtin_amdgcn_raw_buffer_load_b32(rg, gate_sz == 4 ? 0 : kPastEnd, 0, 0);
+    q.g16 = __builtin_amdgcn_raw_buffer_load_b16(rg, gate_sz == 2 ? 0 : kPastEnd, 0, 0);
   };
   // pieces i0 .. i0 + NH - 1
   auto load_row = [&](Row& q, int64_t row, int i0) {

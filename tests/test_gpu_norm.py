@@ -243,6 +243,19 @@ def test_backward_parts_and_determinism():
     assert none["dresidual"].shape == (0, 64) and bool((none["dweight"] == 0).all())
 
 
+@pytest.mark.parametrize("par", ["bf16", "f16", "f32"])
+def test_backward_token_gate_to_the_last_byte(par):
+    """A gate a token whose values end where the tensor's pages do: each
+    token's own value, none read past the last."""
+    T, D = 1 << 20, 8
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[par]
+    u = torch.ones(T, D, device="cuda")
+    gate = (torch.arange(T, device="cuda") % 251 + 1).to(dt)[:, None]
+    out = moe.moe_norm_backward(u, u, None, u, gate=gate, alpha=0.5)
+    assert torch.equal(out["dblock"], 0.5 * gate.float().expand(T, D))
+    assert torch.equal(out["dgate"], torch.full_like(gate, 4.0, dtype=torch.float32))
+
+
 def test_layer_step_together():
     """Norm, router, experts on 8-bit weights, norm with the next
     projection's quantised rows, product; then captured and replayed."""
