@@ -182,10 +182,10 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
 // leaves out lies past its buffer's end (loads give 0, stores write nothing).
 // One counter orders loads and stores, and with branches between them the
 // wait for a row's loads would cover the stores of the row before.
-// HELD: the parameters in LDS, a row in registers between its sums and the
-// rest. Rows of more than 8192 values have room in neither: they read the
-// parameters for every row, and the row again after its sums (4096 x
-// 16384 bf16 in 764 us, 1037 if held; either way the compiler spills).
+// SPLIT: rows of more than 8192 values, whose sums a launch of their own has
+// left in `stats`; blockIdx.y walks a part of the columns (held whole, such a
+// row's partial sums and values spilled: 4096 x 16384 bf16 in 1037 us, not
+// 308).
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kPastEnd = (int)0x80000000u;
 
@@ -234,8 +234,86 @@ __device__ __forceinline__ Wide8 wide_from_f32(const float (&v)[8], int dt) {
   return w;
 }
 
-template <int TPR, int R, int NV, bool HELD>
-__global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_backward_kernel(NormBwdArgs a) {
+// what a row's six sums (norm_backward_kernel) give: its inverse norms, mean(t
+// n) inv, the second norm's mean, a token gate's gradient
+struct RowStats { float inv, m, inv_u, mp, dg; };
+__device__ __forceinline__ RowStats row_stats(const NormBwdArgs& a, const float (&sum)[6],
+                                              float gt) {
+  const float invD = 1.f / (float)a.D;
+  RowStats s;
+  s.inv = rsqrtf(sum[0] * invD + a.eps);
+  s.m = sum[1] * s.inv * s.inv * invD;
+  s.inv_u = a.p ? rsqrtf(sum[2] * invD + a.eps) : 1.f;
+  const float aud = a.w ? sum[3] + s.inv * (sum[4] - s.m * sum[5]) : sum[3];
+  s.mp = gt * s.inv_u * aud * invD;
+  s.dg = s.inv_u * aud;
+  return s;
+}
+
+// eight of the parameters k (0 w, 1 p, 2 alpha times a channel gate) from
+// channel c; ones where there is none, zeros past the row
+__device__ __forceinline__ void read_params(const NormBwdArgs& a, int k, int c, float (&v)[8]) {
+  const void* src = k == 0 ? a.w : k == 1 ? a.p : a.gate_token ? nullptr : a.g;
+  const int dt = k == 2 ? a.gdt : a.wdt;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = c < a.D ? 1.f : 0.f;
+  if (src && c < a.D) {
+    raw8_to_f32(load_raw8(src, dt, c), dt, v);
+    if (k != 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = param(v[j], a.unit);
+    }
+  }
+  if (k == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= a.alpha;
+  }
+}
+
+// the sums of rows of more than 8192 values, a workgroup a row:
+// (inv, m, inv_u, mp) and a token gate's gradient
+__global__ __launch_bounds__(1024) void norm_sums_kernel(NormBwdArgs a, float4* stats) {
+  __shared__ float sh[6 * 16];
+  const int64_t row = wide_block();
+  if (row >= a.T) return;   // whole workgroups
+  const size_t base = (size_t)row * a.D;
+  float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int c = threadIdx.x * 8; c < a.D; c += 8192) {
+    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float dx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.w) {
+      raw8_to_f32(load_raw8(a.r, a.rdt, base + c), a.rdt, r);
+      raw8_to_f32(load_raw8(a.dx, a.dxdt, base + c), a.dxdt, dx);
+    }
+    if (a.u) raw8_to_f32(load_raw8(a.u, a.udt, base + c), a.udt, u);
+    if (a.dr) raw8_to_f32(load_raw8(a.dr, a.rdt, base + c), a.rdt, d);
+    float wv[8], pv[8], gv[8];
+    read_params(a, 0, c, wv);
+    read_params(a, 1, c, pv);
+    read_params(a, 2, c, gv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float tt = dx[j] * wv[j], au = gv[j] * pv[j] * u[j];
+      sum[0] = fmaf(r[j], r[j], sum[0]);
+      sum[1] = fmaf(tt, r[j], sum[1]);
+      sum[2] = fmaf(u[j], u[j], sum[2]);
+      sum[3] = fmaf(au, d[j], sum[3]);
+      sum[4] = fmaf(au, tt, sum[4]);
+      sum[5] = fmaf(au, r[j], sum[5]);
+    }
+  }
+  row_sums<1024>(sum, sh);
+  if (threadIdx.x) return;
+  const RowStats s = row_stats(a, sum, a.g && a.gate_token ? load_one(a.g, a.gdt, row) : 1.f);
+  stats[row] = float4{s.inv, s.m, s.inv_u, s.mp};
+  if (a.dg_token) a.dg_token[row] = s.dg;
+}
+
+template <int TPR, int R, int NV, bool SPLIT>
+__global__ __launch_bounds__(TPR * R, NV == 1 ? 4 : 2) void norm_backward_kernel(
+    NormBwdArgs a, const float4* stats) {
   constexpr int W = TPR / 64;   // waves a row
   extern __shared__ __attribute__((aligned(16))) float par[];   // [3][cols]: w, p, alpha p g
   __shared__ float sh[2][R][6 * W];
@@ -243,50 +321,22 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
   constexpr int cols = TPR * NV * 8;
   const int t = threadIdx.x % TPR;
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);   // whole waves
-  const float invD = 1.f / (float)a.D;
+  const int c0 = SPLIT ? (int)blockIdx.y * cols : 0;   // the first channel
   const bool gate_ch = a.g && !a.gate_token;
   const uint32_t u_values = a.u ? (uint32_t)a.D : 0u, w_values = a.w ? (uint32_t)a.D : 0u;
-  // eight of the parameters k (0 w, 1 p, 2 alpha times a channel gate) from
-  // channel c; ones where there is none, zeros past the row
-  auto read_params = [&](int k, int c, float (&v)[8]) {
-    const void* src = k == 0 ? a.w : k == 1 ? a.p : gate_ch ? a.g : nullptr;
-    const int dt = k == 2 ? a.gdt : a.wdt;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c < a.D ? 1.f : 0.f;
-    if (src && c < a.D) {
-      raw8_to_f32(load_raw8(src, dt, c), dt, v);
-      if (k != 2) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = param(v[j], a.unit);
-      }
-    }
-    if (k == 2) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= a.alpha;
-    }
-  };
   // parameters h .. h + 3 of a thread's eight: four at a time, the loops over
   // halves kept apart, so that no more of them take registers
   auto params = [&](int k, int c, int h, float (&v)[4]) {
-    if (HELD) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = par[k * cols + c + h + j];
-    } else {
-      float w[8];
-      read_params(k, c, w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = w[h + j];
-    }
+    for (int j = 0; j < 4; ++j) v[j] = par[k * cols + c + h + j];
   };
-  if (HELD) {
-    for (int c = threadIdx.x * 8; c < cols; c += TPR * R * 8) {
+  for (int c = threadIdx.x * 8; c < cols; c += TPR * R * 8) {
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        float v[8];
-        read_params(k, c, v);
+    for (int k = 0; k < 3; ++k) {
+      float v[8];
+      read_params(a, k, c0 + c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) par[k * cols + c + j] = v[j];
-      }
+      for (int j = 0; j < 8; ++j) par[k * cols + c + j] = v[j];
     }
   }
   float dw[NV][8], dp[NV][8], dg[NV][8];
@@ -302,128 +352,113 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
                      live ? values * sz : 0u);
   };
   auto load8 = [&](__amdgpu_buffer_rsrc_t rs, int dt, int i) {
-    const int off = (i * TPR + t) * (dt == MOE_F32 ? 32 : 16);
+    const int off = (c0 + (i * TPR + t) * 8) * (dt == MOE_F32 ? 4 : 2);
     Wide8 w;
     w.a = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
     w.b = __builtin_amdgcn_raw_buffer_load_b128(rs, dt == MOE_F32 ? off + 16 : kPastEnd, 0, 0);
     return w;
   };
   auto put8 = [&](__amdgpu_buffer_rsrc_t rs, int dt, int i, const float (&v)[8]) {
-    const int off = (i * TPR + t) * (dt == MOE_F32 ? 32 : 16);
+    const int off = (c0 + (i * TPR + t) * 8) * (dt == MOE_F32 ? 4 : 2);
     const Wide8 w = wide_from_f32(v, dt);
     __builtin_amdgcn_raw_buffer_store_b128(w.a, rs, off, 0, 0);
     __builtin_amdgcn_raw_buffer_store_b128(w.b, rs, dt == MOE_F32 ? off + 16 : kPastEnd, 0, 0);
   };
-  constexpr int NH = HELD ? NV : 1;
-  struct Row { Wide8 r[NH], x[NH], u[NH], e[NH]; uint32_t g32, g16; };
+  struct Row { Wide8 r[NV], x[NV], u[NV], e[NV]; u32x4 st; uint32_t g32, g16; };
   const uint32_t gate_sz = !a.g || !a.gate_token ? 0u : a.gdt == MOE_F32 ? 4u : 2u;
-  auto load_gate = [&](Row& q, int64_t row) {
+  auto load_row = [&](Row& q, int64_t row) {
     const bool live = row < a.T;
+    if (SPLIT)
+      q.st = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(stats + (live ? row : 0), live ? 16u : 0u),
+                                                   0, 0, 0);
     const __amdgpu_buffer_rsrc_t rg =
         make_rsrc(static_cast<const char*>(a.g) + (size_t)(live ? row : 0) * gate_sz,
                   live ? gate_sz : 0u);
     // the one of the other size lies past the end as a whole
     q.g32 = __builtin_amdgcn_raw_buffer_load_b32(rg, gate_sz == 4 ? 0 : kPastEnd, 0, 0);
     q.g16 = __builtin_amdgcn_raw_buffer_load_b16(rg, gate_sz == 2 ? 0 : kPastEnd, 0, 0);
-  };
-  // pieces i0 .. i0 + NH - 1
-  auto load_row = [&](Row& q, int64_t row, int i0) {
     const __amdgpu_buffer_rsrc_t rr = row_of(a.r, a.rdt, row, w_values);
     const __amdgpu_buffer_rsrc_t rx = row_of(a.dx, a.dxdt, row, w_values);
     const __amdgpu_buffer_rsrc_t ru = row_of(a.u, a.udt, row, u_values);
     const __amdgpu_buffer_rsrc_t re = row_of(a.dr, a.rdt, row, a.dr ? (uint32_t)a.D : 0u);
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      q.r[i] = load8(rr, a.rdt, i0 + i);
-      q.x[i] = load8(rx, a.dxdt, i0 + i);
-      q.u[i] = load8(ru, a.udt, i0 + i);
-      q.e[i] = load8(re, a.rdt, i0 + i);
+    for (int i = 0; i < NV; ++i) {
+      q.r[i] = load8(rr, a.rdt, i);
+      q.x[i] = load8(rx, a.dxdt, i);
+      q.u[i] = load8(ru, a.udt, i);
+      q.e[i] = load8(re, a.rdt, i);
     }
   };
   // the same number of turns for every row group: the sums hold barriers
   const int64_t step = (int64_t)gridDim.x * R;
   const int64_t first = (int64_t)blockIdx.x * R;
   Row q;
-  load_gate(q, first + sub);
-  if (HELD) load_row(q, first + sub, 0);
+  load_row(q, first + sub);
   __syncthreads();   // the parameters
   int turn = 0;
   for (int64_t row0 = first; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub;
     const bool live = row < a.T;
-    float r[NH][8], dx[NH][8], u[NH][8], d[NH][8];
-    auto widen_row = [&]() {
+    float r[NV][8], dx[NV][8], u[NV][8], d[NV][8];
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        wide_to_f32(q.r[i], a.rdt, r[i]);
-        wide_to_f32(q.x[i], a.dxdt, dx[i]);
-        wide_to_f32(q.u[i], a.udt, u[i]);
-        wide_to_f32(q.e[i], a.rdt, d[i]);
-      }
-    };
-    if (HELD) widen_row();
+    for (int i = 0; i < NV; ++i) {
+      wide_to_f32(q.r[i], a.rdt, r[i]);
+      wide_to_f32(q.x[i], a.dxdt, dx[i]);
+      wide_to_f32(q.u[i], a.udt, u[i]);
+      wide_to_f32(q.e[i], a.rdt, d[i]);
+    }
+    const u32x4 st = q.st;
     float gt = 1.f;   // a token's gate
     if (gate_sz) {
       gt = a.gdt == MOE_F32 ? __uint_as_float(q.g32)
          : a.gdt == MOE_BF16 ? __uint_as_float(q.g16 << 16)
                              : (float)__builtin_bit_cast(_Float16, (uint16_t)q.g16);
     }
-    load_gate(q, row0 + step + sub);
-    if (HELD) load_row(q, row0 + step + sub, 0);
-    float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // r'^2, t r', u^2, a u (dr', t, r')
+    load_row(q, row0 + step + sub);
+    RowStats rs;
+    if (SPLIT) {
+      rs = {__uint_as_float(st[0]), __uint_as_float(st[1]), __uint_as_float(st[2]),
+            __uint_as_float(st[3]), 0.f};
+    } else {
+      float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // r'^2, t r', u^2, a u (dr', t, r')
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int n = HELD ? i : 0;
-      int c = (i * TPR + t) * 8;
-      if (!HELD) {
-        asm volatile("" : "+v"(c));   // the parameters here, not before the walk
-        load_row(q, row, i);
-        widen_row();
-      }
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * 8;
 #pragma unroll
-      for (int h = 0; h < 8; h += 4) {
-        float wv[4], pv[4], gv[4];
-        params(0, c, h, wv);
-        params(1, c, h, pv);
-        params(2, c, h, gv);
+        for (int h = 0; h < 8; h += 4) {
+          float wv[4], pv[4], gv[4];
+          params(0, c, h, wv);
+          params(1, c, h, pv);
+          params(2, c, h, gv);
 #pragma unroll
-        for (int j = h; j < h + 4; ++j) {
-          const float tt = dx[n][j] * wv[j - h];
-          const float au = gv[j - h] * pv[j - h] * u[n][j];
-          sum[0] = fmaf(r[n][j], r[n][j], sum[0]);
-          sum[1] = fmaf(tt, r[n][j], sum[1]);
-          sum[2] = fmaf(u[n][j], u[n][j], sum[2]);
-          sum[3] = fmaf(au, d[n][j], sum[3]);
-          sum[4] = fmaf(au, tt, sum[4]);
-          sum[5] = fmaf(au, r[n][j], sum[5]);
+          for (int j = h; j < h + 4; ++j) {
+            const float tt = dx[i][j] * wv[j - h];
+            const float au = gv[j - h] * pv[j - h] * u[i][j];
+            sum[0] = fmaf(r[i][j], r[i][j], sum[0]);
+            sum[1] = fmaf(tt, r[i][j], sum[1]);
+            sum[2] = fmaf(u[i][j], u[i][j], sum[2]);
+            sum[3] = fmaf(au, d[i][j], sum[3]);
+            sum[4] = fmaf(au, tt, sum[4]);
+            sum[5] = fmaf(au, r[i][j], sum[5]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      // the halves of sh take turns: a row's reads lie between its barrier and
+      // the next row's, after which the half is written again
+      row_sums<TPR>(sum, sh[turn][sub]);
+      turn ^= 1;
+      rs = row_stats(a, sum, gt);
+      __builtin_amdgcn_raw_buffer_store_b32(
+          __float_as_uint(rs.dg), make_rsrc(a.dg_token + (live ? row : 0), live && a.dg_token ? 4u : 0u),
+          t == 0 ? 0 : kPastEnd, 0, 0);
     }
-    // the halves of sh take turns: a row's reads lie between its barrier and
-    // the next row's, after which the half is written again
-    row_sums<TPR>(sum, sh[turn][sub]);
-    turn ^= 1;
-    const float inv = rsqrtf(sum[0] * invD + a.eps);
-    const float m = sum[1] * inv * inv * invD;   // mean(t n) inv
-    const float inv_u = a.p ? rsqrtf(sum[2] * invD + a.eps) : 1.f;
-    const float aud = a.w ? sum[3] + inv * (sum[4] - m * sum[5]) : sum[3];
-    const float mp = gt * inv_u * aud * invD;
-    __builtin_amdgcn_raw_buffer_store_b32(
-        __float_as_uint(inv_u * aud),
-        make_rsrc(a.dg_token + (live ? row : 0), live && a.dg_token ? 4u : 0u),
-        t == 0 ? 0 : kPastEnd, 0, 0);
+    const float inv = rs.inv, m = rs.m, inv_u = rs.inv_u, mp = rs.mp;
     const __amdgpu_buffer_rsrc_t rd = row_of(a.dr_out, a.rdt, row, (uint32_t)a.D);
     const __amdgpu_buffer_rsrc_t ru = row_of(a.du, a.udt, row, u_values);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int n = HELD ? i : 0;
-      int c = (i * TPR + t) * 8;
-      if (!HELD) {
-        asm volatile("" : "+v"(c));   // the parameters here, not before the walk
-        load_row(q, row, i);
-        widen_row();
-      }
+      const int c = (i * TPR + t) * 8;
       float o[8];
 #pragma unroll
       for (int h = 0; h < 8; h += 4) {
@@ -436,22 +471,22 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
           if (a.w) {
 #pragma unroll
             for (int j = h; j < h + 4; ++j) {
-              dw[i][j] = fmaf(dx[n][j], r[n][j] * inv, dw[i][j]);
-              d[n][j] += inv * (dx[n][j] * wv[j - h] - r[n][j] * m);
+              dw[i][j] = fmaf(dx[i][j], r[i][j] * inv, dw[i][j]);
+              d[i][j] += inv * (dx[i][j] * wv[j - h] - r[i][j] * m);
             }
           }
 #pragma unroll
           for (int j = h; j < h + 4; ++j) {
-            const float v = u[n][j] * inv_u;
-            dg[i][j] = fmaf(a.alpha * d[n][j], v * pv[j - h], dg[i][j]);
-            const float dz = gt * gv[j - h] * d[n][j];
+            const float v = u[i][j] * inv_u;
+            dg[i][j] = fmaf(a.alpha * d[i][j], v * pv[j - h], dg[i][j]);
+            const float dz = gt * gv[j - h] * d[i][j];
             dp[i][j] = fmaf(dz, v, dp[i][j]);
             o[j] = a.p ? inv_u * (dz * pv[j - h] - v * mp) : dz;
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      put8(rd, a.rdt, i, d[n]);
+      put8(rd, a.rdt, i, d[i]);
       put8(ru, a.udt, i, o);
     }
   }
@@ -476,8 +511,8 @@ __global__ __launch_bounds__(TPR * R, NV == 1 || TPR == 1024 ? 4 : 2) void norm_
             for (int j = 0; j < 8; ++j) v[i][j] += fold[(j * (R - 1) + s) * TPR + t];
         }
       }
-      if (c < a.D && !sub)
-        store8(a.part, MOE_F32, ((size_t)k * gridDim.x + blockIdx.x) * a.D + c, v[i]);
+      if (c0 + c < a.D && !sub)
+        store8(a.part, MOE_F32, ((size_t)k * gridDim.x + blockIdx.x) * a.D + c0 + c, v[i]);
     }
   }
 }
@@ -520,12 +555,18 @@ int bwd_slots(int T, int D) {
 
 }  // namespace
 
-size_t norm_backward_part_floats(int T, int D) { return (size_t)3 * bwd_slots(T, D) * D; }
+// the slots, and four values a row whose sums have a launch of their own
+size_t norm_backward_part_floats(int T, int D) {
+  return (size_t)3 * bwd_slots(T, D) * D + (D > 8192 ? (size_t)T * 4 : 0);
+}
 
-template <int TPR, int R, int NV, bool HELD = true>
+template <int TPR, int R, int NV, bool SPLIT = false>
 static void run_norm_backward(const NormBwdArgs& a, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((norm_backward_kernel<TPR, R, NV, HELD>), dim3(grid), dim3(TPR * R),
-                     HELD ? 3 * TPR * NV * 8 * sizeof(float) : 0, s, a);
+  constexpr int cols = TPR * NV * 8;
+  hipLaunchKernelGGL((norm_backward_kernel<TPR, R, NV, SPLIT>),
+                     dim3(grid, SPLIT ? (a.D + cols - 1) / cols : 1), dim3(TPR * R),
+                     3 * cols * sizeof(float), s, a,
+                     reinterpret_cast<const float4*>(a.part + (size_t)3 * grid * a.D));
 }
 
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s) {
@@ -539,7 +580,15 @@ hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t s) {
   else if (a.D <= 2048) run_norm_backward<128, 4, 2>(a, slots, s);
   else if (a.D <= 4096) run_norm_backward<256, 2, 2>(a, slots, s);
   else if (a.D <= 8192) run_norm_backward<512, 1, 2>(a, slots, s);
-  else run_norm_backward<1024, 1, 2, false>(a, slots, s);
+  else {
+    if (a.T > 0) {
+      hipLaunchKernelGGL(norm_sums_kernel, wide_grid(a.T), dim3(1024), 0, s, a,
+                         reinterpret_cast<float4*>(a.part + (size_t)3 * slots * a.D));
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    run_norm_backward<512, 1, 2, true>(a, slots, s);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(norm_columns_kernel, dim3((a.D + 63) / 64, 3), dim3(1024), 0, s, a.part,
