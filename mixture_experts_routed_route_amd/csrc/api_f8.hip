@@ -63,15 +63,16 @@ size_t moe::f8_layer_bytes(const moe_plan_desc& d, int D, int F) {
 // A plan's experts of more rows than this take the tile: its 64-row tiles
 // read 256 weight rows once for all rows, where a stream of thin groups reads
 // them again for every 16 rows. With 32 (64) instead of 16, 512 uniform tokens
-// on 128 experts, top-8, D 2048, F 768 take 266 (332) us, not 190; 4096 skewed
-// ones 516 (530), not 447.
+// on 128 experts, top-8, D 2048, F 768 take 231 (279) us, not 179; 4096 skewed
+// ones 571 (575), not 547.
 constexpr int kF8StreamRows = 16;
 // ... in plans of at least so many pairs an expert and more than so many in
 // all. Below, the tiles' two launches wait for a few workgroups' walks along
 // K: us with tiles / with streams alone at the same D and F: 160 tokens on
-// 128 experts (10 pairs an expert) 172 / 150, 224 (14) 174 / 175, 256 (16)
-// 178 / 200; 32 tokens on 16 experts (16, 256 pairs) 68 / 47, 128 on 8 (32)
-// 42 / 47, 256 on 8 (64) 49 / 55; 1024 skewed ones, top-1 of 128 (8), 103 / 82.
+// 128 experts (10 pairs an expert) 166 / 144, 224 (14) 166 / 149, 256 (16)
+// 172 / 174; 32 tokens on 16 experts (16, 256 pairs) 67 / 41; 512 on 33 (62)
+// 69 / 130, 1024 on 8 (256) 93 / 125; 1024 skewed ones, top-1 of 128 (8), 119 /
+// 78.
 constexpr int kF8TilePairs = 16, kF8TileAll = 256;
 // Above so many tokens always: one expert may hold them all.
 constexpr int kF8StreamT = 1024;
@@ -150,9 +151,9 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       g.list = (const int32_t*)(b + L.tiles);
       g.groups = (const int32_t*)(b + L.meta) + kF8Tiles;
       g.max_groups = L.cap_tiles;
-      // an f16 layer's gate/up sums stay exact: a code of h that moves by a
-      // step weighs more than f16's rounding of y
-      return launch_f8_tile(g, !down && l.xdt == MOE_F16, s);
+      // gate/up in f32: h becomes codes, and one that an error of its sums
+      // moves, moves by a whole step (2^-4 of its value and more)
+      return launch_f8_tile(g, !down, s);
     default:
       return launch_combine(b + L.y, false, p.tok2pair, p.w, p.offsets, d.T,
                             l.D, d.k, d.n_shared, d.E, l.ydt, l.y, s);
