@@ -84,9 +84,9 @@ typedef enum {
      * infinity and stands for NaN. As weights of moe_forward (bf16 / f16
      * x; scales 16-byte aligned), the layer quantises x's rows and the
      * SwiGLU output (f32, per pair and 128 features) and multiplies codes:
-     * with sums in f32 throughout, except that the down products of experts
-     * of more than 16 rows, in plans of many pairs, are summed as moe_gemm_f8
-     * does for a 16-bit output. Pairs are f32. */
+     * with sums in f32 throughout, except that for a 16-bit y the down
+     * products of experts of more than 16 rows, in plans of many pairs, are
+     * summed as moe_gemm_f8 does for a 16-bit output. Pairs are f32. */
     MOE_F8B128 = 6
 } moe_dtype;
 

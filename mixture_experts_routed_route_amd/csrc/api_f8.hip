@@ -152,8 +152,9 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
       g.groups = (const int32_t*)(b + L.meta) + kF8Tiles;
       g.max_groups = L.cap_tiles;
       // gate/up in f32: h becomes codes, and one that an error of its sums
-      // moves, moves by a whole step (2^-4 of its value and more)
-      return launch_f8_tile(g, !down, s);
+      // moves, moves by a whole step (2^-4 of its value and more); down in
+      // f32 where y, the pairs' sum, is not rounded to 16 bits
+      return launch_f8_tile(g, !down || l.ydt == MOE_F32, s);
     default:
       return launch_combine(b + L.y, false, p.tok2pair, p.w, p.offsets, d.T,
                             l.D, d.k, d.n_shared, d.E, l.ydt, l.y, s);

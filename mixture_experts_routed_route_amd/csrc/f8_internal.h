@@ -64,8 +64,7 @@ hipError_t launch_f8_stream(const F8Args& a, hipStream_t s);
 // whether strips may take groups of `rows` rows of K values unquantised
 bool f8_strip_raw_fits(int rows, int K);
 // list: (expert, row0) tiles of kFullBM rows, max_groups of them at most.
-// prec 0 (modes 0 and 2): codes in the 8-bit matrix unit; 1 (modes 0 and 1):
-// widened to f16
+// prec 0 (modes 0 and 2): codes in the 8-bit matrix unit; 1: widened to f16
 hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s);
 
 // One-token calls on MOE_F8B128 weights (gemv_f8.hip).

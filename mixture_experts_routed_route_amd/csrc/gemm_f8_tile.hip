@@ -15,8 +15,8 @@
 // and drops what lies 2^-13 below it, an error of 1.5e-5 of an output on
 // normally distributed rows: for 16-bit outputs (half a step is up to 2^-8 or
 // 2^-11 of the value) far less than their own rounding. PREC 1 widens the
-// codes to f16 (exactly) and sums them in f32 throughout, for f32 outputs and
-// for gate/up: h is coded next, and the few codes that an error of its sums
+// codes to f16 (exactly) and sums them in f32 throughout, for f32 outputs (a
+// layer's down products where y is f32) and for gate/up: h is coded next, and the few codes that an error of its sums
 // moves over a border move by a whole step. With PREC 0 there a bf16 layer of
 // 4096 tokens was 2.0e-3 from the exact y, not 1.7e-3.
 //
@@ -443,7 +443,8 @@ hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s) {
   const dim3 grid((unsigned)blocks), block(512);
   if (prec) {
     if (a.mode == 0) hipLaunchKernelGGL((f8_tile_kernel<0, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((f8_tile_kernel<1, 1>), grid, block, 0, s, a);
+    else if (a.mode == 1) hipLaunchKernelGGL((f8_tile_kernel<1, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((f8_tile_kernel<2, 1>), grid, block, 0, s, a);
   } else {
     if (a.mode == 0) hipLaunchKernelGGL((f8_tile_kernel<0, 0>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((f8_tile_kernel<2, 0>), grid, block, 0, s, a);
