@@ -434,6 +434,14 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it where it is strided or starts off the 16-byte
+    boundary that the library asks for (a slice of rows with an odd number of
+    scales, of experts, of a token gate, of a flat parameter buffer)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 def _weight(w, device) -> tuple:
     if _is_f8(w):
         data, scales = w
@@ -441,7 +449,7 @@ def _weight(w, device) -> tuple:
             raise ValueError("8-bit weights are (float8_e4m3fn codes, float32 scales)")
         if data.device != device or scales.device != device:
             raise ValueError("weights must be on the input's device")
-        data, scales = data.contiguous(), scales.contiguous()
+        data, scales = _aligned(data), _aligned(scales)
         return (Weight(MOE_F8B128, data.data_ptr(), scales.data_ptr()),
                 (data, scales))
     if isinstance(w, (tuple, list)):
@@ -754,7 +762,7 @@ def moe_quant_f8(x: torch.Tensor) -> tuple:
         raise ValueError(f"K={K} must be a positive multiple of 8")
     _c_int("K", K)
     with _on(x.device):
-        x = x.contiguous()
+        x = _aligned(x)
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         s = torch.empty(*x.shape[:-1], _blocks(K), dtype=torch.float32, device=x.device)
         _check(library().moe_quant_f8(x.data_ptr(), _TORCH_TO_MOE[x.dtype],
@@ -778,7 +786,7 @@ def moe_quant_f8_weights(w: torch.Tensor) -> tuple:
     for n in w.shape[:-2]:
         mats *= n
     with _on(w.device):
-        w = w.contiguous()
+        w = _aligned(w)
         q = torch.empty_like(w, dtype=torch.float8_e4m3fn)
         s = torch.empty(*w.shape[:-2], _blocks(N), _blocks(K), dtype=torch.float32,
                         device=w.device)
@@ -824,7 +832,7 @@ def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
         odt = _TORCH_TO_MOE.get(out.dtype)
         if odt is None:
             raise ValueError("the result is float32, bfloat16 or float16")
-        xq, xs, wq, ws = xq.contiguous(), xs.contiguous(), wq.contiguous(), ws.contiguous()
+        xq, xs, wq, ws = _aligned(xq), _aligned(xs), _aligned(wq), _aligned(ws)
         _check(library().moe_gemm_f8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(),
                                      ws.data_ptr(), xq.numel() // K, N, K, out.data_ptr(),
                                      odt, _stream(dev)))
@@ -835,7 +843,7 @@ def _rows_like(t, like, name: str):
     if t.dtype not in _TORCH_TO_MOE or t.shape != like.shape or t.device != like.device:
         raise ValueError(f"{name} must be a float32/bfloat16/float16 tensor of shape "
                          f"{tuple(like.shape)} on the residual's device")
-    return t.contiguous()
+    return _aligned(t)
 
 
 def _norm_vec(v, D, like, dtype):
@@ -844,7 +852,7 @@ def _norm_vec(v, D, like, dtype):
             or v.shape != (D,) or v.device != like.device:
         raise ValueError(f"weight and post_weight must be [{D}] tensors of one "
                          "type (float32/bfloat16/float16) on the residual's device")
-    return v.contiguous()
+    return _aligned(v)
 
 
 def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
@@ -856,7 +864,7 @@ def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
     if D < 8 or D % 8 or D > MOE_NORM_MAX_D:
         raise ValueError(f"D={D} must be a multiple of 8 in 8..{MOE_NORM_MAX_D}")
     _c_int("T", T)
-    residual = residual.contiguous()
+    residual = _aligned(residual)
     udt = wdt = gdt = MOE_F32
     kind = MOE_GATE_NONE
     if block is None:
@@ -883,7 +891,7 @@ def _norm_args(residual, block, weight, post_weight, gate, alpha, eps,
                 or gate.device != residual.device:
             raise ValueError(f"gate must be [{D}] (per channel) or [{T}, 1] (per token), "
                              "float32/bfloat16/float16, on the residual's device")
-        gate = gate.contiguous()
+        gate = _aligned(gate)
         gdt = _TORCH_TO_MOE[gate.dtype]
     d = NormDesc(T, D, _TORCH_TO_MOE[residual.dtype], udt, x_dtype, wdt, gdt, kind,
                  MOE_NORM_UNIT_OFFSET if unit_offset else 0, alpha, eps)
