@@ -297,10 +297,12 @@ moe_status moe_norm_forward(const moe_norm_desc* d, const void* residual,
                             void* stream) {
   const moe_status st = norm_desc_ok(d);
   if (st != MOE_OK) return st;
-  if (!block && (post_weight || d->gate_kind != MOE_GATE_NONE))
-    return set_error(MOE_EINVAL, "a post-norm or a gate needs a block output");
-  if (!block && !weight) return set_error(MOE_EINVAL, "neither a block nor a weight: nothing to do");
+  // a tensor of no rows has no pointer: NULL says nothing about it
   if (d->T > 0) {
+    if (!block && (post_weight || d->gate_kind != MOE_GATE_NONE))
+      return set_error(MOE_EINVAL, "a post-norm or a gate needs a block output");
+    if (!block && !weight)
+      return set_error(MOE_EINVAL, "neither a block nor a weight: nothing to do");
     if (!residual) return set_error(MOE_EINVAL, "residual is NULL");
     if (block && !residual_out) return set_error(MOE_EINVAL, "residual_out is NULL");
     if (weight && !x) return set_error(MOE_EINVAL, "x is NULL");
@@ -342,15 +344,18 @@ moe_status moe_norm_backward(const moe_norm_desc* d, const void* residual_out,
   if (st != MOE_OK) return st;
   if (d->x_dtype == MOE_F8B128)
     return set_error(MOE_EUNSUPPORTED, "dx is f32, bf16 or f16");
-  if (!block && (post_weight || d->gate_kind != MOE_GATE_NONE))
-    return set_error(MOE_EINVAL, "a post-norm or a gate needs a block output");
-  if (!weight && !dresidual_out)
-    return set_error(MOE_EINVAL, "neither a weight nor dresidual_out: no gradient comes in");
   if ((weight && !dweight) || (post_weight && !dpost_weight) ||
-      (d->gate_kind != MOE_GATE_NONE && (!gate || !dgate)))
+      ((d->gate_kind == MOE_GATE_CHANNEL || (d->gate_kind == MOE_GATE_TOKEN && d->T > 0)) &&
+       (!gate || !dgate)))
     return set_error(MOE_EINVAL, "a parameter or its gradient is NULL");
-  if (d->T > 0 && (!dresidual || (block && !dblock) || (weight && (!residual_out || !dx))))
-    return set_error(MOE_EINVAL, "residual_out, dx, dresidual or dblock is NULL");
+  if (d->T > 0) {   // as in the forward; the parameters' gradients are zeros without rows
+    if (!block && (post_weight || d->gate_kind != MOE_GATE_NONE))
+      return set_error(MOE_EINVAL, "a post-norm or a gate needs a block output");
+    if (!weight && !dresidual_out)
+      return set_error(MOE_EINVAL, "neither a weight nor dresidual_out: no gradient comes in");
+    if (!dresidual || (block && !dblock) || (weight && (!residual_out || !dx)))
+      return set_error(MOE_EINVAL, "residual_out, dx, dresidual or dblock is NULL");
+  }
   for (const void* p : {residual_out, block, post_weight, gate, weight, dresidual_out, dx,
                         (const void*)dresidual, (const void*)dblock, (const void*)dpost_weight,
                         (const void*)dgate, (const void*)dweight})

@@ -1,12 +1,13 @@
 """
-Views in the 8-bit and norm calls: tensors that start off a 16-byte boundary,
-as slices of rows, experts, tokens and flat parameter buffers do, give what
-their copies give.
+Views and empty batches in the 8-bit and norm calls: tensors that start off a
+16-byte boundary, as slices of rows, experts, tokens and flat parameter buffers
+do, give what their copies give; no rows give empty rows and zero sums.
 """
 
 import pytest
 import torch
 
+import f8_ref as R
 import mixture_experts_routed_route_amd as moe
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +86,23 @@ def test_norm_of_some_of_the_tokens():
         part = moe.moe_norm_backward(out[t:], u[t:], x[t:], r[t:], w, gate=g[t:])
         for n in ("dresidual", "dblock", "dgate"):
             assert torch.equal(part[n], back[n][t:]), n
+
+
+@pytest.mark.parametrize("D", [64, 8200])
+@pytest.mark.parametrize("gate", [None, "channel", "token"])
+def test_norm_of_no_rows(gate, D):
+    rows = lambda: torch.empty(0, D, device="cuda")  # noqa: E731
+    one = torch.ones(D, device="cuda")
+    g = None if gate is None else one if gate == "channel" else torch.empty(0, 1, device="cuda")
+    out, (q, s) = moe.moe_norm(rows(), rows(), one, one, g, x_dtype=R.F8)
+    assert out.shape == q.shape == (0, D) and s.shape == (0, -(-D // 128))
+    out, x = moe.moe_norm(rows(), rows(), None, one, g)
+    assert out.shape == (0, D) and x is None
+    got = moe.moe_norm_backward(rows(), rows(), rows(), rows(), one, one, g)
+    assert got["dresidual"].shape == got["dblock"].shape == (0, D)
+    for n in ("dweight", "dpost_weight") + (("dgate",) if gate == "channel" else ()):
+        assert torch.equal(got[n], torch.zeros(D, device="cuda")), n
+    assert gate != "token" or got["dgate"].shape == (0, 1)
+    got = moe.moe_norm_backward(rows(), rows(), None, rows(), None, one, g)
+    assert set(got) == {"dresidual", "dblock", "dpost_weight"} | ({"dgate"} if gate else set())
+    assert bool((got["dpost_weight"] == 0).all())
