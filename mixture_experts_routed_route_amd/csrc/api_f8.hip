@@ -175,7 +175,7 @@ hipError_t moe::launch_f8_step(const F8Plan& p, const F8Layer& l, int step, hipS
 static bool f8_split(F8Args* g, bool f32, int ncu) {
   if (g->M <= 64) return false;
   const double c256 = f32 ? 4.1 : 2.1, c128 = f32 ? 1.95 : 1.5, c64 = f32 ? 1.25 : 0.87;
-  const int64_t nnb = (g->N + 255) / 256, nk = (g->K + 127) / 128;
+  const int64_t nnb = ((int64_t)g->N + 255) / 256, nk = (g->K + 127) / 128;
   auto rounds = [&](int64_t tiles) { return (double)((tiles * nnb + ncu - 1) / ncu); };
   double best = 2.0 * ((g->M + 63) / 64 * 64) * g->N * g->K / 172e6;
   bool tile = false;
@@ -208,7 +208,7 @@ moe_status moe_quant_f8(const void* x, int32_t dtype, int64_t rows, int32_t K,
   if (rows > 0 && (!x || !q || !scales)) return set_error(MOE_EINVAL, "x, q or scales is NULL");
   if (!aligned16(x) || !aligned16(q) || !aligned16(scales))
     return set_error(MOE_EINVAL, "x, q and scales must be 16-byte aligned");
-  if (rows > ((int64_t)1 << 31) / ((K + 127) / 128) - 1)
+  if (rows > ((int64_t)1 << 31) / (((int64_t)K + 127) / 128) - 1)
     return set_error(MOE_EUNSUPPORTED, "rows=%lld x K=%d hold 2^31 blocks or more",
                      (long long)rows, K);
   if (rows == 0) return MOE_OK;

@@ -50,10 +50,11 @@ __global__ __launch_bounds__(256) void f8_strip_kernel(F8Args a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int K = a.K, N = a.N;
-  const int nkb = (K + 127) / 128, nnb = (N + 127) / 128;
+  // N may be any size up to 2^31 - 1: no sum past it
+  const int nkb = (K + 127) / 128, nnb = (N - 1) / 128 + 1;
   const int ks = strip_share(nkb), spw = 4 / ks;
   const int kw = wave & (ks - 1);          // this wave's share of K
-  const int strips = (N + 15) / 16;
+  const int strips = (N - 1) / 16 + 1;
   const int sblocks = (strips + spw - 1) / spw;
   const int64_t groups = MODE == 0 ? (a.M + 16 * RB - 1) / (16 * RB) : *a.groups;
   const int64_t items = groups * sblocks;
@@ -356,7 +357,7 @@ static void run_strip(const F8Args& a, unsigned grid, hipStream_t s) {
 
 hipError_t launch_f8_strip(const F8Args& a, int ncu, hipStream_t s) {
   const int spw = 4 / strip_share((a.K + 127) / 128);
-  const int64_t sblocks = ((a.N + 15) / 16 + spw - 1) / spw;
+  const int64_t sblocks = (((int64_t)a.N + 15) / 16 + spw - 1) / spw;
   // 64 rows a workgroup once 16 would make four workgroups a CU: weights are
   // read a fourth as often, by fewer waves (us with 64 / 16 rows: 64 rows by
   // 4096 x 4096 17.6 / 22.0, by 2048 x 1024 7.5 / 5.8; 128 by 1001 x 1040 7.7

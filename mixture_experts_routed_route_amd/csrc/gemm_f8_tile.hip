@@ -68,7 +68,7 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
   const int lr = lane & 15, lq = lane >> 4;
   const int K = a.K, N = a.N;
   const int nk = (K + 127) / 128;
-  const int NNB = MODE == 1 ? N / 128 : (N + kTW - 1) / kTW;
+  const int NNB = MODE == 1 ? N / 128 : (N - 1) / kTW + 1;
   // Block b runs on XCD b mod 8, whose L2 its neighbours share.
   int ti, nb;
   if (MODE == 0) {
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
     };
     // the weights' scales: one a wave's 128 rows and block (gate/up: one of
     // each matrix)
-    const int nn = (N + 127) / 128;
+    const int nn = (N - 1) / 128 + 1;
     const int sb = MODE == 1 ? nb : min(nb * 2 + ww / (NW / 2), nn - 1);
     const float* ws0 = a.B0s + ((size_t)e * nn + sb) * nk;
     const float* ws1 = MODE == 1 ? a.B1s + ((size_t)e * nn + sb) * nk : ws0;
@@ -435,7 +435,7 @@ __global__ __launch_bounds__(512, 1) void f8_tile_kernel(F8Args a) {
 
 hipError_t launch_f8_tile(const F8Args& a, int prec, hipStream_t s) {
   const int64_t tiles = a.mode == 0 ? a.tiles256 + a.tail_tiles : a.max_groups;
-  const int64_t nnb = a.mode == 1 ? a.N / 128 : (a.N + kTW - 1) / kTW;
+  const int64_t nnb = a.mode == 1 ? a.N / 128 : ((int64_t)a.N + kTW - 1) / kTW;
   if (tiles * nnb == 0) return hipSuccess;
   const int64_t blocks = a.mode == 0
       ? (a.tiles256 * nnb + 7) / 8 * 8 + (a.tail_tiles * nnb + 7) / 8 * 8

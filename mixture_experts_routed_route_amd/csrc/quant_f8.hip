@@ -31,7 +31,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(
 
 hipError_t launch_quant_rows(const void* x, int dt, int64_t rows, int K,
                              void* q, float* s, hipStream_t st) {
-  const int64_t nb = (K + 127) / 128;
+  const int64_t nb = ((int64_t)K + 127) / 128;
   const int64_t n = rows * nb;
   if (n == 0) return hipSuccess;
   hipLaunchKernelGGL(quant_rows_kernel, wide_grid((n + 15) / 16), dim3(256), 0, st,
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void quant_weights_kernel(
 
 hipError_t launch_quant_weights(const void* w, int dt, int64_t mats, int N,
                                 int K, void* q, float* s, hipStream_t st) {
-  const int64_t nn = (N + 127) / 128, nk = (K + 127) / 128;
+  const int64_t nn = ((int64_t)N + 127) / 128, nk = ((int64_t)K + 127) / 128;
   const int64_t n = mats * nn * nk;
   if (n == 0) return hipSuccess;
   hipLaunchKernelGGL(quant_weights_kernel, wide_grid(n), dim3(256), 0, st, w, dt,
