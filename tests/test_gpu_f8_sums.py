@@ -9,7 +9,7 @@ import torch
 
 import f8_ref as R
 import mixture_experts_routed_route_amd as moe
-from test_gpu_f8 import DT, _layer, _run
+from test_gpu_f8 import DT, _check, _layer, _product, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,20 @@ def test_error_in_the_norm(dt, T, D, F, E, k, shared):
     err = (y.cpu().double() - ref).norm(dim=1)
     print(f"error {float(err.norm() / ref.norm()):.2e}, bound {float(bound.norm() / ref.norm()):.2e} of y's norm")
     assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(300, 512, 8208), (130, 257, 16528), (70, 300, 8192)])
+def test_product_of_long_rows(M, N, K, out):
+    """More than 64 and 128 blocks of K on the tile: its weights' scales are
+    loaded again, 64 blocks at a time."""
+    got, ref, bound = _product(M, N, K, out, seed=K)
+    err = (got.cpu().double() - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,F", [(8320, 128), (128, 8320)])
+def test_layer_of_long_rows(dt, D, F):
+    wl, ws = _layer(150, D, F, 2, 2, dt, seed=D)
+    _check(wl, ws, torch.float32)
