@@ -433,9 +433,11 @@ moe_status moe_quant_f8_weights(const void *w, int32_t dtype, int64_t mats,
  * or F16). An F32 output's sums are f32 throughout; for a 16-bit output of
  * more than 64 rows each eight neighbouring products are aligned to the
  * largest among them, bits below 2^-13 of its exponent dropped (the 8-bit
- * matrix unit's sum; about 1.5e-5 of the output). K a multiple of 16 up to
- * 2^22; M below 2^31, M and N any other size (0
- * writes nothing). Pointers 16-byte aligned. Async on `stream`. */
+ * matrix unit's sum; about 1.5e-5 of the output) where the sizes do not make
+ * strips of rows, with f32 sums, the faster way: a row's last bits can change
+ * with the rows beside it. K a multiple of 16 up to 2^22; M below 2^31, M and N
+ * any other size (0 writes nothing). Pointers 16-byte aligned. Async on
+ * `stream`. */
 moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,
                        const float *w_scales, int64_t M, int32_t N, int32_t K,
                        void *out, int32_t out_dtype, void *stream);

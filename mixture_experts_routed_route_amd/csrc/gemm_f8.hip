@@ -25,10 +25,10 @@ namespace moe {
 // waves takes 4 / ks strips, ks waves sharing one's blocks of K, their partial
 // sums meeting in LDS: as many as leave each a block (from 16 blocks on only,
 // 64 x 512 . 4096 x 512 took 9.1 us, not 5.9; from 64 on, 8 x 4096 . 1024 x
-// 4096 12.1, not 7.9). A wave holds one block of loads at a time: the up to
-// eight workgroups of a CU cover one another's waits. One row of 2048 values
-// by 4096 takes 4.8 us (1.7 TB/s of weights: a chain of loads, not their
-// rate).
+// 4096 12.1, not 7.9). A wave holds one block of loads at a time: in launches
+// of many workgroups the up to eight of a CU cover one another's waits. One
+// row of 2048 values by 4096 is 256 workgroups, one a CU, whose waves take four
+// blocks in turn: 4.8 us (1.7 TB/s of weights), four waits that nothing covers.
 //
 // SRC 0 (plain products) reads quantised rows. SRC 1 (decode-shaped plans)
 // reads the rows as they are (x in its type, or h in f32) and quantises the

@@ -20,11 +20,13 @@
 // moves over a border move by a whole step. With PREC 0 there a bf16 layer of
 // 4096 tokens was 2.0e-3 from the exact y, not 1.7e-3.
 //
-// 13312 x 4096 x 4096 to f16: 224 us, 1.99 PFLOP/s; a scale for a whole tensor,
-// which no block scales interrupt, lets a library product run at 3.05. Of zeros
-// 8192^3 runs at 2.6 PFLOP/s, of random codes at 2.05: the clock gives way to
-// power first. Next the 128 fma a lane and step that scale and add the blocks'
-// sums, and the waits at a tile's ends.
+// 13312 x 4096 x 4096 to f16: 225 us, 1.99 PFLOP/s; to f32 390 us, 1.14. A
+// library product of the same codes with one scale for a whole tensor takes 202
+// to 231. Traced, the matrix units are busy for 46 % of the cycles at 2.11 GHz
+// (zeros: 47 % at 2.32; to f32 48 % at 2.31; the library's 49 % at 2.14), so
+// power takes a tenth of the clock, and over half of the cycles go to the 128
+// fma a lane and step that scale and add the blocks' sums, which both waves of a
+// SIMD do at the same time, to the barrier of a step, and to a tile's ends.
 #include <algorithm>
 
 #include "f8_common.h"

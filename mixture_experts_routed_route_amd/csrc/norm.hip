@@ -545,8 +545,10 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(
 
 namespace {
 
-// Workgroups of the backward, each leaving one slot of partials: as many as
-// the compute units hold at once, two of 256 threads or one of 512.
+// Workgroups of the backward along its rows, each leaving one slot of
+// partials: as many as the compute units hold at once, two of 256 threads or
+// one of 512. Above 8192 values the columns' two parts, 8192 and the rest,
+// double them, and they run in two rounds.
 int bwd_slots(int T, int D) {
   const int rows = D <= 2048 ? 4 : D <= 4096 ? 2 : 1;
   const int most = D <= 1024 ? 512 : 256;

