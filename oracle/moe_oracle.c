@@ -305,7 +305,7 @@ static void expert_ffn(int64_t D, int64_t F, int64_t e, const double *x,
         }
         double gc = gs, uc = us;
         if (c > 0.0) {
-            gc = gs < c ? gs : c;
+            gc = gs > c ? c : gs;
             uc = us < -c ? -c : (us > c ? c : us);
         }
         hh[f] = silu(gc) * uc;
