@@ -102,7 +102,7 @@ typedef struct {
 
 /* Forward options; moe_options_default() fills the defaults.
  *   swiglu_limit      c of h = silu(min(g, c)) * clamp(u, -c, c); <= 0 turns
- *                     the clamp off. Default 7.0.
+ *                     the clamp off. A NaN stays one. Default 7.0.
  *   splitk_max_pairs  S: bf16/f16 experts holding n <= S pairs run the
  *                     split-K (weight-streaming) tile, the rest the full
  *                     MFMA tile. An f32
