@@ -361,6 +361,39 @@ moe_status moe_forward_get_views(const moe_plan *plan, int32_t D, int32_t F,
                                  const moe_options *opt, const void *ws,
                                  moe_forward_views *out);
 
+/* Most tokens of a moe_decode call. */
+#define MOE_DECODE_MAX_T 16
+
+/* Bytes of device workspace moe_decode needs; 0 if unsupported. */
+size_t moe_decode_workspace_bytes(const moe_plan_desc *desc, int32_t D,
+                                  int32_t F, int32_t x_dtype, int32_t w_dtype);
+
+/* The whole layer for a few tokens (T <= MOE_DECODE_MAX_T) without a plan:
+ * routing, experts and weighted sum of desc, as moe_plan_create and
+ * moe_forward define them (top-k with ties to the lower index and NaN below
+ * -inf, renormalised weights, the capacity limit in token order, a shared
+ * expert, swiglu_limit), in two launches, three with w_router. w_router NULL:
+ * logits [T, E] (f32) are read; otherwise logits = x . w_router^T (w_router
+ * [E, D] in x's dtype, f32 sums) are written first and then used. x is BF16 or
+ * F16, the weights x's dtype or a 4-bit format (as moe_forward's, also beside
+ * a BF16 x; MOE_Q4B32, MOE_Q4A32 and MOE_Q4A64 are used unrounded, q * s (+ b)
+ * in f32). Products are summed in f32; the SwiGLU output is held in two 16-bit
+ * parts (its rounding to x's dtype and the rest), a token's pairs are weighed
+ * and summed in f32 and y (MOE_F32 or x's dtype) is rounded once. The same
+ * bits from run to run. A token whose pairs all drop, without a shared expert,
+ * has a row of zeros. On 4-bit weights a row of x (or a SwiGLU row) that holds
+ * an infinity or a NaN gives NaN. D and F are multiples of 128 up to 2^20.
+ * opt: swiglu_limit and the phase flags (7 the router's map, 3 gate/up with
+ * the routing, 5 down with the weighted sum; NULL: defaults). Pointers 16-byte
+ * aligned, ws 256-byte aligned; calls that may overlap need a workspace each.
+ * Async on `stream`. */
+moe_status moe_decode(const moe_plan_desc *desc, const void *x,
+                      int32_t x_dtype, const void *w_router, float *logits,
+                      moe_weight w_gate, moe_weight w_up, moe_weight w_down,
+                      int32_t D, int32_t F, void *y, int32_t y_dtype,
+                      void *ws, size_t ws_bytes, const moe_options *opt,
+                      void *stream);
+
 /* --- backward ----------------------------------------------------------- */
 
 /* Bytes of device workspace moe_backward needs; 0 if unsupported. */
@@ -441,6 +474,34 @@ moe_status moe_quant_f8_weights(const void *w, int32_t dtype, int64_t mats,
 moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,
                        const float *w_scales, int64_t M, int32_t N, int32_t K,
                        void *out, int32_t out_dtype, void *stream);
+
+/* --- 4-bit weights ---------------------------------------------------------- */
+
+/* w [rows, K] (F32, BF16 or F16) as 4-bit weights of format w_dtype
+ * (MOE_Q4B32, MOE_Q4A32 or MOE_Q4A64): data [rows, K / 2] and scales as that
+ * format has them. MOE_Q4B32: s = fp16(max|v| / 7), q = clamp(rint(v / s), -8,
+ * 7). Affine: s = fp16((max - min) / 15), b = fp16(min), q = clamp(rint((v - b)
+ * / s), 0, 15). Quotients and differences are rounded to f32, rint and fp16()
+ * go to nearest even; s = 0 has q = 0. A group that holds a NaN or an infinity,
+ * or whose s passes fp16's range, stands for NaN; one whose b does, for
+ * infinities or NaN. K a multiple of the group. Pointers 16-byte aligned.
+ * MOE_EUNSUPPORTED above 2^40 values. Async on `stream`. */
+moe_status moe_quant_q4_weights(const void *w, int32_t dtype, int32_t w_dtype,
+                                int64_t rows, int64_t K, void *data,
+                                void *scales, void *stream);
+
+/* out[M, N] = x[M, K] . w[N, K]^T on 4-bit weights (w.dtype MOE_Q4B32,
+ * MOE_Q4A32 or MOE_Q4A64; data [N, K / 2] and scales as moe_quant_q4_weights
+ * writes them): x BF16 or F16, out F32, BF16 or F16. The weights' values are
+ * not rounded: each group's sum of codes times x comes from the matrix units in
+ * f32 and is scaled and added in f32; one rounding to out_dtype. A row of x
+ * that holds an infinity or a NaN gives NaN; bf16 rows' group sums must stay
+ * below 2^120. K a multiple of the format's group up to 2^22; M below 2^31, N
+ * up to 2^31 - 256 (0 writes nothing). Pointers 16-byte aligned. Async on
+ * `stream`. */
+moe_status moe_gemm_q4(const void *x, int32_t x_dtype, moe_weight w, int64_t M,
+                       int32_t N, int32_t K, void *out, int32_t out_dtype,
+                       void *stream);
 
 /* --- norms around a block -------------------------------------------------- */
 

@@ -23,6 +23,15 @@ G = 32 or 64 K values (the format follows from the params' shape); or, for
 8-bit weights, ``(codes float8_e4m3fn [.., N, K], scales float32 [.., ceil(N /
 128), ceil(K / 128)])`` pairs as moe_quant_f8_weights makes them.
 
+A few tokens go through the whole layer in one call, without a plan:
+
+    y, logits = moe_decode(x, w_gate, w_up, w_down, k=8, w_router=w_router)
+
+and the projections of a model on 4-bit weights, from one row on, with the
+quantiser that makes such weights:
+
+    out = moe_gemm_q4(x, moe_quant_q4_weights(w))
+
 Around the layer, the norms after one block and before the next, and the
 projections on 8-bit weights that read their output:
 
@@ -48,6 +57,7 @@ MOE_F8B128 = 6
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 MOE_NORM_UNIT_OFFSET = 1
 MOE_NORM_MAX_D = 16384
+MOE_DECODE_MAX_T = 16
 MOE_OPT_PHASE_EVENTS = 1
 MOE_OPT_BF16_PLAIN_H = 2
 MOE_OPT_EXACT_ROUTES = 4
@@ -84,6 +94,8 @@ EXPORTED = (
     "moe_forward_noalloc", "moe_quant_f8", "moe_quant_f8_weights",
     "moe_gemm_f8", "moe_norm_forward",
     "moe_norm_backward_workspace_bytes", "moe_norm_backward",
+    "moe_quant_q4_weights", "moe_gemm_q4", "moe_decode_workspace_bytes",
+    "moe_decode",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -217,6 +229,15 @@ def library(path: str = LIB_PATH):
     L.moe_norm_backward_workspace_bytes.restype = sz
     L.moe_norm_backward.argtypes = [ctypes.POINTER(NormDesc)] + [vp] * 13 + [sz, vp]
     L.moe_norm_backward.restype = i32
+    L.moe_quant_q4_weights.argtypes = [vp, i32, i32, i64, i64, vp, vp, vp]
+    L.moe_quant_q4_weights.restype = i32
+    L.moe_gemm_q4.argtypes = [vp, i32, Weight, i64, i32, i32, vp, i32, vp]
+    L.moe_gemm_q4.restype = i32
+    L.moe_decode_workspace_bytes.argtypes = [ctypes.POINTER(PlanDesc), i32, i32, i32, i32]
+    L.moe_decode_workspace_bytes.restype = sz
+    L.moe_decode.argtypes = [ctypes.POINTER(PlanDesc), vp, i32, vp, vp, Weight, Weight, Weight,
+                             i32, i32, vp, i32, vp, sz, ctypes.POINTER(Options), vp]
+    L.moe_decode.restype = i32
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_version.argtypes = []
@@ -839,6 +860,145 @@ def moe_gemm_f8(x, w, out_dtype: torch.dtype = torch.bfloat16,
     return out
 
 
+def moe_quant_q4_weights(w: torch.Tensor, w_dtype: int = MOE_Q4B32) -> tuple:
+    """Weights [.., N, K] (float32, bfloat16 or float16; K a multiple of the
+    format's group) as 4-bit weights of a format: (data uint8 [.., N, K/2],
+    params float16), params [.., N, K/32] for MOE_Q4B32, [.., N, K/32, 2] for
+    MOE_Q4A32 and [.., N, K/64, 2] for MOE_Q4A64."""
+    if w.dtype not in _TORCH_TO_MOE or w.dim() < 2:
+        raise ValueError("w must be a float32/bfloat16/float16 tensor [.., N, K]")
+    if w_dtype not in (MOE_Q4B32, MOE_Q4A32, MOE_Q4A64):
+        raise ValueError("w_dtype must be MOE_Q4B32, MOE_Q4A32 or MOE_Q4A64")
+    lead, K = w.shape[:-1], w.shape[-1]
+    G = 64 if w_dtype == MOE_Q4A64 else 32
+    if K < G or K % G:
+        raise ValueError(f"K={K} must be a positive multiple of {G}")
+    with _on(w.device):
+        w = _aligned(w)
+        data = torch.empty(*lead, K // 2, dtype=torch.uint8, device=w.device)
+        shape = (*lead, K // G) if w_dtype == MOE_Q4B32 else (*lead, K // G, 2)
+        params = torch.empty(shape, dtype=torch.float16, device=w.device)
+        _check(library().moe_quant_q4_weights(
+            w.data_ptr(), _TORCH_TO_MOE[w.dtype], w_dtype, w.numel() // K, K,
+            data.data_ptr(), params.data_ptr(), _stream(w.device)))
+    return data, params
+
+
+def moe_gemm_q4(x: torch.Tensor, w, out_dtype: torch.dtype | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """out [.., N] = x . w^T of rows x [.., K] (bfloat16 or float16) and 4-bit
+    weights w = (data uint8 [N, K/2], params float16) of any format (the
+    params' shape picks it). The result has ``out``'s type, or ``out_dtype``
+    (float32, bfloat16 or float16; x's by default)."""
+    data, params = w
+    if x.dtype not in (torch.bfloat16, torch.float16) or x.dim() < 1:
+        raise ValueError("x must be a bfloat16/float16 tensor [.., K]")
+    if data.dtype != torch.uint8 or params.dtype != torch.float16 or data.dim() != 2:
+        raise ValueError("4-bit weights are (uint8 data [N, K/2], float16 params)")
+    lead, K = x.shape[:-1], x.shape[-1]
+    N = data.shape[0]
+    if data.shape[1] * 2 != K or K == 0 or params.shape[0] != N:
+        raise ValueError(f"x {tuple(x.shape)}, data {tuple(data.shape)} and params "
+                         f"{tuple(params.shape)} must be [.., K], [N, K/2] and [N, ..]")
+    wdt = q4_dtype(data, params)
+    _c_int("K", K)
+    _c_int("N", N)
+    dev = x.device
+    if data.device != dev or params.device != dev:
+        raise ValueError("x and w must be on one device")
+    with _on(dev):
+        if out is None:
+            out = torch.empty(*lead, N, dtype=out_dtype or x.dtype, device=dev)
+        elif out.shape != (*lead, N) or not out.is_contiguous() or out.device != dev:
+            raise ValueError(f"out must be a contiguous {(*lead, N)} tensor on x's device")
+        odt = _TORCH_TO_MOE.get(out.dtype)
+        if odt is None:
+            raise ValueError("the result is float32, bfloat16 or float16")
+        x, data, params = _aligned(x), _aligned(data), _aligned(params)
+        _check(library().moe_gemm_q4(x.data_ptr(), _TORCH_TO_MOE[x.dtype],
+                                     Weight(wdt, data.data_ptr(), params.data_ptr()),
+                                     x.numel() // K, N, K, out.data_ptr(), odt,
+                                     _stream(dev)))
+    return out
+
+
+def _aligned_weight(w):
+    return tuple(_aligned(t) for t in w) if isinstance(w, (tuple, list)) else _aligned(w)
+
+
+def moe_decode_workspace_bytes(T, E, k, D, F, x_dtype: int, w_dtype: int,
+                               capacity_factor=0.0, n_shared=0) -> int:
+    d = PlanDesc(T, E, k, n_shared, capacity_factor)
+    return int(library().moe_decode_workspace_bytes(ctypes.byref(d), D, F, x_dtype, w_dtype))
+
+
+def moe_decode(x: torch.Tensor, w_gate, w_up, w_down, k: int,
+               logits: torch.Tensor | None = None,
+               w_router: torch.Tensor | None = None,
+               capacity_factor: float = 0.0, n_shared: int = 0,
+               options: Options | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None,
+               y_dtype: torch.dtype = torch.float32) -> tuple:
+    """The whole layer for x [T, D] of at most 16 tokens (bfloat16 or float16)
+    without a plan: (y, logits). The tokens are routed by ``logits`` (float32
+    [T, E]) or, with ``w_router`` ([E, D] in x's dtype), by x . w_router^T.
+    Weights as moe_forward takes them, in x's dtype or 4-bit. y is float32 or
+    in x's dtype.
+
+    Pass ``workspace`` (uint8, moe_decode_workspace_bytes) and ``out`` to reuse
+    buffers; calls that may overlap need a workspace each."""
+    L = library()
+    if x.dtype not in (torch.bfloat16, torch.float16) or x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16/float16 tensor")
+    T, D = x.shape
+    dev = x.device
+    if (logits is None) == (w_router is None):
+        raise ValueError("one of logits and w_router must be given")
+    if w_router is not None:
+        if w_router.dtype != x.dtype or w_router.dim() != 2 or w_router.shape[1] != D \
+                or w_router.device != dev:
+            raise ValueError("w_router must be [E, D] in x's dtype, on x's device")
+        E = w_router.shape[0]
+    else:
+        if logits.dtype != torch.float32 or logits.dim() != 2 or logits.shape[0] != T \
+                or logits.device != dev:
+            raise ValueError(f"logits must be a float32 [{T}, E] tensor on x's device")
+        E = logits.shape[1]
+    F, Dw = _dims(w_gate)
+    if Dw != D:
+        raise ValueError(f"weights have d_model {Dw}, x has {D}")
+    _c_int("D", D)
+    _c_int("F", F)
+    d = PlanDesc(T, E, int(k), int(n_shared), float(capacity_factor))
+    _check_weight_shapes(d, w_gate, w_up, w_down, D, F)
+    with _on(dev):
+        x = _aligned(x)
+        w_gate, w_up, w_down = (_aligned_weight(w) for w in (w_gate, w_up, w_down))
+        (wg, _), (wu, _), (wd, _) = (_weight(w, dev) for w in (w_gate, w_up, w_down))
+        if w_router is not None:
+            w_router = _aligned(w_router)
+            logits = torch.empty(T, E, dtype=torch.float32, device=dev)
+            read = logits
+        else:
+            read = _aligned(logits)
+        xdt = _TORCH_TO_MOE[x.dtype]
+        nbytes = L.moe_decode_workspace_bytes(ctypes.byref(d), D, F, xdt, wg.dtype)
+        if nbytes == 0:
+            raise MoeError(MOE_EUNSUPPORTED, moe_last_error())
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty(T, D, dtype=y_dtype, device=dev)
+        if out.dtype not in (torch.float32, x.dtype) or out.shape != (T, D) \
+                or not out.is_contiguous() or out.device != dev:
+            raise ValueError("out must be a contiguous [T, D] f32 or x-dtype tensor on x's device")
+        _check(L.moe_decode(ctypes.byref(d), x.data_ptr(), xdt, _ptr(w_router), read.data_ptr(),
+                            wg, wu, wd, D, F, out.data_ptr(), _TORCH_TO_MOE[out.dtype],
+                            workspace.data_ptr(), nbytes,
+                            None if options is None else ctypes.byref(options), _stream(dev)))
+    return out, logits
+
+
 def _rows_like(t, like, name: str):
     if t.dtype not in _TORCH_TO_MOE or t.shape != like.shape or t.device != like.device:
         raise ValueError(f"{name} must be a float32/bfloat16/float16 tensor of shape "
@@ -1009,3 +1169,6 @@ norm_backward = moe_norm_backward
 quant_f8 = moe_quant_f8
 quant_f8_weights = moe_quant_f8_weights
 gemm_f8 = moe_gemm_f8
+quant_q4_weights = moe_quant_q4_weights
+gemm_q4 = moe_gemm_q4
+decode = moe_decode

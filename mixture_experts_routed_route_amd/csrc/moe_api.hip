@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "f8_internal.h"
+#include "q4_internal.h"
 
 using namespace moe;
 
@@ -620,6 +621,112 @@ size_t moe_forward_workspace_bytes(const moe_plan* p, int32_t D, int32_t F,
   const moe_options o = opt ? *opt : defaults();
   if (w_dtype == MOE_F8B128) return f8_layer_bytes(p->desc, D, F);
   return fwd_layout(p->desc, D, F, x_dtype, w_dtype, o).bytes;
+}
+
+// The workspace of moe_decode: SwiGLU outputs in two parts, routing weights, slots.
+struct FewLayout { size_t h, h_lo, w, slots, bytes; };
+
+static FewLayout few_layout(const moe_plan_desc& d, int F) {
+  FewLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
+  const size_t cap = few_slots(d.T, d.E, d.k, d.n_shared);
+  L.h = take(cap * d.T * F * 2);
+  L.h_lo = take(cap * d.T * F * 2);
+  L.w = take((size_t)d.T * d.E * 4);
+  L.slots = take((1 + 2 * cap) * 4);
+  L.bytes = o;
+  return L;
+}
+
+// What moe_decode takes, MOE_OK or the reason.
+static moe_status few_ok(const moe_plan_desc* d, int D, int F, int xdt, int wdt) {
+  std::string why;
+  if (!desc_ok(d, &why)) return fail(MOE_EINVAL, "%s", why.c_str());
+  if (d->T > kFewT)
+    return fail(MOE_EUNSUPPORTED, "T=%d above %d: moe_forward takes more tokens", d->T, kFewT);
+  if (D <= 0 || F <= 0 || D % 128 || F % 128 || D > kRouterMaxD || F > kRouterMaxD)
+    return fail(MOE_EUNSUPPORTED, "D=%d and F=%d must be multiples of 128 in 128..%d", D, F,
+                kRouterMaxD);
+  if ((xdt != MOE_BF16 && xdt != MOE_F16) || (wdt != xdt && q4_fmt(wdt) < 0))
+    return fail(MOE_EUNSUPPORTED, "dtype pair (x=%d, W=%d): bf16 or f16 x, weights in x's type "
+                "or 4-bit", xdt, wdt);
+  return MOE_OK;
+}
+
+size_t moe_decode_workspace_bytes(const moe_plan_desc* d, int32_t D, int32_t F,
+                                  int32_t x_dtype, int32_t w_dtype) {
+  if (few_ok(d, D, F, x_dtype, w_dtype) != MOE_OK) return 0;
+  return few_layout(*d, F).bytes;
+}
+
+moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
+                      const void* w_router, float* logits, moe_weight w_gate,
+                      moe_weight w_up, moe_weight w_down, int32_t D, int32_t F,
+                      void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                      const moe_options* opt, void* stream) {
+  const int wdt = w_gate.dtype;
+  moe_status st = few_ok(d, D, F, x_dtype, wdt);
+  if (st != MOE_OK) return st;
+  const moe_options o = opt ? *opt : defaults();
+  std::string why;
+  if (!weight_ok(w_gate, wdt, &why, "w_gate") || !weight_ok(w_up, wdt, &why, "w_up") ||
+      !weight_ok(w_down, wdt, &why, "w_down"))
+    return fail(MOE_EINVAL, "%s", why.c_str());
+  if (y_dtype != MOE_F32 && y_dtype != x_dtype)
+    return fail(MOE_EUNSUPPORTED, "y dtype %d must be F32 or x's dtype", y_dtype);
+  if (std::isnan(o.swiglu_limit)) return fail(MOE_EINVAL, "NaN option");
+  if (d->T > 0 && (!x || !logits || !y)) return fail(MOE_EINVAL, "x, logits or y is NULL");
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(logits) || !aligned16(y))
+    return fail(MOE_EINVAL, "x, w_router, logits and y must be 16-byte aligned");
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
+  const FewLayout L = few_layout(*d, F);
+  if (ws_bytes < L.bytes)
+    return fail(MOE_EWORKSPACE, "decode workspace %zu bytes < %zu needed", ws_bytes, L.bytes);
+  if (d->T == 0) return MOE_OK;
+  int dev;
+  DevInfo info;
+  st = device_info(&dev, &info);
+  if (st != MOE_OK) return st;
+  PhaseRecord* rec = nullptr;
+  if (o.flags & MOE_OPT_PHASE_EVENTS) {
+    rec = acquire_record(o.flags, &st);
+    if (!rec) return st;
+  }
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* b = static_cast<char*>(ws);
+  hipError_t e;
+  if (w_router) {
+    PhaseScope ps(rec, 7, s);
+    e = launch_rows_product({x, x_dtype, w_router, nullptr, -1, d->T, d->E, D, logits, MOE_F32},
+                            info.ncu, s);
+    if (e != hipSuccess) return hip_fail(e, "router kernel");
+  }
+  FewArgs a{};
+  a.x = x; a.xdt = x_dtype; a.logits = logits;
+  a.wg = w_gate.data; a.wu = w_up.data; a.wd = w_down.data;
+  a.wgs = w_gate.scales; a.wus = w_up.scales; a.wds = w_down.scales;
+  a.fmt = q4_fmt(wdt);
+  a.T = d->T; a.D = D; a.F = F; a.E = d->E; a.k = d->k; a.n_shared = d->n_shared;
+  const int64_t limit = capacity_limit(*d);
+  a.limit = limit < 0 || limit > d->T ? d->T : (int)limit;
+  a.clamp = o.swiglu_limit;
+  a.h = b + L.h; a.h_lo = b + L.h_lo;
+  a.w = (float*)(b + L.w);
+  a.slots = (int32_t*)(b + L.slots);
+  a.y = y; a.ydt = y_dtype;
+  {
+    PhaseScope ps(rec, 3, s);
+    e = launch_few_gateup(a, info.ncu, s);
+  }
+  if (e != hipSuccess) return hip_fail(e, "decode gate/up kernel");
+  {
+    PhaseScope ps(rec, 5, s);
+    e = launch_few_down(a, s);
+  }
+  if (e != hipSuccess) return hip_fail(e, "decode down kernel");
+  return MOE_OK;
 }
 
 moe_status moe_forward(const moe_plan* p, const void* x, int32_t x_dtype,

@@ -9,23 +9,9 @@
 // the argsort/bincount of minagi/pool.py in mini-AGI PR #3 and #4). Here the
 // grouping is a chunked histogram, a column scan and an in-chunk stable rank:
 // deterministic, with no atomics in any ordering decision.
-#include "moe_internal.h"
+#include "route_key.h"
 
 namespace moe {
-
-// Order-preserving map of a float onto uint32: larger float -> larger key.
-// +0 and -0 map to one key; NaN maps to 0, below -inf (0x007FFFFF).
-__device__ __forceinline__ uint32_t order_key(float f) {
-  uint32_t b = __float_as_uint(f);
-  if ((b & 0x7FFFFFFFu) == 0u) b = 0u;
-  if ((b & 0x7F800000u) == 0x7F800000u && (b & 0x007FFFFFu)) return 0u;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-__device__ __forceinline__ float key_value(uint32_t k) {
-  uint32_t b = (k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k;
-  return __uint_as_float(b);
-}
 
 // One step of a wave-wide max of 64-bit values through DPP (a lane reads
 // another lane's registers in the VALU, no LDS round trip): lanes of the

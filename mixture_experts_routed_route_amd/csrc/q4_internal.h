@@ -1,0 +1,51 @@
+// Internal declarations of the 4-bit quantiser, products on 4-bit weights and
+// the layer for a few tokens.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+// ---- quantiser (quant_q4.hip) ----------------------------------------------
+// values [rows, K] of type dt to codes [rows, K / 2] and parameters of a 4-bit
+// format; K a multiple of its group.
+hipError_t launch_quant_q4(const void* w, int dt, int fmt, int64_t rows, int64_t K, void* data,
+                           void* params, hipStream_t s);
+
+// ---- products (gemm_q4.hip) --------------------------------------------------
+// out[M, N] = x[M, K] . w[N, K]^T; fmt a 4-bit format, or -1: w in x's type
+// (K then a multiple of 128).
+struct RowsArgs {
+  const void* x; int xdt;
+  const void* w; const void* params; int fmt;
+  int64_t M; int N, K;
+  void* out; int odt;
+};
+hipError_t launch_rows_product(const RowsArgs& a, int ncu, hipStream_t s);
+
+// ---- the layer for a few tokens (decode.hip) -----------------------------------
+constexpr int kFewT = MOE_DECODE_MAX_T;
+struct FewArgs {
+  const void* x; int xdt;            // [T, D]
+  const float* logits;               // [T, E]
+  const void* wg; const void* wu; const void* wd;     // [E + n_shared, ..]
+  const void* wgs; const void* wus; const void* wds;  // 4-bit parameters, or null
+  int fmt;                           // 4-bit format, or -1: weights in x's type
+  int T, D, F, E, k, n_shared;
+  int limit;                         // most pairs an expert keeps (T: all)
+  float clamp;
+  // workspace
+  void* h; void* h_lo;               // [slots, T, F] SwiGLU outputs, two 16-bit parts
+  float* w;                          // [T, E] routing weights of chosen experts
+  int32_t* slots;                    // [1 + 2 slots]: their number, experts, token masks
+  void* y; int ydt;                  // [T, D]
+};
+// experts that tokens can choose, and the shared one
+constexpr int few_slots(int T, int E, int k, int n_shared) {
+  const int64_t n = (int64_t)T * k;
+  return (int)(n < E ? n : E) + n_shared;
+}
+hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s);
+hipError_t launch_few_down(const FewArgs& a, hipStream_t s);
+
+}  // namespace moe
