@@ -161,138 +161,171 @@ __device__ __forceinline__ void split_store(S* hi, S* lo, size_t at, float h) {
   lo[at] = (S)(rest == rest ? rest : 0.f);
 }
 
-template <class S, int FMT, int NI, int NB>
-__global__ __launch_bounds__(1024) void few_gateup_kernel(FewArgs a) {
-  extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+template <class S, int FMT, int NI>
+__global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, int KL) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  float* part = lds;                                   // [2][waves][2][NI][64]
-  uint32_t* mask = (uint32_t*)(part + (size_t)4 * waves * NI * 64);   // [E]
+  float* part = (float*)(lds + x_lds_bytes<FMT>(a.T, KL));   // [waves][NI][64]
+  uint32_t* mask = (uint32_t*)(part + kRowWaves * NI * 64);   // [E]
   int* experts = (int*)(mask + a.E);                   // [cap]
   uint32_t* masks = (uint32_t*)(experts + cap);        // [cap]
   int* count = (int*)(masks + cap);
-  const int tok = (lane & 3) * 4 + ((lane >> 2) & 3);
-  const int blocks = a.D / 128, turns = (blocks + waves * NB - 1) / (waves * NB);
-  const S* xr = (const S*)a.x + (size_t)(tok < a.T ? tok : 0) * a.D;
-  XBlock<S, FMT> xb[NB];
-  auto load_x = [&](int turn) {
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int kb = (turn * NB + i) * waves + wave;
-      if (kb < blocks)
-        xb[i] = make_xblock<S, FMT>([&](int step) {
-          const int k = kb * 128 + step * 32 + (lane >> 4) * 8;
-          return tok < a.T ? ldg16(xr + k) : uint4{0u, 0u, 0u, 0u};
-        });
-    }
-  };
-  load_x(0);
-  const int n_slots = route_all(a, mask, experts, masks, count);
+  const S* x = (const S*)a.x;
+  const int blocks = a.D / 128, per = KL / 128;
+  if (per >= blocks) stage_x<S, FMT>(lds, x, a.T, 0, KL, a.D);
+  const int n_slots = __builtin_amdgcn_readfirstlane(route_all(a, mask, experts, masks, count));
   const int strips = a.F / 16, items = n_slots * strips;
-  int half = 0;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int slot = item / strips, f0 = (item - slot * strips) * 16;
-    const size_t n = (size_t)experts[slot] * a.F + f0 + (lane & 15);
-    const WRow rg = weight_row<FMT>(a.wg, a.wgs, n, a.D), ru = weight_row<FMT>(a.wu, a.wus, n, a.D);
-    floatx4 g = {0.f, 0.f, 0.f, 0.f}, u = g;
-    for (int turn = 0; turn < turns; ++turn) {
-      WBlock<FMT> bg[NB], bu[NB];
+  const int split = wave_split(items, blocks, gridDim.x), share = 1 << split;
+  const int mine = wave >> split, q = wave & (share - 1), at_once = kRowWaves >> split;
+  const int rounds = (items + gridDim.x * at_once - 1) / (gridDim.x * at_once);
+  for (int r = 0; r < rounds; ++r) {
+    const int item = (r * at_once + mine) * gridDim.x + blockIdx.x;
+    const bool any = item < items;
+    const int slot = any ? item / strips : 0, f0 = any ? (item - slot * strips) * 16 : 0;
+    const int expert = __builtin_amdgcn_readfirstlane(experts[slot]);
+    const int64_t n0 = (int64_t)expert * a.F + f0;
+    floatx4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const WStrip<FMT> m[2] = {weight_strip<FMT, kWhole>(a.wg, a.wgs, n0 + 16, n0, a.D),
+                              weight_strip<FMT, kWhole>(a.wu, a.wus, n0 + 16, n0, a.D)};
+    for (int b0 = 0; b0 < blocks; b0 += per) {
+      const int n = min(per, blocks - b0);
+      const int first = b0 + n * q / share, end = any ? b0 + n * (q + 1) / share : first;
+      Stream<S, FMT, NI, 2, kWhole> st;
+      st.start(m, first, end, a.D);
+      if (per < blocks) {
+        if (r || b0) __syncthreads();   // all waves are done with the turn before
+        stage_x<S, FMT>(lds, x, a.T, b0 * 128, KL, a.D);
+        __syncthreads();
+      }
+      st.run(m, lds, a.T, KL, b0, first, end, a.D, acc);
+    }
+    if (split) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int kb = (turn * NB + i) * waves + wave;
-        if (kb < blocks) {
-          bg[i] = load_wblock<FMT, false>(rg, kb, 0);
-          bu[i] = load_wblock<FMT, false>(ru, kb, 0);
+      for (int j = 0; j < 2; ++j) {
+        if (r || j) __syncthreads();   // what was there has been read
+#pragma unroll
+        for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = acc[j][e];
+        __syncthreads();
+        if (q == 0) {
+#pragma unroll
+          for (int e = 0; e < NI; ++e)
+            for (int w = 1; w < share; ++w) acc[j][e] += part[((wave + w) * NI + e) * 64 + lane];
         }
       }
-      if (turns > 1) load_x(turn);
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        if ((turn * NB + i) * waves + wave < blocks) {
-          block_product<S, FMT, NI>(xb[i], bg[i], g);
-          block_product<S, FMT, NI>(xb[i], bu[i], u);
-        }
     }
-    float* p = part + half * (2 * waves * NI * 64);
-    half ^= 1;
+    if (any && q == 0) {
+      const uint32_t chosen = masks[slot];
 #pragma unroll
-    for (int e = 0; e < NI; ++e) {
-      p[((wave * 2) * NI + e) * 64 + lane] = g[e];
-      p[((wave * 2 + 1) * NI + e) * 64 + lane] = u[e];
-    }
-    __syncthreads();
-    if (threadIdx.x < 64 * NI) {
-      float sg = 0.f, su = 0.f;
-      for (int w = 0; w < waves; ++w) {
-        sg += p[(w * 2) * NI * 64 + threadIdx.x];
-        su += p[(w * 2 + 1) * NI * 64 + threadIdx.x];
+      for (int e = 0; e < NI; ++e) {
+        const int t = 4 * e + (lane >> 4);
+        if ((chosen >> t) & 1u)   // a token's bit: t < T
+          split_store((S*)a.h, (S*)a.h_lo, ((size_t)slot * a.T + t) * a.F + f0 + (lane & 15),
+                      swiglu(acc[0][e], acc[1][e], a.clamp));
       }
-      const int t = 4 * wave + (lane >> 4);
-      if ((masks[slot] >> t) & 1u)   // a token's bit: t < T
-        split_store((S*)a.h, (S*)a.h_lo, ((size_t)slot * a.T + t) * a.F + f0 + (lane & 15),
-                    swiglu(sg, su, a.clamp));
     }
   }
 }
 
+// A block of 128 of an expert's F in the second launch: weights, both parts of h.
+template <int FMT> struct FewUnit {
+  WBlock<FMT> w;
+  uint4 hi[4], lo[4];
+};
+
 template <class S, class O, int FMT, int NI>
-__global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
-  extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+__global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using V = typename R16<S>::V;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  float* part = lds;                                   // [waves][NI][64]
-  int* experts = (int*)(part + (size_t)waves * NI * 64);   // [cap]
+  float* part = (float*)lds;                           // [waves][NI][64]
+  int* experts = (int*)(part + kRowWaves * NI * 64);   // [cap]
   uint32_t* masks = (uint32_t*)(experts + cap);        // [cap]
-  const int n_slots = a.slots[0];
-  for (int i = threadIdx.x; i < n_slots; i += blockDim.x) {
-    experts[i] = a.slots[1 + i];
-    masks[i] = (uint32_t)a.slots[1 + cap + i];
+  float* weights = (float*)(masks + cap);              // [cap, T]
+  const int n_slots = __builtin_amdgcn_readfirstlane(a.slots[0]);
+  for (int i = threadIdx.x; i < n_slots * a.T; i += blockDim.x) {
+    const int slot = i / a.T, t = i - slot * a.T;
+    const int e = a.slots[1 + slot];
+    const uint32_t m = (uint32_t)a.slots[1 + cap + slot];
+    weights[i] = e < a.E && ((m >> t) & 1u) ? a.w[(size_t)t * a.E + e] : 1.f;
+    if (t == 0) {
+      experts[slot] = e;
+      masks[slot] = m;
+    }
   }
   __syncthreads();
-  const int tok = (lane & 3) * 4 + ((lane >> 2) & 3);
+  const int tok = fragment_token();
   const int blocks = a.F / 128, units = n_slots * blocks;
   const int d0 = blockIdx.x * 16;
+  const uint32_t hbytes = (uint32_t)(a.T * a.F) * 2;
+  // unit u: its loads; a lane whose token did not choose the expert reads zeros
+  auto load = [&](int u) {
+    FewUnit<FMT> n;
+    const bool any = u < units;
+    const int slot = any ? u / blocks : 0, kb = any ? u - slot * blocks : 0;
+    const int expert = __builtin_amdgcn_readfirstlane(experts[slot]);
+    const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
+    const int64_t n0 = (int64_t)expert * a.D + d0;
+    const WStrip<FMT> m = weight_strip<FMT, kWhole>(a.wd, a.wds, n0 + 16, n0, a.F);
+    n.w = load_wblock<FMT, kWhole>(m, kb, any ? blocks : 0, a.F);
+    const auto rh = make_rsrc((const S*)a.h + (size_t)slot * a.T * a.F, hbytes);
+    const auto rl = make_rsrc((const S*)a.h_lo + (size_t)slot * a.T * a.F, hbytes);
+    const uint32_t v = any && ((chosen >> tok) & 1u)
+        ? (uint32_t)(tok * a.F + kb * 128 + (lane >> 4) * 8) * 2 : kPastEnd;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n.hi[i] = buffer16(rh, v + 64 * i, 0);
+      n.lo[i] = buffer16(rl, v + 64 * i, 0);
+    }
+    return n;
+  };
   float sum[NI];
 #pragma unroll
   for (int e = 0; e < NI; ++e) sum[e] = 0.f;
-  using V = typename R16<S>::V;
-  for (int unit = wave; unit < units; unit += waves) {
-    const int slot = unit / blocks, kb = unit - slot * blocks;
-    const int expert = experts[slot];
-    const uint32_t m = masks[slot];
-    const WRow row = weight_row<FMT>(a.wd, a.wds, (size_t)expert * a.D + d0 + (lane & 15), a.F);
-    const WBlock<FMT> wb = load_wblock<FMT, false>(row, kb, 0);
-    const bool mine = (m >> tok) & 1u;
-    const size_t at = ((size_t)slot * a.T + (mine ? tok : 0)) * a.F + kb * 128 + (lane >> 4) * 8;
-    uint4 hi[4], lo[4];
+  FewUnit<FMT> next = load(wave);
+  for (int u = wave; u < units; u += kRowWaves) {
+    const FewUnit<FMT> now = next;
+    next = load(u + kRowWaves);
+    const int slot = u / blocks;
+    const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (FMT < 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hi[i] = mine ? ldg16((const S*)a.h + at + 32 * i) : uint4{0u, 0u, 0u, 0u};
-      lo[i] = mine ? ldg16((const S*)a.h_lo + at + 32 * i) : uint4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < 4; ++i) {
+        acc = mfma16(as_v8<V>(now.lo[i]), as_v8<V>(now.w.q[i]), acc);
+        acc = mfma16(as_v8<V>(now.hi[i]), as_v8<V>(now.w.q[i]), acc);
+      }
+    } else {
+      const Q4Steps<FMT> q = q4_steps<FMT, kWhole>(now.w, 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const V hi = as_v8<V>(q4_order(now.hi[i])), lo = as_v8<V>(q4_order(now.lo[i]));
+        const V w = q4_widen<S, FMT>(q.word[i]);
+        const floatx4 c = x_constant<S, FMT>(hi, x_constant<S, FMT>(lo, floatx4{0.f, 0.f, 0.f, 0.f}));
+        const floatx4 m = mfma16(hi, w, mfma16(lo, w, c));
+#pragma unroll
+        for (int e = 0; e < NI; ++e) {
+          acc[e] = fmaf(q.scale(i), m[e], acc[e]);
+          if constexpr (FMT != 0) acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), c[e], acc[e]);
+        }
+      }
     }
-    float wt[NI];
-    bool in[NI];
+    // a token of another expert takes nothing: its zeros times an infinite weight are NaN
 #pragma unroll
     for (int e = 0; e < NI; ++e) {
       const int t = 4 * e + (lane >> 4);
-      in[e] = (m >> t) & 1u;
-      wt[e] = in[e] && expert < a.E ? a.w[(size_t)t * a.E + expert] : 1.f;
+      if ((chosen >> t) & 1u) sum[e] = fmaf(weights[slot * a.T + t], acc[e], sum[e]);
     }
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-    const XBlock<S, FMT> xh = make_xblock<S, FMT>([&](int i) { return hi[i]; });
-    const XBlock<S, FMT> xl = make_xblock<S, FMT>([&](int i) { return lo[i]; });
-    block_product<S, FMT, NI>(xl, wb, acc);
-    block_product<S, FMT, NI>(xh, wb, acc);
-    // a token of another expert takes nothing: its zeros times an infinite weight are NaN
-#pragma unroll
-    for (int e = 0; e < NI; ++e) sum[e] = in[e] ? fmaf(wt[e], acc[e], sum[e]) : sum[e];
   }
 #pragma unroll
   for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = sum[e];
   __syncthreads();
   if (threadIdx.x < 64 * NI) {
     float v = 0.f;
-    for (int w = 0; w < waves; ++w) v += part[w * NI * 64 + threadIdx.x];
+    for (int w = 0; w < kRowWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
     const int t = 4 * wave + (lane >> 4);
     if (t < a.T) static_cast<O*>(a.y)[(size_t)t * a.D + d0 + (lane & 15)] = (O)v;
   }
@@ -300,20 +333,14 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
 
 template <class S, int FMT>
 hipError_t gateup_launch(const FewArgs& a, int ncu, hipStream_t s) {
-  const int blocks = a.D / 128;
-  const int waves = blocks <= 4 ? 4 : blocks <= 16 ? 8 : 16;
   const int ni = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  const int64_t items = (int64_t)cap * (a.F / 16);
-  const int grid = (int)(items < 4 * ncu ? items : 4 * ncu);
-  const size_t lds = (size_t)4 * waves * ni * 256 + (size_t)4 * (a.E + 2 * cap + 1);
-#define MOE_FEW(NI, NB) \
-  hipLaunchKernelGGL((few_gateup_kernel<S, FMT, NI, NB>), dim3(grid), dim3(64 * waves), lds, s, a)
-  if (blocks <= waves) {
-    if (ni == 1) MOE_FEW(1, 1); else if (ni == 2) MOE_FEW(2, 1); else MOE_FEW(4, 1);
-  } else {
-    if (ni == 1) MOE_FEW(1, 2); else if (ni == 2) MOE_FEW(2, 2); else MOE_FEW(4, 2);
-  }
+  const size_t other = (size_t)kRowWaves * ni * 256 + (size_t)4 * (a.E + 2 * cap + 1);
+  const int KL = lds_turn(x_lds_bytes<FMT>(a.T, 128), x_lds_bytes<FMT>(a.T, 256), other, a.D);
+  const size_t lds = x_lds_bytes<FMT>(a.T, KL) + other;
+#define MOE_FEW(NI) \
+  hipLaunchKernelGGL((few_gateup_kernel<S, FMT, NI>), dim3(ncu), dim3(64 * kRowWaves), lds, s, a, KL)
+  if (ni == 1) MOE_FEW(1); else if (ni == 2) MOE_FEW(2); else MOE_FEW(4);
 #undef MOE_FEW
   return hipGetLastError();
 }
@@ -322,10 +349,9 @@ template <class S, class O, int FMT>
 hipError_t down_launch(const FewArgs& a, hipStream_t s) {
   const int ni = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  const int waves = 16;
-  const size_t lds = (size_t)waves * ni * 256 + (size_t)8 * cap;
+  const size_t lds = (size_t)kRowWaves * ni * 256 + (size_t)4 * cap * (2 + a.T);
 #define MOE_FEW(NI) \
-  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI>), dim3(a.D / 16), dim3(64 * waves), lds, s, a)
+  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI>), dim3(a.D / 16), dim3(64 * kRowWaves), lds, s, a)
   if (ni == 1) MOE_FEW(1); else if (ni == 2) MOE_FEW(2); else MOE_FEW(4);
 #undef MOE_FEW
   return hipGetLastError();

@@ -12,87 +12,83 @@ __device__ __forceinline__ void store_out(void* out, size_t at, float v) {
   static_cast<O*>(out)[at] = (O)v;
 }
 
-// Up to 16 rows of x against strips of 16 weight rows. A workgroup's waves share
-// K: wave w holds blocks w, w + waves, .. of x's rows as fragments for all its
-// strips, and the waves' sums meet in LDS. K beyond waves * NB blocks goes in
-// turns that load x again.
-template <class S, class O, int FMT, int NI, int NB, bool RAGGED>
-__global__ __launch_bounds__(1024) void rows_strip_kernel(RowsArgs a) {
-  extern __shared__ float part[];   // [2][waves][NI][64]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+// Up to 16 rows of x against strips of 16 weight rows. Every wave streams its own
+// part of a strip against x in LDS, without a barrier; where there are fewer strips
+// than waves, up to 16 waves share one's blocks and their sums meet in LDS. K whose
+// rows do not fit LDS goes in turns of KL values.
+template <class S, class O, int FMT, int NI, int RAGGED>
+__global__ __launch_bounds__(64 * kRowWaves) void rows_strip_kernel(RowsArgs a, int KL) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = (int64_t)blockIdx.y * 16;
   const int T = (int)min<int64_t>(16, a.M - t0);
-  const int tok = (lane & 3) * 4 + ((lane >> 2) & 3);   // the token of A's row lane & 15
-  const int pieces = a.K / 32, blocks = (a.K + 127) / 128;
-  const int turns = (blocks + waves * NB - 1) / (waves * NB);
-  const S* xr = (const S*)a.x + (size_t)(t0 + (tok < T ? tok : 0)) * a.K;
-  XBlock<S, FMT> xb[NB];
-  auto load_x = [&](int turn) {
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int kb = (turn * NB + i) * waves + wave;
-      if (kb < blocks)
-        xb[i] = make_xblock<S, FMT>([&](int step) {
-          const int k = kb * 128 + step * 32 + (lane >> 4) * 8;
-          return tok < T && (!RAGGED || k < a.K) ? ldg16(xr + k) : uint4{0u, 0u, 0u, 0u};
-        });
-    }
-  };
-  load_x(0);
-  const int strips = (a.N + 15) / 16;
-  int turn_of = 0;
-  for (int strip = blockIdx.x; strip < strips; strip += gridDim.x) {
-    const int n = min(strip * 16 + (lane & 15), a.N - 1);
-    const WRow row = weight_row<FMT>(a.w, a.params, (size_t)n, a.K);
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int turn = 0; turn < turns; ++turn) {
-      WBlock<FMT> wb[NB];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int kb = (turn * NB + i) * waves + wave;
-        if (kb < blocks) wb[i] = load_wblock<FMT, RAGGED>(row, kb, pieces);
+  const S* x = (const S*)a.x + (size_t)t0 * a.K;
+  float* part = (float*)(lds + x_lds_bytes<FMT>(T, KL));   // [waves][NI][64], shared strips
+  const int blocks = (a.K + 127) / 128, per = KL / 128;
+  const int strips = (int)(((int64_t)a.N + 15) / 16);
+  const int split = wave_split(strips, blocks, gridDim.x), share = 1 << split;
+  const int mine = wave >> split, q = wave & (share - 1), at_once = kRowWaves >> split;
+  const int rounds = (strips + gridDim.x * at_once - 1) / (gridDim.x * at_once);
+  for (int r = 0; r < rounds; ++r) {
+    // neighbouring workgroups take neighbouring strips
+    const int strip = (r * at_once + mine) * gridDim.x + blockIdx.x;
+    const bool any = strip < strips;
+    floatx4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+    const WStrip<FMT> m[1] = {
+        weight_strip<FMT, RAGGED>(a.w, a.params, a.N, any ? (int64_t)strip * 16 : 0, a.K)};
+    for (int b0 = 0; b0 < blocks; b0 += per) {
+      const int n = min(per, blocks - b0);
+      const int first = b0 + n * q / share, end = any ? b0 + n * (q + 1) / share : first;
+      Stream<S, FMT, NI, 1, RAGGED> st;
+      st.start(m, first, end, a.K);
+      if (r == 0 || per < blocks) {
+        if (r || b0) __syncthreads();   // all waves are done with the turn before
+        stage_x<S, FMT>(lds, x, T, b0 * 128, KL, a.K);
+        __syncthreads();
       }
-      if (turns > 1) load_x(turn);
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        if ((turn * NB + i) * waves + wave < blocks) block_product<S, FMT, NI>(xb[i], wb[i], acc);
+      st.run(m, lds, T, KL, b0, first, end, a.K, acc);
     }
-    float* p = part + turn_of * (waves * NI * 64);
+    if (split) {
+      if (r) __syncthreads();   // the round before has been read
 #pragma unroll
-    for (int e = 0; e < NI; ++e) p[(wave * NI + e) * 64 + lane] = acc[e];
-    __syncthreads();
-    // the other half of `part` takes the next strip: one barrier a strip
-    turn_of ^= 1;
-    if (threadIdx.x < 64 * NI) {
-      float sum = 0.f;
-      for (int w = 0; w < waves; ++w) sum += p[w * NI * 64 + threadIdx.x];
-      const int t = 4 * wave + (lane >> 4), c = strip * 16 + (lane & 15);
-      if (t < T && c < a.N) store_out<O>(a.out, (size_t)(t0 + t) * a.N + c, sum);
+      for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = acc[0][e];
+      __syncthreads();
+      if (q == 0) {
+#pragma unroll
+        for (int e = 0; e < NI; ++e)
+          for (int w = 1; w < share; ++w) acc[0][e] += part[((wave + w) * NI + e) * 64 + lane];
+      }
+    }
+    if (any && q == 0) {
+      const int n = strip * 16 + (lane & 15);
+#pragma unroll
+      for (int e = 0; e < NI; ++e) {
+        const int t = 4 * e + (lane >> 4);
+        if (t < T && n < a.N) store_out<O>(a.out, (size_t)(t0 + t) * a.N + n, acc[0][e]);
+      }
     }
   }
 }
 
-template <class S, class O, int FMT, bool RAGGED>
+template <class S, class O, int FMT, int RAGGED>
 hipError_t strip_launch(const RowsArgs& a, int ncu, hipStream_t s) {
-  const int blocks = (a.K + 127) / 128, strips = (a.N + 15) / 16;
-  const int waves = blocks <= 4 ? 4 : blocks <= 16 ? 8 : 16;
+  const int strips = (int)(((int64_t)a.N + 15) / 16);
   const int64_t chunks = (a.M + 15) / 16;
-  const int ni = a.M <= 4 ? 1 : a.M <= 8 ? 2 : 4;
-  const int gx = strips < 2 * ncu ? strips : 2 * ncu;
+  const int T = (int)(a.M < 16 ? a.M : 16), ni = T <= 4 ? 1 : T <= 8 ? 2 : 4;
+  const int gx = strips < ncu ? strips : ncu;
+  const size_t part = (size_t)kRowWaves * ni * 256;
+  const int KL = lds_turn(x_lds_bytes<FMT>(T, 128), x_lds_bytes<FMT>(T, 256), part, a.K);
+  const size_t lds = x_lds_bytes<FMT>(T, KL) + part;
   for (int64_t c = 0; c < chunks; c += 32768) {
     RowsArgs b = a;
     b.x = (const S*)a.x + (size_t)c * 16 * a.K;
     b.out = (O*)a.out + (size_t)c * 16 * a.N;
     b.M = a.M - c * 16;
-    const dim3 grid(gx, (unsigned)(chunks - c < 32768 ? chunks - c : 32768)), block(64 * waves);
-    const size_t lds = (size_t)2 * waves * ni * 256;
-#define MOE_STRIP(NI, NB) \
-  hipLaunchKernelGGL((rows_strip_kernel<S, O, FMT, NI, NB, RAGGED>), grid, block, lds, s, b)
-    if (blocks <= waves) {
-      if (ni == 1) MOE_STRIP(1, 1); else if (ni == 2) MOE_STRIP(2, 1); else MOE_STRIP(4, 1);
-    } else {
-      if (ni == 1) MOE_STRIP(1, 2); else if (ni == 2) MOE_STRIP(2, 2); else MOE_STRIP(4, 2);
-    }
+    const dim3 grid(gx, (unsigned)(chunks - c < 32768 ? chunks - c : 32768)), block(64 * kRowWaves);
+#define MOE_STRIP(NI) \
+  hipLaunchKernelGGL((rows_strip_kernel<S, O, FMT, NI, RAGGED>), grid, block, lds, s, b, KL)
+    if (ni == 1) MOE_STRIP(1); else if (ni == 2) MOE_STRIP(2); else MOE_STRIP(4);
 #undef MOE_STRIP
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -102,11 +98,13 @@ hipError_t strip_launch(const RowsArgs& a, int ncu, hipStream_t s) {
 
 template <class S, class O>
 hipError_t by_format(const RowsArgs& a, int ncu, hipStream_t s) {
-  const bool ragged = a.K % 128 != 0;
+  const bool whole = a.K % 128 == 0;
   switch (a.fmt) {
-    case 0: return ragged ? strip_launch<S, O, 0, true>(a, ncu, s) : strip_launch<S, O, 0, false>(a, ncu, s);
-    case 1: return ragged ? strip_launch<S, O, 1, true>(a, ncu, s) : strip_launch<S, O, 1, false>(a, ncu, s);
-    case 2: return ragged ? strip_launch<S, O, 2, true>(a, ncu, s) : strip_launch<S, O, 2, false>(a, ncu, s);
+    case 0:
+      return whole ? strip_launch<S, O, 0, kWhole>(a, ncu, s)
+           : a.K % 64 ? strip_launch<S, O, 0, kOdd>(a, ncu, s) : strip_launch<S, O, 0, kWords>(a, ncu, s);
+    case 1: return whole ? strip_launch<S, O, 1, kWhole>(a, ncu, s) : strip_launch<S, O, 1, kWords>(a, ncu, s);
+    case 2: return whole ? strip_launch<S, O, 2, kWhole>(a, ncu, s) : strip_launch<S, O, 2, kWords>(a, ncu, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -115,7 +113,7 @@ template <class S>
 hipError_t by_output(const RowsArgs& a, int ncu, hipStream_t s) {
   if (a.fmt < 0) {   // the router's map
     if (a.odt != MOE_F32 || a.K % 128) return hipErrorInvalidValue;
-    return strip_launch<S, float, -1, false>(a, ncu, s);
+    return strip_launch<S, float, -1, kWhole>(a, ncu, s);
   }
   return a.odt == MOE_F32 ? by_format<S, float>(a, ncu, s)
        : a.odt == MOE_BF16 ? by_format<S, __bf16>(a, ncu, s) : by_format<S, _Float16>(a, ncu, s);

@@ -6,6 +6,18 @@
 
 namespace moe {
 
+// Bytes of LDS a workgroup may use.
+constexpr size_t kLdsBytes = 160 * 1024;
+
+// Values of K that a workgroup's x takes in LDS at once: all (up to a multiple of
+// 128), or the most that fit beside `other` bytes; one and two blocks take b1 and
+// b2 bytes.
+inline int lds_turn(size_t b1, size_t b2, size_t other, int K) {
+  const int64_t all = ((int64_t)K + 127) / 128;
+  const int64_t fit = 1 + (int64_t)((kLdsBytes - other - b1) / (b2 - b1));
+  return (int)(128 * (all < fit ? all : fit));
+}
+
 // ---- quantiser (quant_q4.hip) ----------------------------------------------
 // values [rows, K] of type dt to codes [rows, K / 2] and parameters of a 4-bit
 // format; K a multiple of its group.

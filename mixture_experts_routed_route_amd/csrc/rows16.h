@@ -82,63 +82,104 @@ __device__ __forceinline__ uint4 lane_group_transpose(uint4 v) {
   return uint4{c[0], c[1], d[0], d[1]};
 }
 
-// A block of 128 values of 16 rows, as loaded. FMT -1: 16-bit weights.
+// A block of 128 values of 16 rows, as loaded. FMT -1: 16-bit weights, lane l of
+// load i the values 32 i + 8 (l >> 4) .. of row l & 15, as the matrix instruction
+// takes them. 4-bit: lane l the 32 codes ("piece") l & 3 of row l >> 2, so that
+// neighbouring lanes read neighbouring bytes (the cache takes one access for 64
+// such bytes, not four; with a row a lane its accesses bound the stream at 3.5
+// TB/s), and in lanes 0 .. 15 the parameters of row l.
 template <int FMT> struct WBlock {
   uint4 q;
   uint32_t p[FMT == 1 ? 4 : 2];
 };
 template <> struct WBlock<-1> { uint4 q[4]; };
 
-// A lane's weight row: its first byte and its parameters' first byte.
-struct WRow { const char* q; const char* p; };
+// Where a row's length leaves the last block short: not at all (K a multiple of
+// 128); rows of whole 4-byte words of parameters; rows of an odd number of 2-byte
+// scales.
+enum Ragged : int { kWhole = 0, kWords = 1, kOdd = 2 };
 
-// Row n of a [rows, K] matrix of format FMT.
-template <int FMT>
-__device__ __forceinline__ WRow weight_row(const void* data, const void* params, size_t n, int K) {
-  if constexpr (FMT < 0) return {(const char*)data + n * (size_t)K * 2, nullptr};
-  else return {(const char*)data + n * (size_t)(K / 2),
-               (const char*)params + n * (size_t)(K / Q4F<FMT>::kGroup) * Q4F<FMT>::kPB};
+// 16 weight rows: descriptors of their bytes and parameters (scalar) and the
+// lane's place in them. Rows past the matrix's last (and blocks past the end, see
+// load_wblock) read as zeros, without a memory access.
+template <int FMT> struct WStrip {
+  __amdgpu_buffer_rsrc_t q, p;
+  const char* prow;          // kOdd: the lane's row of parameters
+  uint32_t vq, vp;
+};
+
+__device__ __forceinline__ uint4 buffer16(__amdgpu_buffer_rsrc_t r, uint32_t v, uint32_t s) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, v, s, 0));
+}
+__device__ __forceinline__ uint2 buffer8(__amdgpu_buffer_rsrc_t r, uint32_t v, uint32_t s) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, v, s, 0));
 }
 
-// Block kb (values 128 kb ..) of the lane's row. Lane group g loads bytes 16 g
-// of each 64. RAGGED: K is no multiple of 128, and pieces of 32 values behind
-// the row's last (pieces = K / 32) are read from the last with parameters of
-// zero (x's fragments are zero there).
-template <int FMT, bool RAGGED>
-__device__ __forceinline__ WBlock<FMT> load_wblock(const WRow& r, int kb, int pieces) {
-  const int g = (threadIdx.x >> 4) & 3;
-  WBlock<FMT> b;
+// a lane's offset past every descriptor's end (the scalar offset is left out of the
+// range check)
+constexpr uint32_t kPastEnd = 0x80000000u;
+
+// Rows n0 .. of the matrix [N, K] at data / params.
+template <int FMT, int RAGGED>
+__device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void* params, int64_t N,
+                                                    int64_t n0, int K) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t rows = (uint32_t)(N - n0 < 16 ? N - n0 : 16);
+  WStrip<FMT> r;
+  const uint32_t rb = FMT < 0 ? (uint32_t)K * 2 : (uint32_t)K / 2;
+  r.q = make_rsrc((const char*)data + n0 * (int64_t)rb, rows * rb);
+  r.prow = nullptr;
   if constexpr (FMT < 0) {
-    static_assert(!RAGGED, "16-bit weights come in whole blocks");
+    r.vq = (lane & 15) * rb + (lane >> 4) * 16u;
+    r.vp = 0;
+    r.p = r.q;
+  } else {
+    using Q = Q4F<FMT>;
+    const uint32_t pb = (uint32_t)(K / Q::kGroup) * Q::kPB;
+    const char* p = (const char*)params + n0 * (int64_t)pb;
+    r.vq = (lane >> 2) * rb + (lane & 3) * 16u;
+    r.p = make_rsrc(p, rows * pb);
+    r.vp = lane < 16 ? lane * pb : kPastEnd;
+    if constexpr (RAGGED == kOdd) r.prow = p + (size_t)((lane & 15) < rows ? lane & 15 : 0u) * pb;
+  }
+  return r;
+}
+
+// Block kb (values 128 kb ..) of the strip; kb >= end gives zeros. In a short last
+// block the pieces behind the row's end have parameters of zero (their codes are the
+// next row's, x's fragments are zero there).
+template <int FMT, int RAGGED>
+__device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb, int end, int K) {
+  WBlock<FMT> b;
+  const uint32_t at = (uint32_t)(kb < end ? kb : end - 1);
+  const uint32_t v = kb < end ? r.vq : kPastEnd;
+  if constexpr (FMT < 0) {
+    static_assert(RAGGED == kWhole, "16-bit weights come in whole blocks");
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b.q[i] = ldg16(r.q + (size_t)kb * 256 + 64 * i + 16 * g);
+    for (int i = 0; i < 4; ++i) b.q[i] = buffer16(r.q, v + 64u * i, at * 256u);
   } else {
     using Q = Q4F<FMT>;
     constexpr int kP = FMT == 1 ? 4 : 2;
-    const int piece = 4 * kb + g;
-    b.q = ldg16(r.q + (size_t)(RAGGED ? min(piece, pieces - 1) : piece) * 16);
-    const char* p = r.p + (size_t)kb * (128 / Q::kGroup) * Q::kPB;
-    if (!RAGGED || 4 * kb + 4 <= pieces) {
-      // rows of an odd number of parameters start on two or four bytes
-      if constexpr (RAGGED) __builtin_memcpy(b.p, p, 4 * kP);
-      else __builtin_memcpy(b.p, __builtin_assume_aligned(p, 4), 4 * kP);
-    } else {
-      const int left = pieces - 4 * kb;   // 1 .. 3 pieces
-#pragma unroll
-      for (int i = 0; i < kP; ++i) b.p[i] = 0u;
-      if constexpr (FMT == 0) {
-        for (int i = 0; i < left; ++i) {
-          const uint32_t s = *reinterpret_cast<const uint16_t*>(p + 2 * i);
-          if (i < 2) b.p[0] |= s << (16 * i);
-          else b.p[1] = s;
-        }
+    constexpr uint32_t kPer = 128 / Q::kGroup * Q::kPB;
+    b.q = buffer16(r.q, v, at * 64u);
+    if constexpr (RAGGED != kOdd) {
+      const uint32_t vp = kb < end ? r.vp : kPastEnd;
+      if constexpr (FMT == 1) {
+        const uint4 w = buffer16(r.p, vp, at * kPer);
+        b.p[0] = w.x; b.p[1] = w.y; b.p[2] = w.z; b.p[3] = w.w;
       } else {
-        // a64 rows are whole pairs of pieces
-        const int n = FMT == 1 ? left : left / 2;
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-          if (i < n) b.p[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+        const uint2 w = buffer8(r.p, vp, at * kPer);
+        b.p[0] = w.x; b.p[1] = w.y;
       }
+    } else {
+      static_assert(RAGGED != kOdd || FMT == 0, "only scales alone have two bytes");
+      const int left = kb < end ? K / 32 - 4 * kb : 0;   // pieces
+      const char* p = r.prow + (size_t)at * kPer;
+      b.p[0] = b.p[1] = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left)
+          b.p[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * i) << (16 * (i & 1));
     }
   }
   return b;
@@ -151,22 +192,82 @@ template <class S, int FMT> struct XBlock {
   floatx4 c[FMT < 0 ? 1 : 4];
 };
 
-// x16(step): the lane's eight values of a step (zero past K), in order.
-template <class S, int FMT, class F>
-__device__ __forceinline__ XBlock<S, FMT> make_xblock(F&& x16) {
+// -off * the sum over a step's values, of every token
+template <class S, int FMT>
+__device__ __forceinline__ floatx4 x_constant(typename R16<S>::V v, floatx4 c) {
+  typename R16<S>::V k;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) k[j] = (S)(-kQ4Off<S, FMT>);
+  return mfma16(v, k, c);
+}
+
+// The token in row lane & 15 of a fragment.
+__device__ __forceinline__ int fragment_token() {
+  return (threadIdx.x & 3) * 4 + ((threadIdx.x >> 2) & 3);
+}
+
+// x of up to 16 tokens over K values in LDS, for all waves of a workgroup: rows of
+// K values and 16 bytes (so that 16 rows at one place lie in different banks),
+// in the codes' order for 4-bit weights, then their constants, 16 floats a step.
+template <int FMT>
+constexpr size_t x_lds_bytes(int T, int K) {
+  return (size_t)T * (K * 2 + 16) + (FMT < 0 ? 0 : (size_t)K / 32 * 64);
+}
+
+// Values k0 .. k0 + KL of rows of x (K values apart; zeros from K on), KL a
+// multiple of 128. The caller waits at a barrier.
+template <class S, int FMT>
+__device__ __forceinline__ void stage_x(char* lds, const S* x, int T, int k0, int KL, int K) {
   using V = typename R16<S>::V;
+  constexpr int kAhead = 4;   // loads in flight
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int tok = fragment_token(), steps = KL / 32, stride = KL * 2 + 16;
+  const auto rsrc = make_rsrc(x, (uint32_t)T * (uint32_t)K * 2u);
+  float* c = (float*)(lds + (size_t)T * stride);
+  for (int f0 = wave; f0 < steps; f0 += waves * kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + 32 * (f0 + i * waves) + (lane >> 4) * 8;
+      // lanes without a token, and values behind the row, read zeros
+      v[i] = buffer16(rsrc, tok < T && k < K ? (uint32_t)(tok * K + k) * 2u : kPastEnd, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int f = f0 + i * waves;
+      if (f >= steps) break;
+      if constexpr (FMT >= 0) {
+        v[i] = q4_order(v[i]);
+        const floatx4 s = x_constant<S, FMT>(as_v8<V>(v[i]), floatx4{0.f, 0.f, 0.f, 0.f});
+        if ((lane & 15) == 0) *reinterpret_cast<floatx4*>(c + f * 16 + (lane >> 4) * 4) = s;
+      }
+      if (tok < T) *reinterpret_cast<uint4*>(lds + tok * stride + f * 64 + (lane >> 4) * 16) = v[i];
+    }
+  }
+}
+
+// Block kb of the staged x; lanes of rows past T read the first. NI as below.
+template <class S, int FMT, int NI>
+__device__ __forceinline__ XBlock<S, FMT> x_block(const char* lds, int T, int KL, int kb) {
+  using V = typename R16<S>::V;
+  const int lane = threadIdx.x & 63, tok = fragment_token(), stride = KL * 2 + 16;
+  const char* p = lds + (tok < T ? tok : 0) * stride + kb * 256 + (lane >> 4) * 16;
+  const char* c = lds + (size_t)T * stride + kb * 256 + (lane >> 4) * 16;
   XBlock<S, FMT> b;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint4 v = x16(i);
-    if constexpr (FMT < 0) {
-      b.v[i] = as_v8<V>(v);
-    } else {
-      b.v[i] = as_v8<V>(q4_order(v));
-      V k;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) k[j] = (S)(-kQ4Off<S, FMT>);
-      b.c[i] = mfma16(b.v[i], k, floatx4{0.f, 0.f, 0.f, 0.f});
+    b.v[i] = as_v8<V>(*reinterpret_cast<const uint4*>(p + 64 * i));
+    if constexpr (FMT >= 0) {
+      // elements from NI on go nowhere
+      if constexpr (NI == 4) b.c[i] = *reinterpret_cast<const floatx4*>(c + 64 * i);
+      else if constexpr (NI == 2) {
+        const float2 h = *reinterpret_cast<const float2*>(c + 64 * i);
+        b.c[i] = floatx4{h.x, h.y, h.y, h.y};
+      } else {
+        const float h = *reinterpret_cast<const float*>(c + 64 * i);
+        b.c[i] = floatx4{h, h, h, h};
+      }
     }
   }
   return b;
@@ -179,36 +280,118 @@ __device__ __forceinline__ float half_hi(uint32_t w) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
 }
 
-// acc[i] += the block's products of the lane's tokens 4 i + (lane >> 4) with
+// Lane l of 0 .. 15's value in lanes l, 16 + l, 32 + l and 48 + l.
+__device__ __forceinline__ uint32_t lane_group_bcast(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false)[0];
+}
+
+// Lane 4 r + p's word to lane r + 16 p.
+__device__ __forceinline__ uint4 rows_to_columns(uint4 v) {
+  const int lane = threadIdx.x & 63, from = ((lane & 15) * 4 + (lane >> 4)) * 4;
+  return uint4{(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.x),
+               (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.y),
+               (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.z),
+               (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.w)};
+}
+
+// A block's four steps of 4-bit weights, ready for the matrix instruction: words of
+// eight codes (row lane & 15), parameters of the lane's row.
+template <int FMT> struct Q4Steps {
+  uint32_t word[4];
+  uint32_t p[FMT == 1 ? 4 : 2];
+  __device__ __forceinline__ float scale(int i) const {
+    if constexpr (FMT == 0) return i & 1 ? half_hi(p[i / 2]) : half_lo(p[i / 2]);
+    else return half_lo(p[FMT == 1 ? i : i / 2]);
+  }
+  __device__ __forceinline__ float bias(int i) const {
+    static_assert(FMT != 0, "a signed code has no bias");
+    return half_hi(p[FMT == 1 ? i : i / 2]);
+  }
+};
+
+// left: pieces from the block's first to the row's end.
+template <int FMT, int RAGGED>
+__device__ __forceinline__ Q4Steps<FMT> q4_steps(const WBlock<FMT>& w, int left) {
+  Q4Steps<FMT> s;
+  const uint4 t = lane_group_transpose(rows_to_columns(w.q));
+  s.word[0] = t.x; s.word[1] = t.y; s.word[2] = t.z; s.word[3] = t.w;
+#pragma unroll
+  for (int i = 0; i < (FMT == 1 ? 4 : 2); ++i) {
+    s.p[i] = RAGGED == kOdd ? w.p[i] : lane_group_bcast(w.p[i]);
+    if constexpr (RAGGED == kWords)
+      if ((FMT == 1 ? i : 2 * i) >= left) s.p[i] = 0u;
+  }
+  return s;
+}
+
+// acc[i] += the block's products of the lane's tokens 4 i + (lane >> 4), i < NI, with
 // its weight row.
-template <class S, int FMT, int NI>
-__device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const WBlock<FMT>& w,
+template <class S, int FMT, int NI, int RAGGED>
+__device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const WBlock<FMT>& w, int left,
                                               floatx4& acc) {
   using V = typename R16<S>::V;
   if constexpr (FMT < 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc = mfma16(x.v[i], as_v8<V>(w.q[i]), acc);
   } else {
-    const uint4 t = lane_group_transpose(w.q);
-    const uint32_t words[4] = {t.x, t.y, t.z, t.w};
+    const Q4Steps<FMT> q = q4_steps<FMT, RAGGED>(w, left);
+    // two matrix instructions before the sums of the first are needed
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const floatx4 m = mfma16(x.v[i], q4_widen<S, FMT>(words[i]), x.c[i]);
-      float s, b = 0.f;
-      if constexpr (FMT == 0) {
-        s = i & 1 ? half_hi(w.p[i / 2]) : half_lo(w.p[i / 2]);
-      } else {
-        const uint32_t sb = w.p[FMT == 1 ? i : i / 2];
-        s = half_lo(sb);
-        b = half_hi(sb) * (-1.f / kQ4Off<S, FMT>);   // c holds -off sum x; exact
-      }
+    for (int h = 0; h < 4; h += 2) {
+      floatx4 m[2];
 #pragma unroll
-      for (int e = 0; e < NI; ++e) {
-        acc[e] = fmaf(s, m[e], acc[e]);
-        if constexpr (FMT != 0) acc[e] = fmaf(b, x.c[i][e], acc[e]);
+      for (int i = 0; i < 2; ++i) m[i] = mfma16(x.v[h + i], q4_widen<S, FMT>(q.word[h + i]), x.c[h + i]);
+#pragma unroll
+      for (int i = h; i < h + 2; ++i)
+#pragma unroll
+        for (int e = 0; e < NI; ++e) {
+          acc[e] = fmaf(q.scale(i), m[i - h][e], acc[e]);
+          // c holds -off sum x; the quotient is exact
+          if constexpr (FMT != 0) acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), x.c[i][e], acc[e]);
+        }
+    }
+  }
+}
+
+// A wave's stream: blocks first .. end - 1 of MATS strips against the staged x
+// (whose block 0 is block k0b of the rows), kDepth blocks of each strip in flight.
+template <class S, int FMT, int NI, int MATS, int RAGGED> struct Stream {
+  // as many as 128 registers a wave hold without spills
+  static constexpr int kDepth = (FMT < 0 ? 4 : FMT == 1 || NI > 1 ? 6 : 8) / MATS;
+  WBlock<FMT> buf[kDepth][MATS];
+
+  __device__ __forceinline__ void start(const WStrip<FMT> (&m)[MATS], int first, int end, int K) {
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i)
+#pragma unroll
+      for (int j = 0; j < MATS; ++j) buf[i][j] = load_wblock<FMT, RAGGED>(m[j], first + i, end, K);
+  }
+  __device__ __forceinline__ void run(const WStrip<FMT> (&m)[MATS], const char* lds, int T, int KL, int k0b,
+                                      int first, int end, int K, floatx4 (&acc)[MATS]) {
+    for (int kb = first; kb < end; kb += kDepth) {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        if (kb + i >= end) break;
+        const XBlock<S, FMT> x = x_block<S, FMT, NI>(lds, T, KL, kb + i - k0b);
+#pragma unroll
+        for (int j = 0; j < MATS; ++j) {
+          block_product<S, FMT, NI, RAGGED>(x, buf[i][j], K / 32 - 4 * (kb + i), acc[j]);
+          buf[i][j] = load_wblock<FMT, RAGGED>(m[j], kb + i + kDepth, end, K);
+        }
       }
     }
   }
+};
+
+// A workgroup has kRowWaves waves; 1 << split of them share a strip's blocks. The
+// fewest that give every wave of the launch a part of `strips` strips of `blocks`
+// blocks each.
+constexpr int kRowWaves = 16;
+__device__ __forceinline__ int wave_split(int64_t strips, int blocks, int workgroups) {
+  int s = 0;
+  while (s < 4 && (strips << s) < (int64_t)workgroups * kRowWaves && (2 << s) <= blocks) ++s;
+  return s;
 }
 
 }  // namespace moe
