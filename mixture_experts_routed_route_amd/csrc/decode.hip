@@ -43,22 +43,30 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   return v;
 }
 
-// The tokens that chose each expert, as bits of mask[e] (LDS, zeroed); weights
-// (global [T, E], chosen entries) where weights is not null. PER logits a lane.
+// Words of 64 experts that a token's choices take.
+__device__ __forceinline__ int choice_words(int E) { return (E + 63) / 64; }
+
+// Each token's k experts, as bits of chosen[t][e / 64] (LDS), a wave a token; its
+// weights (global [T, E], chosen entries) where weights is not null. PER = words.
 // Ties go to the lower expert, NaN ranks below -inf, as in moe_plan_create.
 template <int PER>
-__device__ __forceinline__ void route_tokens(const FewArgs& a, uint32_t* mask, float* weights) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+__device__ __forceinline__ void route_tokens(const FewArgs& a, uint64_t* chosen, float* weights) {
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int t = wave; t < a.T; t += waves) {
     float l[PER];
-    uint32_t key[PER], sel = 0u, top = 0u;
+    uint32_t key[PER], top = 0u;
+    uint64_t sel[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       const int e = lane + 64 * p;
       l[p] = e < a.E ? a.logits[(size_t)t * a.E + e] : 0.f;
     }
 #pragma unroll
-    for (int p = 0; p < PER; ++p) key[p] = lane + 64 * p < a.E ? order_key(l[p]) + 1u : 0u;   // 0: none
+    for (int p = 0; p < PER; ++p) {
+      key[p] = lane + 64 * p < a.E ? order_key(l[p]) + 1u : 0u;   // 0: none
+      sel[p] = 0ull;
+    }
     for (int j = 0; j < a.k; ++j) {
       uint32_t m = key[0];
 #pragma unroll
@@ -69,25 +77,24 @@ __device__ __forceinline__ void route_tokens(const FewArgs& a, uint32_t* mask, f
 #pragma unroll
       for (int p = 0; p < PER; ++p) {
         const uint64_t at = __ballot(key[p] == m);
-        if (open && at) {
-          open = false;
-          if (lane == __builtin_ctzll(at)) {
-            key[p] = 0u;
-            sel |= 1u << p;
-          }
-        }
+        const uint64_t bit = open ? at & (0ull - at) : 0ull;
+        open = open && !at;
+        sel[p] |= bit;
+        if ((bit >> lane) & 1ull) key[p] = 0u;
       }
     }
+    if (lane == 0) {
 #pragma unroll
-    for (int p = 0; p < PER; ++p)
-      if ((sel >> p) & 1u) atomicOr(&mask[lane + 64 * p], 1u << t);
+      for (int p = 0; p < PER; ++p)
+        if (64 * p < a.E) chosen[t * choice_words(a.E) + p] = sel[p];
+    }
     if (!weights) continue;
     const float l0 = key_value(top - 1u);
     float ex[PER], sum = 0.f;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       ex[p] = 0.f;
-      if ((sel >> p) & 1u) {
+      if ((sel[p] >> lane) & 1ull) {
         // exp(l - l0): the difference's rounding error is put back
         const float d = l[p] - l0, back = d + l0;
         const float err = (l[p] - back) + ((back - d) - l0);
@@ -99,57 +106,75 @@ __device__ __forceinline__ void route_tokens(const FewArgs& a, uint32_t* mask, f
     sum = wave_sum_f(sum);
 #pragma unroll
     for (int p = 0; p < PER; ++p)
-      if ((sel >> p) & 1u) weights[(size_t)t * a.E + lane + 64 * p] = ex[p] / sum;
+      if ((sel[p] >> lane) & 1ull) weights[(size_t)t * a.E + lane + 64 * p] = ex[p] / sum;
   }
 }
 
-// Routing of all tokens: the experts in use, in order, and their tokens' masks
-// after the limit, in LDS (experts[slot], masks[slot]); returns their number.
-// The first workgroup writes them and the weights for the second launch.
-__device__ __forceinline__ int route_all(const FewArgs& a, uint32_t* mask, int* experts, uint32_t* masks,
-                                         int* count) {
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) mask[e] = 0u;
-  __syncthreads();
+// Expert 64 p + lane's tokens, as bits, after the limit (its first tokens stay).
+__device__ __forceinline__ uint32_t tokens_of(const FewArgs& a, const uint64_t* chosen, int p) {
+  const int lane = threadIdx.x & 63, words = choice_words(a.E);
+  uint32_t m = 0u;
+  for (int t = 0; t < a.T; ++t) m |= (uint32_t)((chosen[t * words + p] >> lane) & 1ull) << t;
+  for (int over = __popc(m) - a.limit; over > 0; --over) m &= ~(0x80000000u >> __clz((int)m));
+  return m;
+}
+
+// The experts in use, in order, then the shared one: their number; and expert and
+// tokens of number `slot` (or of none). Every wave for itself.
+__device__ __forceinline__ int experts_in_use(const FewArgs& a, const uint64_t* chosen) {
+  int n = 0;
+  for (int p = 0; p < choice_words(a.E); ++p) n += __popcll(__ballot(tokens_of(a, chosen, p) != 0u));
+  return n + a.n_shared;
+}
+__device__ __forceinline__ void expert_of(const FewArgs& a, const uint64_t* chosen, int slot, int* expert,
+                                          uint32_t* tokens) {
+  *expert = a.E;
+  *tokens = (1u << a.T) - 1u;
+  int n = 0;
+  for (int p = 0; p < choice_words(a.E); ++p) {
+    const uint32_t m = tokens_of(a, chosen, p);
+    uint64_t used = __ballot(m != 0u);
+    const int here = __popcll(used);
+    if (slot < n + here) {   // wave-uniform
+      for (int i = n; i < slot; ++i) used &= used - 1ull;
+      const int l = __builtin_ctzll(used);
+      *expert = 64 * p + l;
+      *tokens = (uint32_t)__builtin_amdgcn_readlane((int)m, l);
+      return;
+    }
+    n += here;
+  }
+}
+
+// Routing of all tokens into chosen[T][words] (LDS); the first workgroup writes what
+// the second launch reads: the weights, and the experts in use with their tokens.
+__device__ __forceinline__ void route_all(const FewArgs& a, uint64_t* chosen) {
   float* weights = blockIdx.x == 0 ? a.w : nullptr;
-  if (a.E <= 128) route_tokens<2>(a, mask, weights);
-  else if (a.E <= 256) route_tokens<4>(a, mask, weights);
-  else route_tokens<16>(a, mask, weights);
+  if (a.E <= 128) route_tokens<2>(a, chosen, weights);
+  else if (a.E <= 256) route_tokens<4>(a, chosen, weights);
+  else route_tokens<16>(a, chosen, weights);
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
+  if (blockIdx.x == 0 && threadIdx.x < 64) {
+    const int lane = threadIdx.x, cap = few_slots(a.T, a.E, a.k, a.n_shared);
     int n = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-      uint32_t m = e0 + lane < a.E ? mask[e0 + lane] : 0u;
-      // the first `limit` tokens stay
-      for (int over = __popc(m) - a.limit; over > 0; --over) m &= ~(0x80000000u >> __clz((int)m));
+    for (int p = 0; p < choice_words(a.E); ++p) {
+      const uint32_t m = tokens_of(a, chosen, p);
       const uint64_t used = __ballot(m != 0u);
       if (m) {
         const int at = n + __popcll(used & ((1ull << lane) - 1ull));
-        experts[at] = e0 + lane;
-        masks[at] = m;
+        a.slots[1 + at] = 64 * p + lane;
+        a.slots[1 + cap + at] = (int32_t)m;
       }
       n += __popcll(used);
     }
-    if (a.n_shared) {
-      if (lane == 0) {
-        experts[n] = a.E;
-        masks[n] = (1u << a.T) - 1u;
+    if (lane == 0) {
+      if (a.n_shared) {
+        a.slots[1 + n] = a.E;
+        a.slots[1 + cap + n] = (int32_t)((1u << a.T) - 1u);
       }
-      ++n;
+      a.slots[0] = n + a.n_shared;
     }
-    if (lane == 0) *count = n;
   }
-  __syncthreads();
-  const int n = *count;
-  if (blockIdx.x == 0) {
-    const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      a.slots[1 + i] = experts[i];
-      a.slots[1 + cap + i] = (int32_t)masks[i];
-    }
-    if (threadIdx.x == 0) a.slots[0] = n;
-  }
-  return n;
 }
 
 template <class S>
@@ -166,17 +191,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
   float* part = (float*)(lds + x_lds_bytes<FMT>(a.T, KL));   // [waves][NI][64]
-  uint32_t* mask = (uint32_t*)(part + kRowWaves * NI * 64);   // [E]
-  int* experts = (int*)(mask + a.E);                   // [cap]
-  uint32_t* masks = (uint32_t*)(experts + cap);        // [cap]
-  int* count = (int*)(masks + cap);
+  uint64_t* chosen = (uint64_t*)(part + kRowWaves * NI * 64);   // [T][words]
   const S* x = (const S*)a.x;
   const int blocks = a.D / 128, per = KL / 128;
-  if (per >= blocks) stage_x<S, FMT>(lds, x, a.T, 0, KL, a.D);
-  const int n_slots = __builtin_amdgcn_readfirstlane(route_all(a, mask, experts, masks, count));
-  const int strips = a.F / 16, items = n_slots * strips;
+  route_all(a, chosen);
+  const int strips = a.F / 16, items = experts_in_use(a, chosen) * strips;
   const int split = wave_split(items, blocks, gridDim.x), share = 1 << split;
   const int mine = wave >> split, q = wave & (share - 1), at_once = kRowWaves >> split;
   const int rounds = (items + gridDim.x * at_once - 1) / (gridDim.x * at_once);
@@ -184,7 +204,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
     const int item = (r * at_once + mine) * gridDim.x + blockIdx.x;
     const bool any = item < items;
     const int slot = any ? item / strips : 0, f0 = any ? (item - slot * strips) * 16 : 0;
-    const int expert = __builtin_amdgcn_readfirstlane(experts[slot]);
+    int expert;
+    uint32_t tokens;
+    expert_of(a, chosen, slot, &expert, &tokens);
     const int64_t n0 = (int64_t)expert * a.F + f0;
     floatx4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     const WStrip<FMT> m[2] = {weight_strip<FMT, kWhole>(a.wg, a.wgs, n0 + 16, n0, a.D),
@@ -194,7 +216,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
       const int first = b0 + n * q / share, end = any ? b0 + n * (q + 1) / share : first;
       Stream<S, FMT, NI, 2, kWhole> st;
       st.start(m, first, end, a.D);
-      if (per < blocks) {
+      if (r == 0 || per < blocks) {
         if (r || b0) __syncthreads();   // all waves are done with the turn before
         stage_x<S, FMT>(lds, x, a.T, b0 * 128, KL, a.D);
         __syncthreads();
@@ -208,36 +230,38 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
 #pragma unroll
         for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = acc[j][e];
         __syncthreads();
-        if (q == 0) {
-#pragma unroll
-          for (int e = 0; e < NI; ++e)
-            for (int w = 1; w < share; ++w) acc[j][e] += part[((wave + w) * NI + e) * 64 + lane];
-        }
+        if (q == 0) add_shared<NI>(part, wave, share, acc[j]);
       }
     }
     if (any && q == 0) {
-      const uint32_t chosen = masks[slot];
+      // beside 4-bit weights h lies in the codes' order within each eight values
+      const int f = lane & 15, at = FMT < 0 ? f : (f & 8) | ((f & 3) << 1) | ((f >> 2) & 1);
 #pragma unroll
       for (int e = 0; e < NI; ++e) {
         const int t = 4 * e + (lane >> 4);
-        if ((chosen >> t) & 1u)   // a token's bit: t < T
-          split_store((S*)a.h, (S*)a.h_lo, ((size_t)slot * a.T + t) * a.F + f0 + (lane & 15),
+        if ((tokens >> t) & 1u)   // a token's bit: t < T
+          split_store((S*)a.h, (S*)a.h_lo, ((size_t)slot * a.T + t) * a.F + f0 + at,
                       swiglu(acc[0][e], acc[1][e], a.clamp));
       }
     }
   }
 }
 
-// A block of 128 of an expert's F in the second launch: weights, both parts of h.
-template <int FMT> struct FewUnit {
+// kN neighbouring blocks of 128 of an expert's F in the second launch. R = 16 output
+// columns: one block. R = 8: two, the first's weight rows as rows 0 .. 7 of the strip,
+// the second's as rows 8 .. 15; each block's h is multiplied by all 16, and the half
+// of the products that belongs to the other block goes nowhere.
+template <int FMT, int R> struct FewUnit {
+  static constexpr int kN = 16 / R;
   WBlock<FMT> w;
-  uint4 hi[4], lo[4];
+  uint4 hi[kN][4], lo[kN][4];
 };
 
-template <class S, class O, int FMT, int NI>
+template <class S, class O, int FMT, int NI, int R>
 __global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using V = typename R16<S>::V;
+  constexpr int kN = 16 / R;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
@@ -246,70 +270,98 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
   uint32_t* masks = (uint32_t*)(experts + cap);        // [cap]
   float* weights = (float*)(masks + cap);              // [cap, T]
   const int n_slots = __builtin_amdgcn_readfirstlane(a.slots[0]);
-  for (int i = threadIdx.x; i < n_slots * a.T; i += blockDim.x) {
-    const int slot = i / a.T, t = i - slot * a.T;
-    const int e = a.slots[1 + slot];
-    const uint32_t m = (uint32_t)a.slots[1 + cap + slot];
-    weights[i] = e < a.E && ((m >> t) & 1u) ? a.w[(size_t)t * a.E + e] : 1.f;
-    if (t == 0) {
-      experts[slot] = e;
-      masks[slot] = m;
-    }
+  for (int i = threadIdx.x; i < cap; i += blockDim.x) {   // those from n_slots on are not used
+    experts[i] = a.slots[1 + i];
+    masks[i] = (uint32_t)a.slots[1 + cap + i];
   }
   __syncthreads();
   const int tok = fragment_token();
-  const int blocks = a.F / 128, units = n_slots * blocks;
-  const int d0 = blockIdx.x * 16;
+  const int blocks = a.F / 128, per = (blocks + kN - 1) / kN, units = n_slots * per;
+  const int d0 = blockIdx.x * R;
   const uint32_t hbytes = (uint32_t)(a.T * a.F) * 2;
-  // unit u: its loads; a lane whose token did not choose the expert reads zeros
+  const uint32_t rb = FMT < 0 ? (uint32_t)a.F * 2 : (uint32_t)a.F / 2;
+  // the block of a unit that this lane loads weights (parameters) of
+  const bool second = kN == 2 && (FMT < 0 ? (lane & 15) >= 8 : lane >= 32);
+  const bool second_p = kN == 2 && (lane & 15) >= 8;
   auto load = [&](int u) {
-    FewUnit<FMT> n;
+    FewUnit<FMT, R> n;
     const bool any = u < units;
-    const int slot = any ? u / blocks : 0, kb = any ? u - slot * blocks : 0;
+    const int slot = any ? u / per : 0, kb = any ? (u - slot * per) * kN : 0;
     const int expert = __builtin_amdgcn_readfirstlane(experts[slot]);
     const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
     const int64_t n0 = (int64_t)expert * a.D + d0;
-    const WStrip<FMT> m = weight_strip<FMT, kWhole>(a.wd, a.wds, n0 + 16, n0, a.F);
+    WStrip<FMT> m = weight_strip<FMT, kWhole>(a.wd, a.wds, n0 + R, n0, a.F);
+    if constexpr (kN == 2) {
+      const bool odd = kb + 1 >= blocks;   // no second block
+      if (second) m.vq = odd ? kPastEnd : m.vq - 8u * rb + (FMT < 0 ? 256u : 64u);
+      if constexpr (FMT >= 0) {
+        using Q = Q4F<FMT>;
+        if (second_p && lane < 16)
+          m.vp = odd ? kPastEnd : m.vp - 8u * ((uint32_t)(a.F / Q::kGroup) * Q::kPB) + 128 / Q::kGroup * Q::kPB;
+      }
+    }
     n.w = load_wblock<FMT, kWhole>(m, kb, any ? blocks : 0, a.F);
     const auto rh = make_rsrc((const S*)a.h + (size_t)slot * a.T * a.F, hbytes);
     const auto rl = make_rsrc((const S*)a.h_lo + (size_t)slot * a.T * a.F, hbytes);
-    const uint32_t v = any && ((chosen >> tok) & 1u)
-        ? (uint32_t)(tok * a.F + kb * 128 + (lane >> 4) * 8) * 2 : kPastEnd;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      n.hi[i] = buffer16(rh, v + 64 * i, 0);
-      n.lo[i] = buffer16(rl, v + 64 * i, 0);
+    for (int j = 0; j < kN; ++j) {
+      // a lane whose token did not choose the expert reads zeros
+      const uint32_t v = any && kb + j < blocks && ((chosen >> tok) & 1u)
+          ? (uint32_t)(tok * a.F + (kb + j) * 128 + (lane >> 4) * 8) * 2 : kPastEnd;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        n.hi[j][i] = buffer16(rh, v + 64 * i, 0);
+        n.lo[j][i] = buffer16(rl, v + 64 * i, 0);
+      }
     }
     return n;
   };
   float sum[NI];
 #pragma unroll
   for (int e = 0; e < NI; ++e) sum[e] = 0.f;
-  FewUnit<FMT> next = load(wave);
+  FewUnit<FMT, R> next = load(wave);
+  for (int i = threadIdx.x; i < n_slots * a.T; i += blockDim.x) {
+    const int slot = i / a.T, t = i - slot * a.T, e = experts[slot];
+    weights[i] = e < a.E && ((masks[slot] >> t) & 1u) ? a.w[(size_t)t * a.E + e] : 1.f;
+  }
+  __syncthreads();
   for (int u = wave; u < units; u += kRowWaves) {
-    const FewUnit<FMT> now = next;
+    const FewUnit<FMT, R> now = next;
     next = load(u + kRowWaves);
-    const int slot = u / blocks;
+    const int slot = u / per;
     const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
     floatx4 acc = {0.f, 0.f, 0.f, 0.f};
     if constexpr (FMT < 0) {
+      floatx4 p[kN];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc = mfma16(as_v8<V>(now.lo[i]), as_v8<V>(now.w.q[i]), acc);
-        acc = mfma16(as_v8<V>(now.hi[i]), as_v8<V>(now.w.q[i]), acc);
+      for (int j = 0; j < kN; ++j) {
+        p[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[j] = mfma16(as_v8<V>(now.lo[j][i]), as_v8<V>(now.w.q[i]), p[j]);
+          p[j] = mfma16(as_v8<V>(now.hi[j][i]), as_v8<V>(now.w.q[i]), p[j]);
+        }
       }
+#pragma unroll
+      for (int e = 0; e < NI; ++e) acc[e] = kN == 2 && second_p ? p[kN - 1][e] : p[0][e];
     } else {
       const Q4Steps<FMT> q = q4_steps<FMT, kWhole>(now.w, 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const V hi = as_v8<V>(q4_order(now.hi[i])), lo = as_v8<V>(q4_order(now.lo[i]));
         const V w = q4_widen<S, FMT>(q.word[i]);
-        const floatx4 c = x_constant<S, FMT>(hi, x_constant<S, FMT>(lo, floatx4{0.f, 0.f, 0.f, 0.f}));
-        const floatx4 m = mfma16(hi, w, mfma16(lo, w, c));
+        floatx4 m[kN], c[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          const V hi = as_v8<V>(now.hi[j][i]), lo = as_v8<V>(now.lo[j][i]);
+          c[j] = x_constant<S, FMT>(hi, x_constant<S, FMT>(lo, floatx4{0.f, 0.f, 0.f, 0.f}));
+          m[j] = mfma16(hi, w, mfma16(lo, w, c[j]));
+        }
 #pragma unroll
         for (int e = 0; e < NI; ++e) {
-          acc[e] = fmaf(q.scale(i), m[e], acc[e]);
-          if constexpr (FMT != 0) acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), c[e], acc[e]);
+          const bool o = kN == 2 && second_p;
+          acc[e] = fmaf(q.scale(i), o ? m[kN - 1][e] : m[0][e], acc[e]);
+          if constexpr (FMT != 0)
+            acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), o ? c[kN - 1][e] : c[0][e], acc[e]);
         }
       }
     }
@@ -325,17 +377,18 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
   __syncthreads();
   if (threadIdx.x < 64 * NI) {
     float v = 0.f;
+#pragma unroll
     for (int w = 0; w < kRowWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
-    const int t = 4 * wave + (lane >> 4);
-    if (t < a.T) static_cast<O*>(a.y)[(size_t)t * a.D + d0 + (lane & 15)] = (O)v;
+    if constexpr (kN == 2) v += __shfl_xor(v, 8);
+    const int t = 4 * wave + (lane >> 4), c = lane & 15;
+    if (t < a.T && c < R) static_cast<O*>(a.y)[(size_t)t * a.D + d0 + c] = (O)v;
   }
 }
 
 template <class S, int FMT>
 hipError_t gateup_launch(const FewArgs& a, int ncu, hipStream_t s) {
   const int ni = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
-  const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  const size_t other = (size_t)kRowWaves * ni * 256 + (size_t)4 * (a.E + 2 * cap + 1);
+  const size_t other = (size_t)kRowWaves * ni * 256 + (size_t)8 * a.T * ((a.E + 63) / 64);
   const int KL = lds_turn(x_lds_bytes<FMT>(a.T, 128), x_lds_bytes<FMT>(a.T, 256), other, a.D);
   const size_t lds = x_lds_bytes<FMT>(a.T, KL) + other;
 #define MOE_FEW(NI) \
@@ -346,13 +399,17 @@ hipError_t gateup_launch(const FewArgs& a, int ncu, hipStream_t s) {
 }
 
 template <class S, class O, int FMT>
-hipError_t down_launch(const FewArgs& a, hipStream_t s) {
+hipError_t down_launch(const FewArgs& a, int ncu, hipStream_t s) {
   const int ni = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
   const size_t lds = (size_t)kRowWaves * ni * 256 + (size_t)4 * cap * (2 + a.T);
-#define MOE_FEW(NI) \
-  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI>), dim3(a.D / 16), dim3(64 * kRowWaves), lds, s, a)
-  if (ni == 1) MOE_FEW(1); else if (ni == 2) MOE_FEW(2); else MOE_FEW(4);
+#define MOE_FEW(NI, R) \
+  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI, R>), dim3(a.D / R), dim3(64 * kRowWaves), lds, s, a)
+  if (a.D / 16 >= ncu) {
+    if (ni == 1) MOE_FEW(1, 16); else if (ni == 2) MOE_FEW(2, 16); else MOE_FEW(4, 16);
+  } else {
+    if (ni == 1) MOE_FEW(1, 8); else if (ni == 2) MOE_FEW(2, 8); else MOE_FEW(4, 8);
+  }
 #undef MOE_FEW
   return hipGetLastError();
 }
@@ -369,12 +426,12 @@ hipError_t gateup_fmt(const FewArgs& a, int ncu, hipStream_t s) {
 }
 
 template <class S, class O>
-hipError_t down_fmt(const FewArgs& a, hipStream_t s) {
+hipError_t down_fmt(const FewArgs& a, int ncu, hipStream_t s) {
   switch (a.fmt) {
-    case -1: return down_launch<S, O, -1>(a, s);
-    case 0: return down_launch<S, O, 0>(a, s);
-    case 1: return down_launch<S, O, 1>(a, s);
-    case 2: return down_launch<S, O, 2>(a, s);
+    case -1: return down_launch<S, O, -1>(a, ncu, s);
+    case 0: return down_launch<S, O, 0>(a, ncu, s);
+    case 1: return down_launch<S, O, 1>(a, ncu, s);
+    case 2: return down_launch<S, O, 2>(a, ncu, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -387,11 +444,11 @@ hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_few_down(const FewArgs& a, hipStream_t s) {
+hipError_t launch_few_down(const FewArgs& a, int ncu, hipStream_t s) {
   if (a.xdt == MOE_BF16)
-    return a.ydt == MOE_F32 ? down_fmt<__bf16, float>(a, s) : down_fmt<__bf16, __bf16>(a, s);
+    return a.ydt == MOE_F32 ? down_fmt<__bf16, float>(a, ncu, s) : down_fmt<__bf16, __bf16>(a, ncu, s);
   if (a.xdt == MOE_F16)
-    return a.ydt == MOE_F32 ? down_fmt<_Float16, float>(a, s) : down_fmt<_Float16, _Float16>(a, s);
+    return a.ydt == MOE_F32 ? down_fmt<_Float16, float>(a, ncu, s) : down_fmt<_Float16, _Float16>(a, ncu, s);
   return hipErrorInvalidValue;
 }
 

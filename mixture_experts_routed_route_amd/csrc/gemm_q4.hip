@@ -54,11 +54,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_strip_kernel(RowsArgs a, 
 #pragma unroll
       for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = acc[0][e];
       __syncthreads();
-      if (q == 0) {
-#pragma unroll
-        for (int e = 0; e < NI; ++e)
-          for (int w = 1; w < share; ++w) acc[0][e] += part[((wave + w) * NI + e) * 64 + lane];
-      }
+      if (q == 0) add_shared<NI>(part, wave, share, acc[0]);
     }
     if (any && q == 0) {
       const int n = strip * 16 + (lane & 15);

@@ -723,7 +723,7 @@ moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
   if (e != hipSuccess) return hip_fail(e, "decode gate/up kernel");
   {
     PhaseScope ps(rec, 5, s);
-    e = launch_few_down(a, s);
+    e = launch_few_down(a, info.ncu, s);
   }
   if (e != hipSuccess) return hip_fail(e, "decode down kernel");
   return MOE_OK;

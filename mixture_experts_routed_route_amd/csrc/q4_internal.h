@@ -58,6 +58,6 @@ constexpr int few_slots(int T, int E, int k, int n_shared) {
   return (int)(n < E ? n : E) + n_shared;
 }
 hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s);
-hipError_t launch_few_down(const FewArgs& a, hipStream_t s);
+hipError_t launch_few_down(const FewArgs& a, int ncu, hipStream_t s);
 
 }  // namespace moe

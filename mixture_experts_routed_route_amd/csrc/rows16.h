@@ -259,15 +259,12 @@ __device__ __forceinline__ XBlock<S, FMT> x_block(const char* lds, int T, int KL
   for (int i = 0; i < 4; ++i) {
     b.v[i] = as_v8<V>(*reinterpret_cast<const uint4*>(p + 64 * i));
     if constexpr (FMT >= 0) {
-      // elements from NI on go nowhere
-      if constexpr (NI == 4) b.c[i] = *reinterpret_cast<const floatx4*>(c + 64 * i);
-      else if constexpr (NI == 2) {
-        const float2 h = *reinterpret_cast<const float2*>(c + 64 * i);
-        b.c[i] = floatx4{h.x, h.y, h.y, h.y};
-      } else {
-        const float h = *reinterpret_cast<const float*>(c + 64 * i);
-        b.c[i] = floatx4{h, h, h, h};
-      }
+      // elements from NI on go nowhere: whatever their registers hold
+      floatx4 h;
+      if constexpr (NI == 4) h = *reinterpret_cast<const floatx4*>(c + 64 * i);
+#pragma unroll
+      for (int e = 0; e < NI && NI < 4; ++e) h[e] = reinterpret_cast<const float*>(c + 64 * i)[e];
+      b.c[i] = h;
     }
   }
   return b;
@@ -282,8 +279,7 @@ __device__ __forceinline__ float half_hi(uint32_t w) {
 
 // Lane l of 0 .. 15's value in lanes l, 16 + l, 32 + l and 48 + l.
 __device__ __forceinline__ uint32_t lane_group_bcast(uint32_t v) {
-  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false)[0];
+  return (uint32_t)__builtin_amdgcn_ds_bpermute((threadIdx.x & 15) * 4, (int)v);
 }
 
 // Lane 4 r + p's word to lane r + 16 p.
@@ -356,42 +352,67 @@ __device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const WBl
 
 // A wave's stream: blocks first .. end - 1 of MATS strips against the staged x
 // (whose block 0 is block k0b of the rows), kDepth blocks of each strip in flight.
+// A block of 4-bit codes is half a cache line of each row: two are asked for back to
+// back, or the line would be fetched twice.
 template <class S, int FMT, int NI, int MATS, int RAGGED> struct Stream {
+  static constexpr int kPair = FMT < 0 ? 1 : 2;
   // as many as 128 registers a wave hold without spills
-  static constexpr int kDepth = (FMT < 0 ? 4 : FMT == 1 || NI > 1 ? 6 : 8) / MATS;
+  static constexpr int kDepth = FMT < 0 ? 4 / MATS : (MATS == 1 ? (FMT == 1 || NI > 1 ? 6 : 8) : 4);
   WBlock<FMT> buf[kDepth][MATS];
 
   __device__ __forceinline__ void start(const WStrip<FMT> (&m)[MATS], int first, int end, int K) {
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i)
+    for (int i = 0; i < kDepth; i += kPair) fill(m, i, first + i, end, K);
+  }
+  __device__ __forceinline__ void fill(const WStrip<FMT> (&m)[MATS], int i, int kb, int end, int K) {
 #pragma unroll
-      for (int j = 0; j < MATS; ++j) buf[i][j] = load_wblock<FMT, RAGGED>(m[j], first + i, end, K);
+    for (int j = 0; j < MATS; ++j)
+#pragma unroll
+      for (int h = 0; h < kPair; ++h) buf[i + h][j] = load_wblock<FMT, RAGGED>(m[j], kb + h, end, K);
   }
   __device__ __forceinline__ void run(const WStrip<FMT> (&m)[MATS], const char* lds, int T, int KL, int k0b,
                                       int first, int end, int K, floatx4 (&acc)[MATS]) {
     for (int kb = first; kb < end; kb += kDepth) {
 #pragma unroll
-      for (int i = 0; i < kDepth; ++i) {
-        if (kb + i >= end) break;
-        const XBlock<S, FMT> x = x_block<S, FMT, NI>(lds, T, KL, kb + i - k0b);
+      for (int i = 0; i < kDepth; i += kPair) {
 #pragma unroll
-        for (int j = 0; j < MATS; ++j) {
-          block_product<S, FMT, NI, RAGGED>(x, buf[i][j], K / 32 - 4 * (kb + i), acc[j]);
-          buf[i][j] = load_wblock<FMT, RAGGED>(m[j], kb + i + kDepth, end, K);
+        for (int h = 0; h < kPair; ++h) {
+          if (kb + i + h >= end) break;
+          const XBlock<S, FMT> x = x_block<S, FMT, NI>(lds, T, KL, kb + i + h - k0b);
+#pragma unroll
+          for (int j = 0; j < MATS; ++j)
+            block_product<S, FMT, NI, RAGGED>(x, buf[i + h][j], K / 32 - 4 * (kb + i + h), acc[j]);
         }
+        if (kb + i >= end) break;
+        fill(m, i, kb + i + kDepth, end, K);
       }
     }
   }
 };
 
-// A workgroup has kRowWaves waves; 1 << split of them share a strip's blocks. The
-// fewest that give every wave of the launch a part of `strips` strips of `blocks`
-// blocks each.
+// A workgroup has kRowWaves waves; 1 << split of them share a strip's blocks: the
+// most that still give each strip its waves at once.
 constexpr int kRowWaves = 16;
 __device__ __forceinline__ int wave_split(int64_t strips, int blocks, int workgroups) {
   int s = 0;
-  while (s < 4 && (strips << s) < (int64_t)workgroups * kRowWaves && (2 << s) <= blocks) ++s;
+  while (s < 4 && (strips << (s + 1)) <= (int64_t)workgroups * kRowWaves && (2 << s) <= blocks) ++s;
   return s;
+}
+
+// The sums of the waves that share a strip, in the first of them (wave a multiple
+// of share): part [waves][NI][64] of all waves, between barriers.
+template <int NI>
+__device__ __forceinline__ void add_shared(const float* part, int wave, int share, floatx4& acc) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int e = 0; e < NI; ++e) {
+    float v[kRowWaves];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w)
+      v[w] = w < share ? part[((wave + w) * NI + e) * 64 + lane] : 0.f;
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) acc[e] += v[w];
+  }
 }
 
 }  // namespace moe
