@@ -177,13 +177,14 @@ __device__ __forceinline__ void route_all(const FewArgs& a, uint64_t* chosen) {
   }
 }
 
+// h's rounding at h[at], the rest at h[at + F].
 template <class S>
-__device__ __forceinline__ void split_store(S* hi, S* lo, size_t at, float h) {
-  const S v = (S)h;
-  hi[at] = v;
+__device__ __forceinline__ void split_store(S* h, size_t at, int F, float v) {
+  const S hi = (S)v;
+  h[at] = hi;
   // an infinity stays one: inf - inf would make the sum of the parts a NaN
-  const float rest = h - (float)v;
-  lo[at] = (S)(rest == rest ? rest : 0.f);
+  const float rest = v - (float)hi;
+  h[at + F] = (S)(rest == rest ? rest : 0.f);
 }
 
 template <class S, int FMT, int NI>
@@ -240,33 +241,43 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
       for (int e = 0; e < NI; ++e) {
         const int t = 4 * e + (lane >> 4);
         if ((tokens >> t) & 1u)   // a token's bit: t < T
-          split_store((S*)a.h, (S*)a.h_lo, ((size_t)slot * a.T + t) * a.F + f0 + at,
+          split_store((S*)a.h, ((size_t)slot * a.T + t) * 2 * a.F + f0 + at, a.F,
                       swiglu(acc[0][e], acc[1][e], a.clamp));
       }
     }
   }
 }
 
-// kN neighbouring blocks of 128 of an expert's F in the second launch. R = 16 output
-// columns: one block. R = 8: two, the first's weight rows as rows 0 .. 7 of the strip,
-// the second's as rows 8 .. 15; each block's h is multiplied by all 16, and the half
+// What a wave of the second launch takes at once: R = 16 output columns of kW blocks of
+// 128 of an expert's F (4-bit: two, a cache line of each row; else one), or R = 8
+// columns of two blocks, the first's weight rows as rows 0 .. 7 of a strip, the second's
+// as rows 8 .. 15; each of the kN blocks' h is then multiplied by all 16, and the half
 // of the products that belongs to the other block goes nowhere.
-template <int FMT, int R> struct FewUnit {
-  static constexpr int kN = 16 / R;
-  WBlock<FMT> w;
-  uint4 hi[kN][4], lo[kN][4];
+// h's two parts: up to 8 tokens have both in one fragment (PARTS 1: row 2 t of h and row
+// 2 t + 1 are two of its 16), more have a fragment of each (PARTS 2).
+template <int FMT, int R, int PARTS> struct FewUnit {
+  static constexpr int kW = R == 8 || FMT < 0 ? 1 : 2;
+  static constexpr int kN = R == 8 || FMT >= 0 ? 2 : 1;
+  WBlock<FMT> w[kW];
+  uint4 h[kN][PARTS][4];
 };
 
-template <class S, class O, int FMT, int NI, int R>
-__global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
+// Waves of a workgroup: h's fragments of more than 8 tokens beside 4-bit weights take
+// half of a compute unit's registers in 8.
+template <int FMT, int PARTS> constexpr int kDownWaves = FMT >= 0 && PARTS == 2 ? 8 : 16;
+
+template <class S, class O, int FMT, int NI, int R, int PARTS>
+__global__ __launch_bounds__(64 * (kDownWaves<FMT, PARTS>)) void few_down_kernel(FewArgs a) {
+  constexpr int kWaves = kDownWaves<FMT, PARTS>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using V = typename R16<S>::V;
-  constexpr int kN = 16 / R;
+  using U = FewUnit<FMT, R, PARTS>;
+  constexpr int kN = U::kN, kW = U::kW;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
   float* part = (float*)lds;                           // [waves][NI][64]
-  int* experts = (int*)(part + kRowWaves * NI * 64);   // [cap]
+  int* experts = (int*)(part + kWaves * NI * 64);   // [cap]
   uint32_t* masks = (uint32_t*)(experts + cap);        // [cap]
   float* weights = (float*)(masks + cap);              // [cap, T]
   const int n_slots = __builtin_amdgcn_readfirstlane(a.slots[0]);
@@ -275,59 +286,63 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
     masks[i] = (uint32_t)a.slots[1 + cap + i];
   }
   __syncthreads();
-  const int tok = fragment_token();
   const int blocks = a.F / 128, per = (blocks + kN - 1) / kN, units = n_slots * per;
   const int d0 = blockIdx.x * R;
-  const uint32_t hbytes = (uint32_t)(a.T * a.F) * 2;
+  const uint32_t hbytes = (uint32_t)(a.T * a.F) * 4;
   const uint32_t rb = FMT < 0 ? (uint32_t)a.F * 2 : (uint32_t)a.F / 2;
-  // the block of a unit that this lane loads weights (parameters) of
-  const bool second = kN == 2 && (FMT < 0 ? (lane & 15) >= 8 : lane >= 32);
-  const bool second_p = kN == 2 && (lane & 15) >= 8;
+  // R = 8: whether this lane's weights (parameters, products) are the second block's
+  const bool second = FMT < 0 ? (lane & 15) >= 8 : lane >= 32, second_col = (lane & 15) >= 8;
+  // the row of h in the lane's row of a fragment: 2 t + part, or 2 t
+  const int vrow = PARTS == 1 ? fragment_token() : 2 * fragment_token();
+  // units go to the waves in runs
+  const int first = units * wave / kWaves, last = units * (wave + 1) / kWaves;
   auto load = [&](int u) {
-    FewUnit<FMT, R> n;
-    const bool any = u < units;
+    U n;
+    const bool any = u < last;
     const int slot = any ? u / per : 0, kb = any ? (u - slot * per) * kN : 0;
     const int expert = __builtin_amdgcn_readfirstlane(experts[slot]);
     const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
     const int64_t n0 = (int64_t)expert * a.D + d0;
     WStrip<FMT> m = weight_strip<FMT, kWhole>(a.wd, a.wds, n0 + R, n0, a.F);
-    if constexpr (kN == 2) {
+    if constexpr (R == 8) {
       const bool odd = kb + 1 >= blocks;   // no second block
       if (second) m.vq = odd ? kPastEnd : m.vq - 8u * rb + (FMT < 0 ? 256u : 64u);
       if constexpr (FMT >= 0) {
         using Q = Q4F<FMT>;
-        if (second_p && lane < 16)
+        if (second_col && lane < 16)
           m.vp = odd ? kPastEnd : m.vp - 8u * ((uint32_t)(a.F / Q::kGroup) * Q::kPB) + 128 / Q::kGroup * Q::kPB;
       }
     }
-    n.w = load_wblock<FMT, kWhole>(m, kb, any ? blocks : 0, a.F);
-    const auto rh = make_rsrc((const S*)a.h + (size_t)slot * a.T * a.F, hbytes);
-    const auto rl = make_rsrc((const S*)a.h_lo + (size_t)slot * a.T * a.F, hbytes);
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+      n.w[j] = load_wblock<FMT, kWhole>(m, kb + j, any ? blocks : 0, a.F);
+    const auto rh = make_rsrc((const S*)a.h + (size_t)slot * a.T * 2 * a.F, hbytes);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       // a lane whose token did not choose the expert reads zeros
-      const uint32_t v = any && kb + j < blocks && ((chosen >> tok) & 1u)
-          ? (uint32_t)(tok * a.F + (kb + j) * 128 + (lane >> 4) * 8) * 2 : kPastEnd;
+      const uint32_t v = any && kb + j < blocks && ((chosen >> (vrow >> 1)) & 1u)
+          ? (uint32_t)(vrow * a.F + (kb + j) * 128 + (lane >> 4) * 8) * 2 : kPastEnd;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        n.hi[j][i] = buffer16(rh, v + 64 * i, 0);
-        n.lo[j][i] = buffer16(rl, v + 64 * i, 0);
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) n.h[j][p][i] = buffer16(rh, v + 64 * i, (uint32_t)(p * a.F) * 2);
     }
     return n;
   };
   float sum[NI];
 #pragma unroll
   for (int e = 0; e < NI; ++e) sum[e] = 0.f;
-  FewUnit<FMT, R> next = load(wave);
+  U next = load(first);
   for (int i = threadIdx.x; i < n_slots * a.T; i += blockDim.x) {
     const int slot = i / a.T, t = i - slot * a.T, e = experts[slot];
     weights[i] = e < a.E && ((masks[slot] >> t) & 1u) ? a.w[(size_t)t * a.E + e] : 1.f;
   }
   __syncthreads();
-  for (int u = wave; u < units; u += kRowWaves) {
-    const FewUnit<FMT, R> now = next;
-    next = load(u + kRowWaves);
+  // the token of element e
+  auto token = [&](int e) { return PARTS == 1 ? 2 * e + (lane >> 5) : 4 * e + (lane >> 4); };
+  for (int u = first; u < last; ++u) {
+    const U now = next;
+    next = load(u + 1);
     const int slot = u / per;
     const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
     floatx4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -337,40 +352,48 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
       for (int j = 0; j < kN; ++j) {
         p[j] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[j] = mfma16(as_v8<V>(now.lo[j][i]), as_v8<V>(now.w.q[i]), p[j]);
-          p[j] = mfma16(as_v8<V>(now.hi[j][i]), as_v8<V>(now.w.q[i]), p[j]);
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = PARTS - 1; q >= 0; --q)
+            p[j] = mfma16(as_v8<V>(now.h[j][q][i]), as_v8<V>(now.w[0].q[i]), p[j]);
       }
 #pragma unroll
-      for (int e = 0; e < NI; ++e) acc[e] = kN == 2 && second_p ? p[kN - 1][e] : p[0][e];
+      for (int e = 0; e < NI; ++e) acc[e] = R == 8 && second_col ? p[kN - 1][e] : p[0][e];
     } else {
-      const Q4Steps<FMT> q = q4_steps<FMT, kWhole>(now.w, 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const V w = q4_widen<S, FMT>(q.word[i]);
-        floatx4 m[kN], c[kN];
+      for (int b = 0; b < kW; ++b) {
+        uint32_t prm[FMT == 1 ? 4 : 2];
+        block_params<FMT, kWhole>(now.w[b], prm);
+        const Q4Steps<FMT> q = q4_steps<FMT, kWhole>(now.w[b].q, prm, 4);
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-          const V hi = as_v8<V>(now.hi[j][i]), lo = as_v8<V>(now.lo[j][i]);
-          c[j] = x_constant<S, FMT>(hi, x_constant<S, FMT>(lo, floatx4{0.f, 0.f, 0.f, 0.f}));
-          m[j] = mfma16(hi, w, mfma16(lo, w, c[j]));
-        }
+        for (int i = 0; i < 4; ++i) {
+          const V w = q4_widen<S, FMT>(q.word[i]);
+          // R = 8: the strip against both blocks' h; R = 16: a strip a block
+          constexpr int kH = R == 8 ? 2 : 1;
+          floatx4 m[kH], c[kH];
 #pragma unroll
-        for (int e = 0; e < NI; ++e) {
-          const bool o = kN == 2 && second_p;
-          acc[e] = fmaf(q.scale(i), o ? m[kN - 1][e] : m[0][e], acc[e]);
-          if constexpr (FMT != 0)
-            acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), o ? c[kN - 1][e] : c[0][e], acc[e]);
+          for (int j = 0; j < kH; ++j) {
+            c[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = PARTS - 1; p >= 0; --p) c[j] = x_constant<S, FMT>(as_v8<V>(now.h[b + j][p][i]), c[j]);
+            m[j] = c[j];
+#pragma unroll
+            for (int p = PARTS - 1; p >= 0; --p) m[j] = mfma16(as_v8<V>(now.h[b + j][p][i]), w, m[j]);
+          }
+#pragma unroll
+          for (int e = 0; e < NI; ++e) {
+            const bool o = R == 8 && second_col;
+            acc[e] = fmaf(q.scale(i), o ? m[kH - 1][e] : m[0][e], acc[e]);
+            if constexpr (FMT != 0)
+              acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), o ? c[kH - 1][e] : c[0][e], acc[e]);
+          }
         }
       }
     }
     // a token of another expert takes nothing: its zeros times an infinite weight are NaN
 #pragma unroll
-    for (int e = 0; e < NI; ++e) {
-      const int t = 4 * e + (lane >> 4);
-      if ((chosen >> t) & 1u) sum[e] = fmaf(weights[slot * a.T + t], acc[e], sum[e]);
-    }
+    for (int e = 0; e < NI; ++e)
+      if ((chosen >> token(e)) & 1u) sum[e] = fmaf(weights[slot * a.T + token(e)], acc[e], sum[e]);
   }
 #pragma unroll
   for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = sum[e];
@@ -378,10 +401,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_down_kernel(FewArgs a) {
   if (threadIdx.x < 64 * NI) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
-    if constexpr (kN == 2) v += __shfl_xor(v, 8);
-    const int t = 4 * wave + (lane >> 4), c = lane & 15;
-    if (t < a.T && c < R) static_cast<O*>(a.y)[(size_t)t * a.D + d0 + c] = (O)v;
+    for (int w = 0; w < kWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
+    if constexpr (R == 8) v += __shfl_xor(v, 8);        // the two blocks
+    if constexpr (PARTS == 1) v += __shfl_xor(v, 16);   // the two parts
+    const int t = token(wave), c = lane & 15;
+    if (t < a.T && c < R && (PARTS == 2 || !(lane & 16)))
+      static_cast<O*>(a.y)[(size_t)t * a.D + d0 + c] = (O)v;
   }
 }
 
@@ -400,15 +425,18 @@ hipError_t gateup_launch(const FewArgs& a, int ncu, hipStream_t s) {
 
 template <class S, class O, int FMT>
 hipError_t down_launch(const FewArgs& a, int ncu, hipStream_t s) {
-  const int ni = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
+  const int ni = a.T <= 2 ? 1 : a.T <= 4 ? 2 : 4;   // with both parts of h; above 8 tokens, of one
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
   const size_t lds = (size_t)kRowWaves * ni * 256 + (size_t)4 * cap * (2 + a.T);
-#define MOE_FEW(NI, R) \
-  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI, R>), dim3(a.D / R), dim3(64 * kRowWaves), lds, s, a)
+#define MOE_FEW(NI, R, PARTS) \
+  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI, R, PARTS>), dim3(a.D / R), \
+                     dim3(64 * (kDownWaves<FMT, PARTS>)), lds, s, a)
   if (a.D / 16 >= ncu) {
-    if (ni == 1) MOE_FEW(1, 16); else if (ni == 2) MOE_FEW(2, 16); else MOE_FEW(4, 16);
+    if (ni == 1) MOE_FEW(1, 16, 1); else if (ni == 2) MOE_FEW(2, 16, 1);
+    else if (a.T <= 8) MOE_FEW(4, 16, 1); else MOE_FEW(4, 16, 2);
   } else {
-    if (ni == 1) MOE_FEW(1, 8); else if (ni == 2) MOE_FEW(2, 8); else MOE_FEW(4, 8);
+    if (ni == 1) MOE_FEW(1, 8, 1); else if (ni == 2) MOE_FEW(2, 8, 1);
+    else if (a.T <= 8) MOE_FEW(4, 8, 1); else MOE_FEW(4, 8, 2);
   }
 #undef MOE_FEW
   return hipGetLastError();

@@ -624,15 +624,14 @@ size_t moe_forward_workspace_bytes(const moe_plan* p, int32_t D, int32_t F,
 }
 
 // The workspace of moe_decode: SwiGLU outputs in two parts, routing weights, slots.
-struct FewLayout { size_t h, h_lo, w, slots, bytes; };
+struct FewLayout { size_t h, w, slots, bytes; };
 
 static FewLayout few_layout(const moe_plan_desc& d, int F) {
   FewLayout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   const size_t cap = few_slots(d.T, d.E, d.k, d.n_shared);
-  L.h = take(cap * d.T * F * 2);
-  L.h_lo = take(cap * d.T * F * 2);
+  L.h = take(cap * d.T * F * 4);
   L.w = take((size_t)d.T * d.E * 4);
   L.slots = take((1 + 2 * cap) * 4);
   L.bytes = o;
@@ -712,7 +711,7 @@ moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
   const int64_t limit = capacity_limit(*d);
   a.limit = limit < 0 || limit > d->T ? d->T : (int)limit;
   a.clamp = o.swiglu_limit;
-  a.h = b + L.h; a.h_lo = b + L.h_lo;
+  a.h = b + L.h;
   a.w = (float*)(b + L.w);
   a.slots = (int32_t*)(b + L.slots);
   a.y = y; a.ydt = y_dtype;

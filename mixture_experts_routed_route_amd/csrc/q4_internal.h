@@ -47,7 +47,7 @@ struct FewArgs {
   int limit;                         // most pairs an expert keeps (T: all)
   float clamp;
   // workspace
-  void* h; void* h_lo;               // [slots, T, F] SwiGLU outputs, two 16-bit parts
+  void* h;                           // [slots, T, 2, F] SwiGLU outputs, in two 16-bit parts
   float* w;                          // [T, E] routing weights of chosen experts
   int32_t* slots;                    // [1 + 2 slots]: their number, experts, token masks
   void* y; int ydt;                  // [T, D]

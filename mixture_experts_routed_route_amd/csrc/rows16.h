@@ -105,7 +105,7 @@ enum Ragged : int { kWhole = 0, kWords = 1, kOdd = 2 };
 template <int FMT> struct WStrip {
   __amdgpu_buffer_rsrc_t q, p;
   const char* prow;          // kOdd: the lane's row of parameters
-  uint32_t vq, vp;
+  uint32_t vq, vp, vr;       // vp: parameters a block, vr: a run (load_params)
 };
 
 __device__ __forceinline__ uint4 buffer16(__amdgpu_buffer_rsrc_t r, uint32_t v, uint32_t s) {
@@ -131,7 +131,7 @@ __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void
   r.prow = nullptr;
   if constexpr (FMT < 0) {
     r.vq = (lane & 15) * rb + (lane >> 4) * 16u;
-    r.vp = 0;
+    r.vp = r.vr = 0;
     r.p = r.q;
   } else {
     using Q = Q4F<FMT>;
@@ -140,6 +140,7 @@ __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void
     r.vq = (lane >> 2) * rb + (lane & 3) * 16u;
     r.p = make_rsrc(p, rows * pb);
     r.vp = lane < 16 ? lane * pb : kPastEnd;
+    r.vr = (lane >> 2) * pb + (lane & 3) * 16u;
     if constexpr (RAGGED == kOdd) r.prow = p + (size_t)((lane & 15) < rows ? lane & 15 : 0u) * pb;
   }
   return r;
@@ -148,7 +149,7 @@ __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void
 // Block kb (values 128 kb ..) of the strip; kb >= end gives zeros. In a short last
 // block the pieces behind the row's end have parameters of zero (their codes are the
 // next row's, x's fragments are zero there).
-template <int FMT, int RAGGED>
+template <int FMT, int RAGGED, bool PARAMS = true>
 __device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb, int end, int K) {
   WBlock<FMT> b;
   const uint32_t at = (uint32_t)(kb < end ? kb : end - 1);
@@ -162,7 +163,8 @@ __device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb,
     constexpr int kP = FMT == 1 ? 4 : 2;
     constexpr uint32_t kPer = 128 / Q::kGroup * Q::kPB;
     b.q = buffer16(r.q, v, at * 64u);
-    if constexpr (RAGGED != kOdd) {
+    if constexpr (!PARAMS) {
+    } else if constexpr (RAGGED != kOdd) {
       const uint32_t vp = kb < end ? r.vp : kPastEnd;
       if constexpr (FMT == 1) {
         const uint4 w = buffer16(r.p, vp, at * kPer);
@@ -183,6 +185,32 @@ __device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb,
     }
   }
   return b;
+}
+
+// Parameters of kRun blocks from block kb on, as loaded: lane 4 r + q has 16 bytes of
+// row r. A run's bytes are asked for at once: 8 bytes a row and block would be a
+// request each.
+template <int FMT> constexpr int kRun = FMT == 1 ? 4 : 8;
+
+template <int FMT>
+__device__ __forceinline__ uint4 load_params(const WStrip<FMT>& r, int kb, int end) {
+  using Q = Q4F<FMT>;
+  return buffer16(r.p, kb < end ? r.vr : kPastEnd,
+                  (uint32_t)(kb < end ? kb : 0) * (128 / Q::kGroup * Q::kPB));
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Block i of the run (a constant) for the lane's row (lane & 15).
+template <int FMT>
+__device__ __forceinline__ void run_params(const uint4& p, int i, uint32_t* out) {
+  const int row = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int k = 0; k < (FMT == 1 ? 4 : 2); ++k)
+    out[k] = (uint32_t)__builtin_amdgcn_ds_bpermute(
+        (row + (FMT == 1 ? i : i >> 1)) * 4, (int)word_of(p, FMT == 1 ? k : (i & 1) * 2 + k));
 }
 
 // Fragments of x over a block of 128 values (4 steps), and for 4-bit weights
@@ -306,47 +334,48 @@ template <int FMT> struct Q4Steps {
   }
 };
 
-// left: pieces from the block's first to the row's end.
+// Codes as loaded, parameters of the lane's row; left: pieces from the block's first
+// to the row's end.
 template <int FMT, int RAGGED>
-__device__ __forceinline__ Q4Steps<FMT> q4_steps(const WBlock<FMT>& w, int left) {
+__device__ __forceinline__ Q4Steps<FMT> q4_steps(uint4 codes, const uint32_t* params, int left) {
   Q4Steps<FMT> s;
-  const uint4 t = lane_group_transpose(rows_to_columns(w.q));
+  const uint4 t = lane_group_transpose(rows_to_columns(codes));
   s.word[0] = t.x; s.word[1] = t.y; s.word[2] = t.z; s.word[3] = t.w;
 #pragma unroll
   for (int i = 0; i < (FMT == 1 ? 4 : 2); ++i) {
-    s.p[i] = RAGGED == kOdd ? w.p[i] : lane_group_bcast(w.p[i]);
+    s.p[i] = params[i];
     if constexpr (RAGGED == kWords)
       if ((FMT == 1 ? i : 2 * i) >= left) s.p[i] = 0u;
   }
   return s;
 }
 
+// a block's parameters as load_wblock reads them, for the lane's row
+template <int FMT, int RAGGED>
+__device__ __forceinline__ void block_params(const WBlock<FMT>& w, uint32_t* out) {
+#pragma unroll
+  for (int i = 0; i < (FMT == 1 ? 4 : 2); ++i) out[i] = RAGGED == kOdd ? w.p[i] : lane_group_bcast(w.p[i]);
+}
+
 // acc[i] += the block's products of the lane's tokens 4 i + (lane >> 4), i < NI, with
 // its weight row.
-template <class S, int FMT, int NI, int RAGGED>
-__device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const WBlock<FMT>& w, int left,
+template <class S, int FMT, int NI>
+__device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const Q4Steps<FMT>& q,
                                               floatx4& acc) {
-  using V = typename R16<S>::V;
-  if constexpr (FMT < 0) {
+  // two matrix instructions before the sums of the first are needed
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc = mfma16(x.v[i], as_v8<V>(w.q[i]), acc);
-  } else {
-    const Q4Steps<FMT> q = q4_steps<FMT, RAGGED>(w, left);
-    // two matrix instructions before the sums of the first are needed
+  for (int h = 0; h < 4; h += 2) {
+    floatx4 m[2];
 #pragma unroll
-    for (int h = 0; h < 4; h += 2) {
-      floatx4 m[2];
+    for (int i = 0; i < 2; ++i) m[i] = mfma16(x.v[h + i], q4_widen<S, FMT>(q.word[h + i]), x.c[h + i]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[i] = mfma16(x.v[h + i], q4_widen<S, FMT>(q.word[h + i]), x.c[h + i]);
+    for (int i = h; i < h + 2; ++i)
 #pragma unroll
-      for (int i = h; i < h + 2; ++i)
-#pragma unroll
-        for (int e = 0; e < NI; ++e) {
-          acc[e] = fmaf(q.scale(i), m[i - h][e], acc[e]);
-          // c holds -off sum x; the quotient is exact
-          if constexpr (FMT != 0) acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), x.c[i][e], acc[e]);
-        }
-    }
+      for (int e = 0; e < NI; ++e) {
+        acc[e] = fmaf(q.scale(i), m[i - h][e], acc[e]);
+        // c holds -off sum x; the quotient is exact
+        if constexpr (FMT != 0) acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), x.c[i][e], acc[e]);
+      }
   }
 }
 
@@ -355,36 +384,67 @@ __device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const WBl
 // A block of 4-bit codes is half a cache line of each row: two are asked for back to
 // back, or the line would be fetched twice.
 template <class S, int FMT, int NI, int MATS, int RAGGED> struct Stream {
+  static constexpr bool kRuns = FMT >= 0 && RAGGED != kOdd;   // parameters by runs
   static constexpr int kPair = FMT < 0 ? 1 : 2;
   // as many as 128 registers a wave hold without spills
-  static constexpr int kDepth = FMT < 0 ? 4 / MATS : (MATS == 1 ? (FMT == 1 || NI > 1 ? 6 : 8) : 4);
-  WBlock<FMT> buf[kDepth][MATS];
+  static constexpr int kDepth = FMT < 0 ? 4 / MATS : MATS == 1 ? 8 : 4;
+  static constexpr int kTurn = !kRuns ? kDepth : FMT == 1 ? (kDepth > 4 ? kDepth : 4) : 8;
+  using Codes = WBlock<FMT>;
+  Codes buf[kDepth][MATS];
+  static constexpr int kR = kRuns ? kRun<FMT> : 8;   // blocks a run
+  uint4 run_next[MATS];
 
-  __device__ __forceinline__ void start(const WStrip<FMT> (&m)[MATS], int first, int end, int K) {
-#pragma unroll
-    for (int i = 0; i < kDepth; i += kPair) fill(m, i, first + i, end, K);
-  }
   __device__ __forceinline__ void fill(const WStrip<FMT> (&m)[MATS], int i, int kb, int end, int K) {
 #pragma unroll
     for (int j = 0; j < MATS; ++j)
 #pragma unroll
-      for (int h = 0; h < kPair; ++h) buf[i + h][j] = load_wblock<FMT, RAGGED>(m[j], kb + h, end, K);
+      for (int h = 0; h < kPair; ++h)
+        buf[i + h][j] = load_wblock<FMT, RAGGED, !kRuns>(m[j], kb + h, end, K);
+  }
+  __device__ __forceinline__ void start(const WStrip<FMT> (&m)[MATS], int first, int end, int K) {
+    if constexpr (kRuns)
+#pragma unroll
+      for (int j = 0; j < MATS; ++j) run_next[j] = load_params<FMT>(m[j], first, end);
+#pragma unroll
+    for (int i = 0; i < kDepth; i += kPair) fill(m, i, first + i, end, K);
   }
   __device__ __forceinline__ void run(const WStrip<FMT> (&m)[MATS], const char* lds, int T, int KL, int k0b,
                                       int first, int end, int K, floatx4 (&acc)[MATS]) {
-    for (int kb = first; kb < end; kb += kDepth) {
+    for (int kb = first; kb < end; kb += kTurn) {
+      uint4 params[MATS];
 #pragma unroll
-      for (int i = 0; i < kDepth; i += kPair) {
+      for (int i = 0; i < kTurn; i += kPair) {
+        if constexpr (kRuns) {
+          if (i % kR == 0) {
+#pragma unroll
+            for (int j = 0; j < MATS; ++j) {
+              params[j] = run_next[j];
+              run_next[j] = load_params<FMT>(m[j], kb + i + kR, end);
+            }
+          }
+        }
 #pragma unroll
         for (int h = 0; h < kPair; ++h) {
           if (kb + i + h >= end) break;
           const XBlock<S, FMT> x = x_block<S, FMT, NI>(lds, T, KL, kb + i + h - k0b);
 #pragma unroll
-          for (int j = 0; j < MATS; ++j)
-            block_product<S, FMT, NI, RAGGED>(x, buf[i + h][j], K / 32 - 4 * (kb + i + h), acc[j]);
+          for (int j = 0; j < MATS; ++j) {
+            const Codes& w = buf[(i + h) % kDepth][j];
+            if constexpr (FMT < 0) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                acc[j] = mfma16(x.v[s], as_v8<typename R16<S>::V>(w.q[s]), acc[j]);
+            } else {
+              uint32_t p[FMT == 1 ? 4 : 2];
+              if constexpr (kRuns) run_params<FMT>(params[j], (i + h) % kR, p);
+              else block_params<FMT, RAGGED>(w, p);
+              block_product<S, FMT, NI>(
+                  x, q4_steps<FMT, RAGGED>(w.q, p, K / 32 - 4 * (kb + i + h)), acc[j]);
+            }
+          }
         }
         if (kb + i >= end) break;
-        fill(m, i, kb + i + kDepth, end, K);
+        fill(m, i % kDepth, kb + i + kDepth, end, K);
       }
     }
   }
