@@ -497,7 +497,7 @@ moe_status moe_quant_q4_weights(const void *w, int32_t dtype, int32_t w_dtype,
  * f32 and is scaled and added in f32; one rounding to out_dtype. A row of x
  * that holds an infinity or a NaN gives NaN; bf16 rows' group sums must stay
  * below 2^120. K a multiple of the format's group up to 2^22; M below 2^31, N
- * up to 2^31 - 256 (0 writes nothing). Pointers 16-byte aligned. Async on
+ * up to 2^26 (0 writes nothing). Pointers 16-byte aligned. Async on
  * `stream`. */
 moe_status moe_gemm_q4(const void *x, int32_t x_dtype, moe_weight w, int64_t M,
                        int32_t N, int32_t K, void *out, int32_t out_dtype,

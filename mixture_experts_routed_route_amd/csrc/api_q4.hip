@@ -19,7 +19,8 @@ moe_status launched(hipError_t e, const char* where) {
 
 // a row of x stays below 2^31 bytes by far, and so do offsets within a row
 constexpr int kQ4MaxK = 1 << 22;
-constexpr int kQ4MaxN = INT32_MAX - 255;
+// a launch holds fewer than 2^32 threads along x
+constexpr int kQ4MaxN = 1 << 26;
 
 }  // namespace
 
@@ -65,14 +66,15 @@ moe_status moe_gemm_q4(const void* x, int32_t x_dtype, moe_weight w, int64_t M, 
   if (!aligned(x, 16) || !aligned(w.data, 16) || !aligned(w.scales, 16) || !aligned(out, 16))
     return set_error(MOE_EINVAL, "pointers must be 16-byte aligned");
   if (M > (int64_t)INT32_MAX || N > kQ4MaxN)
-    return set_error(MOE_EUNSUPPORTED, "M=%lld must be below 2^31, N=%d at most 2^31 - 256",
+    return set_error(MOE_EUNSUPPORTED, "M=%lld must be below 2^31, N=%d at most 2^26",
                      (long long)M, N);
   if (!any) return MOE_OK;
   int ncu;
   const moe_status st = current_cus(&ncu);
   if (st != MOE_OK) return st;
   const RowsArgs a{x, x_dtype, w.data, w.scales, fmt, M, N, K, out, out_dtype};
-  return launched(launch_rows_product(a, ncu, reinterpret_cast<hipStream_t>(stream)),
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return launched(M <= 16 ? launch_rows_product(a, ncu, s) : launch_q4_tile(a, ncu, s),
                   "4-bit product");
 }
 

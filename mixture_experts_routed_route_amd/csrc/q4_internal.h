@@ -33,7 +33,10 @@ struct RowsArgs {
   int64_t M; int N, K;
   void* out; int odt;
 };
+// up to 16 rows (more in turns)
 hipError_t launch_rows_product(const RowsArgs& a, int ncu, hipStream_t s);
+// any number of rows, 4-bit weights (gemm_q4_tile.hip)
+hipError_t launch_q4_tile(const RowsArgs& a, int ncu, hipStream_t s);
 
 // ---- the layer for a few tokens (decode.hip) -----------------------------------
 constexpr int kFewT = MOE_DECODE_MAX_T;

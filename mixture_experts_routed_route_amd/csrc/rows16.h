@@ -124,7 +124,7 @@ template <int FMT, int RAGGED>
 __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void* params, int64_t N,
                                                     int64_t n0, int K) {
   const uint32_t lane = threadIdx.x & 63;
-  const uint32_t rows = (uint32_t)(N - n0 < 16 ? N - n0 : 16);
+  const uint32_t rows = n0 >= N ? 0u : (uint32_t)(N - n0 < 16 ? N - n0 : 16);
   WStrip<FMT> r;
   const uint32_t rb = FMT < 0 ? (uint32_t)K * 2 : (uint32_t)K / 2;
   r.q = make_rsrc((const char*)data + n0 * (int64_t)rb, rows * rb);
@@ -141,7 +141,8 @@ __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void
     r.p = make_rsrc(p, rows * pb);
     r.vp = lane < 16 ? lane * pb : kPastEnd;
     r.vr = (lane >> 2) * pb + (lane & 3) * 16u;
-    if constexpr (RAGGED == kOdd) r.prow = p + (size_t)((lane & 15) < rows ? lane & 15 : 0u) * pb;
+    if constexpr (RAGGED == kOdd)   // rows past the last read the matrix's first
+      r.prow = (lane & 15) < rows ? p + (size_t)(lane & 15) * pb : (const char*)params;
   }
   return r;
 }

@@ -46,7 +46,7 @@ def _gemm(lib, x=0x1000, xdt=moe.MOE_F16, wdt=moe.MOE_Q4A32, w=0x2000, s=0x3000,
 @pytest.mark.parametrize("kw,want", [
     (dict(wdt=moe.MOE_F16), U), (dict(wdt=moe.MOE_F8B128), U), (dict(xdt=moe.MOE_F32), U), (dict(xdt=moe.MOE_Q4B32), U),
     (dict(odt=moe.MOE_Q4B32), U), (dict(M=-1), E), (dict(N=-1), E), (dict(K=0), E), (dict(K=144), E),
-    (dict(wdt=moe.MOE_Q4A64, K=96), E), (dict(K=(1 << 22) + 32), E), (dict(M=1 << 31), U), (dict(N=2 ** 31 - 255), U),
+    (dict(wdt=moe.MOE_Q4A64, K=96), E), (dict(K=(1 << 22) + 32), E), (dict(M=1 << 31), U), (dict(N=(1 << 26) + 1), U), (dict(N=2 ** 31 - 1), U),
     (dict(x=None), E), (dict(w=None), E), (dict(s=None), E), (dict(out=None), E), (dict(x=0x1008), E),
     (dict(w=0x2008), E), (dict(s=0x3004), E), (dict(out=0x4002), E)])
 def test_product_refuses(lib, kw, want):
