@@ -39,8 +39,8 @@ __device__ __forceinline__ typename R16<S>::V q4_widen_in_order(uint32_t w) {
 }
 
 // x staged as rows of 128 values, 16 pieces of 16 bytes; piece j of row r lies at place
-// j ^ (r & 7), so that 8 neighbouring rows' pieces lie in different banks.
-__device__ __forceinline__ int place(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) * 16); }
+// j ^ (r & 15), so that 16 neighbouring rows' pieces lie in different banks.
+__device__ __forceinline__ int place(int row, int piece) { return row * 256 + ((piece ^ (row & 15)) * 16); }
 
 // acc[m][s] += a block of MT x 16 rows of x (staged) against NS strips; left: pieces
 // from the block's first to the row's end.
@@ -105,20 +105,15 @@ __device__ __forceinline__ void store_as(void* out, int odt, size_t at, float v)
 // 128 rows x 256 columns a workgroup of four waves side by side, two workgroups a
 // compute unit; x by direct loads to LDS, a block of 128 values ahead, weights in
 // registers a block ahead, one barrier a block.
-constexpr int kTileM = 128, kTileN = 256;
+constexpr int kTileM = 128, kTileN = 256, kStage = kTileM * 256;
 
-template <class S, int FMT, int RAGGED>
-__global__ __launch_bounds__(256, 2) void q4_tile_kernel(RowsArgs a, int tiles_n, int tiles) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];   // two blocks of x
-  constexpr int kStage = kTileM * 256;
+// MT x 16 rows from m0 on
+template <class S, int FMT, int RAGGED, int MT>
+__device__ __forceinline__ void q4_tile(const RowsArgs& a, char* lds, int64_t m0, int64_t n0) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // an XCD's workgroups (numbers equal modulo 8) take neighbouring tiles
-  const int per = (tiles + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return;
-  const int64_t m0 = (int64_t)(id / tiles_n) * kTileM;
-  const int64_t n0 = (int64_t)(id % tiles_n) * kTileN + wave * 64;
-  const uint32_t rows = (uint32_t)(a.M - m0 < kTileM ? a.M - m0 : kTileM), rb = (uint32_t)a.K * 2;
+  n0 += wave * 64;
+  const uint32_t rows = (uint32_t)(a.M - m0 < MT * 16 ? a.M - m0 : MT * 16), rb = (uint32_t)a.K * 2;
   // (its type by name: with auto the host pass drops the kernel without a word)
   const __amdgpu_buffer_rsrc_t rx = make_rsrc((const S*)a.x + m0 * a.K, rows * rb);
   const int blocks = (a.K + 127) / 128;
@@ -127,16 +122,17 @@ __global__ __launch_bounds__(256, 2) void q4_tile_kernel(RowsArgs a, int tiles_n
   for (int s = 0; s < 4; ++s) strip[s] = weight_strip<FMT, RAGGED>(a.w, a.params, a.N, n0 + 16 * s, a.K);
   auto stage = [&](int kb, int buf) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int row = wave * 32 + j * 4 + (lane >> 4), piece = (lane & 15) ^ (row & 7);
+    for (int j = 0; j < MT; ++j) {
+      const int first = (wave * MT + j) * 4;   // the first of four rows
+      const int row = first + (lane >> 4), piece = (lane & 15) ^ (row & 15);
       const uint32_t v = kb * 128 + piece * 8 < a.K ? (uint32_t)row * rb + piece * 16 : kPastEnd;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rx, (lds_ptr_t)(lds + buf * kStage + (wave * 32 + j * 4) * 256), 16, (int)v, kb * 256, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(lds + buf * kStage + first * 256), 16, (int)v,
+                                               kb * 256, 0, 0);
     }
   };
-  floatx4 acc[8][4];
+  floatx4 acc[MT][4];
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[m][s] = floatx4{0.f, 0.f, 0.f, 0.f};
   WBlock<FMT> next[4];
@@ -154,12 +150,12 @@ __global__ __launch_bounds__(256, 2) void q4_tile_kernel(RowsArgs a, int tiles_n
 #pragma unroll
       for (int s = 0; s < 4; ++s) next[s] = load_wblock<FMT, RAGGED>(strip[s], kb + 1, blocks, a.K);
     }
-    tile_block<S, FMT, RAGGED, 8, 4>(lds + (kb & 1) * kStage, w, a.K / 32 - 4 * kb, acc);
+    tile_block<S, FMT, RAGGED, MT, 4>(lds + (kb & 1) * kStage, w, a.K / 32 - 4 * kb, acc);
     wait_vmcnt<0>();
     __syncthreads();
   }
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t row = m0 + m * 16 + (lane >> 4) * 4 + e;
@@ -171,6 +167,25 @@ __global__ __launch_bounds__(256, 2) void q4_tile_kernel(RowsArgs a, int tiles_n
         }
       }
     }
+}
+
+template <class S, int FMT, int RAGGED>
+__global__ __launch_bounds__(256, 2) void q4_tile_kernel(RowsArgs a, int tiles_n, int whole, int tiles) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];   // two blocks of x
+  // An XCD's workgroups (numbers equal modulo 8) take neighbouring tiles, first of the
+  // `whole` ones, then of those of half the rows.
+  const int big = (whole + 7) & ~7, n = (int)blockIdx.x;
+  const bool all = n < big;
+  const int k = all ? n : n - big, count = all ? whole : tiles - whole;
+  const int per = (count + 7) / 8, local = (k & 7) * per + (k >> 3);
+  if ((k >> 3) >= per || local >= count) return;
+  const int64_t n0 = (int64_t)(local % tiles_n) * kTileN;
+  if (all) {
+    q4_tile<S, FMT, RAGGED, 8>(a, lds, (int64_t)(local / tiles_n) * kTileM, n0);
+  } else {
+    const int64_t m0 = (int64_t)(whole / tiles_n) * kTileM + (int64_t)(local / tiles_n) * (kTileM / 2);
+    q4_tile<S, FMT, RAGGED, 4>(a, lds, m0, n0);
+  }
 }
 
 // ---- some rows --------------------------------------------------------------------
@@ -259,27 +274,39 @@ hipError_t slice_launch(const RowsArgs& a, hipStream_t s) {
   return hipSuccess;
 }
 
+// Tiles in full rounds of the compute units' workgroups, and one more round of half
+// tiles where those rows fit it.
+template <class S, int FMT, int RAGGED>
+hipError_t whole_tiles(const RowsArgs& a, int64_t tn, int ncu, hipStream_t s) {
+  // rows of tiles in turns whose number fits an int
+  const int64_t tm = (a.M + kTileM - 1) / kTileM, step = std::max<int64_t>(1, (1 << 28) / tn);
+  for (int64_t y = 0; y < tm; y += step) {
+    RowsArgs b = a;
+    b.x = (const char*)a.x + (size_t)y * kTileM * a.K * 2;
+    b.out = (char*)a.out + (size_t)y * kTileM * a.N * (a.odt == MOE_F32 ? 4 : 2);
+    b.M = std::min<int64_t>(a.M - y * kTileM, step * kTileM);
+    const int64_t rows = (b.M + kTileM - 1) / kTileM, slots = 2 * ncu;
+    int64_t big = rows * tn / slots * slots / tn;   // rows of tiles in full rounds
+    const int64_t halves = (b.M - big * kTileM + kTileM / 2 - 1) / (kTileM / 2);
+    if (halves * tn > slots) big = rows;
+    const int64_t whole = big * tn, rest = big == rows ? 0 : halves * tn;
+    const unsigned grid = (unsigned)((whole + 7) / 8 * 8 + (rest + 7) / 8 * 8);
+    hipLaunchKernelGGL((q4_tile_kernel<S, FMT, RAGGED>), dim3(grid), dim3(256), 2 * kStage, s, b, (int)tn,
+                       (int)whole, (int)(whole + rest));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <class S, int FMT, int RAGGED>
 hipError_t tile_launch(const RowsArgs& a, int ncu, hipStream_t s) {
-  const int64_t tn = ((int64_t)a.N + kTileN - 1) / kTileN, tm = (a.M + kTileM - 1) / kTileM;
-  if (tn * tm >= ncu) {
-    // rows of tiles in turns whose number fits an int
-    const int64_t step = std::max<int64_t>(1, (1 << 28) / tn);
-    for (int64_t y = 0; y < tm; y += step) {
-      RowsArgs b = a;
-      const size_t osz = a.odt == MOE_F32 ? 4 : 2;
-      b.x = (const char*)a.x + (size_t)y * kTileM * a.K * 2;
-      b.out = (char*)a.out + (size_t)y * kTileM * a.N * osz;
-      b.M = std::min<int64_t>(a.M - y * kTileM, step * kTileM);
-      const int64_t tiles = (b.M + kTileM - 1) / kTileM * tn;
-      hipLaunchKernelGGL((q4_tile_kernel<S, FMT, RAGGED>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256),
-                         2 * kTileM * 256, s, b, (int)tn, (int)tiles);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
-  }
+  const int64_t tn = ((int64_t)a.N + kTileN - 1) / kTileN;
   const int64_t strips = ((int64_t)a.N + 15) / 16;
+  // Slices of 64 x 64 take 23 us a round of the compute units at K = 4096, tiles 73 however
+  // few: us of slices / tiles at N = 4096, 300 rows 46 / 73, 640 rows 70 / 72, 1024 rows 90
+  // / 74, 2048 rows 180 / 119.
+  if ((a.M + 63) / 64 * (((int64_t)a.N + 63) / 64) > 3 * ncu) return whole_tiles<S, FMT, RAGGED>(a, tn, ncu, s);
   if (a.M <= 32) return slice_launch<S, FMT, RAGGED, 2, 1>(a, s);
   const int64_t r64 = (a.M + 63) / 64;
   if (r64 * strips <= 2 * ncu) return slice_launch<S, FMT, RAGGED, 4, 1>(a, s);
