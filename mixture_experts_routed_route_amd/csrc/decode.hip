@@ -43,137 +43,140 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   return v;
 }
 
+// Router's map: logits[t, e] = x[t] . w[e], a workgroup an expert, a slice of 8 values
+// of the row a thread, f32 products in a fixed order. NT >= T.
+template <class S, int NT>
+__global__ __launch_bounds__(512) void few_router_kernel(const S* __restrict__ x, const S* __restrict__ w,
+                                                         float* __restrict__ logits, int T, int D, int E) {
+  __shared__ float part[8][NT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  float acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+  for (int d = threadIdx.x * 8; d < D; d += blockDim.x * 8) {
+    typedef S V __attribute__((ext_vector_type(8)));
+    const V wv = *reinterpret_cast<const V*>(w + (size_t)blockIdx.x * D + d);
+    V xv[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)   // rows behind the last read it again
+      xv[t] = *reinterpret_cast<const V*>(x + (size_t)min(t, T - 1) * D + d);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[t] = fmaf((float)xv[t][i], (float)wv[i], acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float v = wave_sum_f(acc[t]);
+    if (lane == 0) part[wave][t] = v;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < T) {
+    float v = 0.f;
+    for (int i = 0; i < waves; ++i) v += part[i][threadIdx.x];
+    logits[(size_t)threadIdx.x * E + blockIdx.x] = v;
+  }
+}
+
 // Words of 64 experts that a token's choices take.
 __device__ __forceinline__ int choice_words(int E) { return (E + 63) / 64; }
 
 // Each token's k experts, as bits of chosen[t][e / 64] (LDS), a wave a token; its
-// weights (global [T, E], chosen entries) where weights is not null. PER = words.
+// weights (global [T, E], chosen entries) where weights is not null. PER >= words.
 // Ties go to the lower expert, NaN ranks below -inf, as in moe_plan_create.
 template <int PER>
-__device__ __forceinline__ void route_tokens(const FewArgs& a, uint64_t* chosen, float* weights) {
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int t = wave; t < a.T; t += waves) {
-    float l[PER];
-    uint32_t key[PER], top = 0u;
-    uint64_t sel[PER];
+__device__ __forceinline__ void route_token(const FewArgs& a, int t, uint64_t* chosen, float* weights) {
+  const int lane = threadIdx.x & 63;
+  float l[PER];
+  uint32_t key[PER], top = 0u;
+  uint64_t sel[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) l[p] = lane + 64 * p < a.E ? a.logits[(size_t)t * a.E + lane + 64 * p] : 0.f;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    key[p] = lane + 64 * p < a.E ? order_key(l[p]) + 1u : 0u;   // 0: none
+    sel[p] = 0ull;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int p = 1; p < PER; ++p) m = max(m, key[p]);
+    m = wave_max_u32(m);
+    if (j == 0) top = m;
+    bool open = true;   // the lowest expert among equal ones
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      const int e = lane + 64 * p;
-      l[p] = e < a.E ? a.logits[(size_t)t * a.E + e] : 0.f;
+      const uint64_t at = __ballot(key[p] == m);
+      const uint64_t bit = open ? at & (0ull - at) : 0ull;
+      open = open && !at;
+      sel[p] |= bit;
+      if ((bit >> lane) & 1ull) key[p] = 0u;
     }
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      key[p] = lane + 64 * p < a.E ? order_key(l[p]) + 1u : 0u;   // 0: none
-      sel[p] = 0ull;
-    }
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t m = key[0];
-#pragma unroll
-      for (int p = 1; p < PER; ++p) m = max(m, key[p]);
-      m = wave_max_u32(m);
-      if (j == 0) top = m;
-      bool open = true;   // the lowest expert among equal ones
-#pragma unroll
-      for (int p = 0; p < PER; ++p) {
-        const uint64_t at = __ballot(key[p] == m);
-        const uint64_t bit = open ? at & (0ull - at) : 0ull;
-        open = open && !at;
-        sel[p] |= bit;
-        if ((bit >> lane) & 1ull) key[p] = 0u;
-      }
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int p = 0; p < PER; ++p)
-        if (64 * p < a.E) chosen[t * choice_words(a.E) + p] = sel[p];
-    }
-    if (!weights) continue;
-    const float l0 = key_value(top - 1u);
-    float ex[PER], sum = 0.f;
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      ex[p] = 0.f;
-      if ((sel[p] >> lane) & 1ull) {
-        // exp(l - l0): the difference's rounding error is put back
-        const float d = l[p] - l0, back = d + l0;
-        const float err = (l[p] - back) + ((back - d) - l0);
-        ex[p] = expf(d);
-        if (ex[p] > 0.f && err == err) ex[p] = fmaf(ex[p], err, ex[p]);
-      }
-      sum += ex[p];
-    }
-    sum = wave_sum_f(sum);
+  }
+  if (lane == 0) {
 #pragma unroll
     for (int p = 0; p < PER; ++p)
-      if ((sel[p] >> lane) & 1ull) weights[(size_t)t * a.E + lane + 64 * p] = ex[p] / sum;
+      if (64 * p < a.E) chosen[t * choice_words(a.E) + p] = sel[p];
   }
+  if (!weights) return;
+  const float l0 = key_value(top - 1u);
+  float ex[PER], sum = 0.f;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    ex[p] = 0.f;
+    if ((sel[p] >> lane) & 1ull) {
+      // exp(l - l0): the difference's rounding error is put back
+      const float d = l[p] - l0, back = d + l0;
+      const float err = (l[p] - back) + ((back - d) - l0);
+      ex[p] = expf(d);
+      if (ex[p] > 0.f && err == err) ex[p] = fmaf(ex[p], err, ex[p]);
+    }
+    sum += ex[p];
+  }
+  sum = wave_sum_f(sum);
+#pragma unroll
+  for (int p = 0; p < PER; ++p)
+    if ((sel[p] >> lane) & 1ull) weights[(size_t)t * a.E + lane + 64 * p] = ex[p] / sum;
 }
 
-// Expert 64 p + lane's tokens, as bits, after the limit (its first tokens stay).
-__device__ __forceinline__ uint32_t tokens_of(const FewArgs& a, const uint64_t* chosen, int p) {
+// The experts in use, in order, the shared one last: their tokens (bits, after the
+// limit, which keeps an expert's first ones) and the pairs before them. list in LDS:
+// [0] their number, then [cap] experts, [cap] tokens, [cap] pairs before. A wave a word of experts.
+__device__ __forceinline__ void list_experts(const FewArgs& a, const uint64_t* chosen, int32_t* list) {
   const int lane = threadIdx.x & 63, words = choice_words(a.E);
-  uint32_t m = 0u;
-  for (int t = 0; t < a.T; ++t) m |= (uint32_t)((chosen[t * words + p] >> lane) & 1ull) << t;
-  for (int over = __popc(m) - a.limit; over > 0; --over) m &= ~(0x80000000u >> __clz((int)m));
-  return m;
-}
-
-// The experts in use, in order, then the shared one: their number; and expert and
-// tokens of number `slot` (or of none). Every wave for itself.
-__device__ __forceinline__ int experts_in_use(const FewArgs& a, const uint64_t* chosen) {
-  int n = 0;
-  for (int p = 0; p < choice_words(a.E); ++p) n += __popcll(__ballot(tokens_of(a, chosen, p) != 0u));
-  return n + a.n_shared;
-}
-__device__ __forceinline__ void expert_of(const FewArgs& a, const uint64_t* chosen, int slot, int* expert,
-                                          uint32_t* tokens) {
-  *expert = a.E;
-  *tokens = (1u << a.T) - 1u;
-  int n = 0;
-  for (int p = 0; p < choice_words(a.E); ++p) {
-    const uint32_t m = tokens_of(a, chosen, p);
-    uint64_t used = __ballot(m != 0u);
-    const int here = __popcll(used);
-    if (slot < n + here) {   // wave-uniform
-      for (int i = n; i < slot; ++i) used &= used - 1ull;
-      const int l = __builtin_ctzll(used);
-      *expert = 64 * p + l;
-      *tokens = (uint32_t)__builtin_amdgcn_readlane((int)m, l);
-      return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
+  if (wave >= words) return;
+  int n = 0, pairs = 0;
+  for (int p = 0; p <= wave; ++p) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int t = 0; t < kFewT; ++t) m |= (uint32_t)((chosen[t * words + p] >> lane) & 1ull) << t;
+    for (int over = __popc(m) - a.limit; over > 0; --over) m &= ~(0x80000000u >> __clz((int)m));
+    const uint64_t used = __ballot(m != 0u), below = (1ull << lane) - 1ull;
+    int here = 0, before = pairs;
+#pragma unroll
+    for (int t = 0; t < kFewT; ++t) {
+      const uint64_t of = __ballot((m >> t) & 1u);
+      here += __popcll(of);
+      before += __popcll(of & below);
     }
-    n += here;
+    if (p == wave && m) {
+      const int at = 1 + n + __popcll(used & below);
+      list[at] = 64 * p + lane;
+      list[at + cap] = (int32_t)m;
+      list[at + 2 * cap] = before;
+    }
+    n += __popcll(used);
+    pairs += here;
   }
-}
-
-// Routing of all tokens into chosen[T][words] (LDS); the first workgroup writes what
-// the second launch reads: the weights, and the experts in use with their tokens.
-__device__ __forceinline__ void route_all(const FewArgs& a, uint64_t* chosen) {
-  float* weights = blockIdx.x == 0 ? a.w : nullptr;
-  if (a.E <= 128) route_tokens<2>(a, chosen, weights);
-  else if (a.E <= 256) route_tokens<4>(a, chosen, weights);
-  else route_tokens<16>(a, chosen, weights);
-  __syncthreads();
-  if (blockIdx.x == 0 && threadIdx.x < 64) {
-    const int lane = threadIdx.x, cap = few_slots(a.T, a.E, a.k, a.n_shared);
-    int n = 0;
-    for (int p = 0; p < choice_words(a.E); ++p) {
-      const uint32_t m = tokens_of(a, chosen, p);
-      const uint64_t used = __ballot(m != 0u);
-      if (m) {
-        const int at = n + __popcll(used & ((1ull << lane) - 1ull));
-        a.slots[1 + at] = 64 * p + lane;
-        a.slots[1 + cap + at] = (int32_t)m;
-      }
-      n += __popcll(used);
+  if (wave == words - 1 && lane == 0) {
+    if (a.n_shared) {
+      list[1 + n] = a.E;
+      list[1 + n + cap] = (int32_t)((1u << a.T) - 1u);
+      list[1 + n + 2 * cap] = pairs;
     }
-    if (lane == 0) {
-      if (a.n_shared) {
-        a.slots[1 + n] = a.E;
-        a.slots[1 + cap + n] = (int32_t)((1u << a.T) - 1u);
-      }
-      a.slots[0] = n + a.n_shared;
-    }
+    list[0] = n + a.n_shared;
   }
 }
 
@@ -187,17 +190,36 @@ __device__ __forceinline__ void split_store(S* h, size_t at, int F, float v) {
   h[at + F] = (S)(rest == rest ? rest : 0.f);
 }
 
+// Both matrices' sums of waves that share strips lie in LDS at once, up to 8 tokens.
+template <int NI> constexpr int kParts = NI <= 2 ? 2 : 1;
+
 template <class S, int FMT, int NI>
 __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, int KL) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kPart = kRowWaves * NI * 64;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float* part = (float*)(lds + x_lds_bytes<FMT>(a.T, KL));   // [waves][NI][64]
-  uint64_t* chosen = (uint64_t*)(part + kRowWaves * NI * 64);   // [T][words]
+  const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
+  float* part = (float*)(lds + x_lds_bytes<FMT>(a.T, KL));   // [kParts][waves][NI][64]
+  uint64_t* chosen = (uint64_t*)(part + kParts<NI> * kPart);   // [kFewT][words]
+  int32_t* list = (int32_t*)(chosen + kFewT * choice_words(a.E));   // [1 + 3 cap]
   const S* x = (const S*)a.x;
   const int blocks = a.D / 128, per = KL / 128;
-  route_all(a, chosen);
-  const int strips = a.F / 16, items = experts_in_use(a, chosen) * strips;
+  if (wave < a.T) {
+    float* weights = blockIdx.x == 0 ? a.w : nullptr;
+    if (a.E <= 128) route_token<2>(a, wave, chosen, weights);
+    else if (a.E <= 256) route_token<4>(a, wave, chosen, weights);
+    else route_token<16>(a, wave, chosen, weights);
+  } else if (lane < choice_words(a.E)) {
+    chosen[wave * choice_words(a.E) + lane] = 0ull;   // no token
+  }
+  __syncthreads();
+  list_experts(a, chosen, list);
+  __syncthreads();
+  const int n_slots = __builtin_amdgcn_readfirstlane(list[0]);
+  if (blockIdx.x == 0)   // for the second launch
+    for (int i = threadIdx.x; i < 1 + 3 * cap; i += blockDim.x) a.list[i] = list[i];
+  const int strips = a.F / 16, items = n_slots * strips;
   const int split = wave_split(items, blocks, gridDim.x), share = 1 << split;
   const int mine = wave >> split, q = wave & (share - 1), at_once = kRowWaves >> split;
   const int rounds = (items + gridDim.x * at_once - 1) / (gridDim.x * at_once);
@@ -205,9 +227,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
     const int item = (r * at_once + mine) * gridDim.x + blockIdx.x;
     const bool any = item < items;
     const int slot = any ? item / strips : 0, f0 = any ? (item - slot * strips) * 16 : 0;
-    int expert;
-    uint32_t tokens;
-    expert_of(a, chosen, slot, &expert, &tokens);
+    const int expert = __builtin_amdgcn_readfirstlane(list[1 + slot]);
     const int64_t n0 = (int64_t)expert * a.F + f0;
     floatx4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     const WStrip<FMT> m[2] = {weight_strip<FMT, kWhole>(a.wg, a.wgs, n0 + 16, n0, a.D),
@@ -226,23 +246,30 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
     }
     if (split) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2; j += kParts<NI>) {
         if (r || j) __syncthreads();   // what was there has been read
 #pragma unroll
-        for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = acc[j][e];
+        for (int i = 0; i < kParts<NI>; ++i)
+#pragma unroll
+          for (int e = 0; e < NI; ++e) part[i * kPart + (wave * NI + e) * 64 + lane] = acc[j + i][e];
         __syncthreads();
-        if (q == 0) add_shared<NI>(part, wave, share, acc[j]);
+        if (q == 0) {
+#pragma unroll
+          for (int i = 0; i < kParts<NI>; ++i) add_shared<NI>(part + i * kPart, wave, share, acc[j + i]);
+        }
       }
     }
     if (any && q == 0) {
+      const uint32_t tokens = (uint32_t)list[1 + cap + slot];
+      const int pair0 = list[1 + 2 * cap + slot];
       // beside 4-bit weights h lies in the codes' order within each eight values
       const int f = lane & 15, at = FMT < 0 ? f : (f & 8) | ((f & 3) << 1) | ((f >> 2) & 1);
 #pragma unroll
       for (int e = 0; e < NI; ++e) {
         const int t = 4 * e + (lane >> 4);
         if ((tokens >> t) & 1u)   // a token's bit: t < T
-          split_store((S*)a.h, ((size_t)slot * a.T + t) * 2 * a.F + f0 + at, a.F,
-                      swiglu(acc[0][e], acc[1][e], a.clamp));
+          split_store((S*)a.h, (size_t)(pair0 + __popc(tokens & ((1u << t) - 1u))) * 2 * a.F + f0 + at,
+                      a.F, swiglu(acc[0][e], acc[1][e], a.clamp));
       }
     }
   }
@@ -253,59 +280,124 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
 // columns of two blocks, the first's weight rows as rows 0 .. 7 of a strip, the second's
 // as rows 8 .. 15; each of the kN blocks' h is then multiplied by all 16, and the half
 // of the products that belongs to the other block goes nowhere.
-// h's two parts: up to 8 tokens have both in one fragment (PARTS 1: row 2 t of h and row
-// 2 t + 1 are two of its 16), more have a fragment of each (PARTS 2).
-template <int FMT, int R, int PARTS> struct FewUnit {
+template <int FMT, int R> struct FewUnit {
   static constexpr int kW = R == 8 || FMT < 0 ? 1 : 2;
   static constexpr int kN = R == 8 || FMT >= 0 ? 2 : 1;
   WBlock<FMT> w[kW];
-  uint4 h[kN][PARTS][4];
+};
+// units in flight a wave
+template <int FMT, int R> constexpr int kDownDepth = FMT == 0 && R == 8 ? 8 : 4;
+
+constexpr int kDownWaves = 16;
+static_assert(kRowWaves >= kFewT, "a wave a token");
+
+// h in LDS: a row a pair and part (2 pair + part), KL values, then 16 bytes, whose first
+// four are the pair's routing weight; behind the rows 256 bytes of zeros.
+constexpr size_t h_row(int KL) { return (size_t)KL * 2 + 16; }
+
+// A turn: a range of F and the experts s0 .. s1 - 1, as many as LDS holds h of; its
+// units go to the waves in runs, u .. last - 1.
+struct DownTurn {
+  int c0, nb;          // first block of the range of F, blocks
+  int s0, s1, pair0;   // experts, pairs before the first
+  int per, u, last;    // units an expert
+  uint32_t inv;        // 2^32 / per, rounded up: fewer than 2^32 / per units
+  __device__ __forceinline__ int expert_of(int unit) const { return per == 1 ? unit : (int)__umulhi(unit, inv); }
 };
 
-// Waves of a workgroup: h's fragments of more than 8 tokens beside 4-bit weights take
-// half of a compute unit's registers in 8.
-template <int FMT, int PARTS> constexpr int kDownWaves = FMT >= 0 && PARTS == 2 ? 8 : 16;
-
 template <class S, class O, int FMT, int NI, int R, int PARTS>
-__global__ __launch_bounds__(64 * (kDownWaves<FMT, PARTS>)) void few_down_kernel(FewArgs a) {
-  constexpr int kWaves = kDownWaves<FMT, PARTS>;
+__global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, int KL, int rows) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using V = typename R16<S>::V;
-  using U = FewUnit<FMT, R, PARTS>;
-  constexpr int kN = U::kN, kW = U::kW;
+  using U = FewUnit<FMT, R>;
+  constexpr int kN = U::kN, kW = U::kW, kDepth = kDownDepth<FMT, R>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  float* part = (float*)lds;                           // [waves][NI][64]
-  int* experts = (int*)(part + kWaves * NI * 64);   // [cap]
-  uint32_t* masks = (uint32_t*)(experts + cap);        // [cap]
-  float* weights = (float*)(masks + cap);              // [cap, T]
-  const int n_slots = __builtin_amdgcn_readfirstlane(a.slots[0]);
-  for (int i = threadIdx.x; i < cap; i += blockDim.x) {   // those from n_slots on are not used
-    experts[i] = a.slots[1 + i];
-    masks[i] = (uint32_t)a.slots[1 + cap + i];
-  }
+  const int row = (int)h_row(KL), zeros = rows * 2 * row;
+  int* experts = (int*)(lds + zeros + 256);   // [cap]
+  uint32_t* masks = (uint32_t*)(experts + cap);   // [cap]
+  int* before = (int*)(masks + cap);              // [cap]
+  const int n_slots = __builtin_amdgcn_readfirstlane(a.list[0]);
+  for (int i = threadIdx.x; i < 3 * cap; i += blockDim.x)   // those from n_slots on are not used
+    experts[i] = a.list[1 + i];
+  if (threadIdx.x < 64) reinterpret_cast<uint32_t*>(lds + zeros)[threadIdx.x] = 0u;
   __syncthreads();
-  const int blocks = a.F / 128, per = (blocks + kN - 1) / kN, units = n_slots * per;
-  const int d0 = blockIdx.x * R;
-  const uint32_t hbytes = (uint32_t)(a.T * a.F) * 4;
+  const int blocks = a.F / 128, per_turn = KL / 128, d0 = blockIdx.x * R;
   const uint32_t rb = FMT < 0 ? (uint32_t)a.F * 2 : (uint32_t)a.F / 2;
   // R = 8: whether this lane's weights (parameters, products) are the second block's
   const bool second = FMT < 0 ? (lane & 15) >= 8 : lane >= 32, second_col = (lane & 15) >= 8;
-  // the row of h in the lane's row of a fragment: 2 t + part, or 2 t
-  const int vrow = PARTS == 1 ? fragment_token() : 2 * fragment_token();
-  // units go to the waves in runs
-  const int first = units * wave / kWaves, last = units * (wave + 1) / kWaves;
-  auto load = [&](int u) {
-    U n;
-    const bool any = u < last;
-    const int slot = any ? u / per : 0, kb = any ? (u - slot * per) * kN : 0;
+
+  // the next turn, false after the last
+  auto turn = [&](DownTurn& w) __attribute__((always_inline)) {
+    w.s0 = w.s1;
+    if (w.s0 >= n_slots) {
+      w.s0 = 0;
+      w.c0 += w.nb;
+    }
+    w.u = w.last = 0;
+    if (w.c0 >= blocks || n_slots == 0) return false;
+    w.nb = min(per_turn, blocks - w.c0);
+    w.per = (w.nb + kN - 1) / kN;
+    w.inv = 0xFFFFFFFFu / (uint32_t)w.per + 1u;
+    w.pair0 = __builtin_amdgcn_readfirstlane(before[w.s0]);
+    // one expert's rows always fit
+    for (w.s1 = w.s0;;) {
+      const int s = w.s1 + lane;
+      const bool fits = s < n_slots && before[s] + __popc(masks[s]) - w.pair0 <= rows;
+      const uint64_t no = ~__ballot(fits);
+      w.s1 += no ? __builtin_ctzll(no) : 64;
+      if (no) break;
+    }
+    const int units = (w.s1 - w.s0) * w.per;
+    w.u = units * wave / kDownWaves;
+    w.last = units * (wave + 1) / kDownWaves;
+    return true;
+  };
+  // h of the turn's pairs, and their weights
+  auto stage = [&](const DownTurn& w) __attribute__((always_inline)) {
+    constexpr int kAhead = 4;
+    const int end = __builtin_amdgcn_readfirstlane(before[w.s1 - 1] + __popc(masks[w.s1 - 1]));
+    for (int i = threadIdx.x; i < (w.s1 - w.s0) * 16; i += 64 * kDownWaves) {
+      const int s = w.s0 + (i >> 4), t = i & 15;
+      const uint32_t m = masks[s];
+      if ((m >> t) & 1u) {
+        const int e = experts[s], p = before[s] - w.pair0 + __popc(m & ((1u << t) - 1u));
+        *reinterpret_cast<float*>(lds + 2 * p * row + KL * 2) = e < a.E ? a.w[(size_t)t * a.E + e] : 1.f;
+      }
+    }
+    // sixteen lanes a row's block
+    const int n = (end - w.pair0) * 2 * w.nb, c = lane & 15;
+    const auto h = make_rsrc((const S*)a.h + (size_t)w.pair0 * 2 * a.F, (uint32_t)(end - w.pair0) * 4u * a.F);
+    constexpr int kStep = kDownWaves * 4;
+    const int dr = kStep / w.nb, db = kStep - dr * w.nb, i0 = threadIdx.x >> 4;
+    int r = i0 / w.nb, b = i0 - r * w.nb;
+    for (int i = i0; i < n; i += kStep * kAhead) {
+      uint4 v[kAhead];
+      int to[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        to[j] = r * row + b * 256 + c * 16;
+        v[j] = buffer16(h, i + j * kStep < n ? (uint32_t)(r * a.F + (w.c0 + b) * 128 + c * 8) * 2u : kPastEnd, 0);
+        r += dr;
+        b += db;
+        if (b >= w.nb) { b -= w.nb; ++r; }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i + j * kStep < n) *reinterpret_cast<uint4*>(lds + to[j]) = v[j];
+    }
+  };
+  // unit u's weights; none from the run's end on
+  auto load = [&](U& n, const DownTurn& w, int u) __attribute__((always_inline)) {
+    const bool any = u < w.last;
+    const int slot = any ? w.s0 + w.expert_of(u) : 0;
+    const int kb = any ? w.c0 + (u - (slot - w.s0) * w.per) * kN : 0, end = any ? w.c0 + w.nb : 0;
     const int expert = __builtin_amdgcn_readfirstlane(experts[slot]);
-    const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
     const int64_t n0 = (int64_t)expert * a.D + d0;
     WStrip<FMT> m = weight_strip<FMT, kWhole>(a.wd, a.wds, n0 + R, n0, a.F);
     if constexpr (R == 8) {
-      const bool odd = kb + 1 >= blocks;   // no second block
+      const bool odd = kb + 1 >= end;   // no second block
       if (second) m.vq = odd ? kPastEnd : m.vq - 8u * rb + (FMT < 0 ? 256u : 64u);
       if constexpr (FMT >= 0) {
         using Q = Q4F<FMT>;
@@ -313,72 +405,78 @@ __global__ __launch_bounds__(64 * (kDownWaves<FMT, PARTS>)) void few_down_kernel
           m.vp = odd ? kPastEnd : m.vp - 8u * ((uint32_t)(a.F / Q::kGroup) * Q::kPB) + 128 / Q::kGroup * Q::kPB;
       }
     }
+    constexpr bool kPair = kW == 2 && FMT != 1;   // parameters of both blocks: 16 bytes a row
 #pragma unroll
-    for (int j = 0; j < kW; ++j)
-      n.w[j] = load_wblock<FMT, kWhole>(m, kb + j, any ? blocks : 0, a.F);
-    const auto rh = make_rsrc((const S*)a.h + (size_t)slot * a.T * 2 * a.F, hbytes);
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      // a lane whose token did not choose the expert reads zeros
-      const uint32_t v = any && kb + j < blocks && ((chosen >> (vrow >> 1)) & 1u)
-          ? (uint32_t)(vrow * a.F + (kb + j) * 128 + (lane >> 4) * 8) * 2 : kPastEnd;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) n.h[j][p][i] = buffer16(rh, v + 64 * i, (uint32_t)(p * a.F) * 2);
+    for (int j = 0; j < kW; ++j) n.w[j] = load_wblock<FMT, kWhole, !kPair>(m, kb + j, end, a.F);
+    if constexpr (kPair) {
+      using Q = Q4F<FMT>;
+      const uint4 p = buffer16(m.p, kb < end ? m.vp : kPastEnd,
+                               (uint32_t)(kb < end ? kb : 0) * (128 / Q::kGroup * Q::kPB));
+      n.w[0].p[0] = p.x; n.w[0].p[1] = p.y;
+      n.w[kW - 1].p[0] = p.z; n.w[kW - 1].p[1] = p.w;
     }
-    return n;
   };
+
+  // what the lane reads of h: the row 2 t + part of a fragment's row, or 2 t; what it
+  // adds to: the token of element e
+  const int vrow = PARTS == 1 ? fragment_token() : 2 * fragment_token();
+  auto token = [&](int e) { return PARTS == 1 ? 2 * e + (lane >> 5) : 4 * e + (lane >> 4); };
   float sum[NI];
 #pragma unroll
   for (int e = 0; e < NI; ++e) sum[e] = 0.f;
-  U next = load(first);
-  for (int i = threadIdx.x; i < n_slots * a.T; i += blockDim.x) {
-    const int slot = i / a.T, t = i - slot * a.T, e = experts[slot];
-    weights[i] = e < a.E && ((masks[slot] >> t) & 1u) ? a.w[(size_t)t * a.E + e] : 1.f;
-  }
-  __syncthreads();
-  // the token of element e
-  auto token = [&](int e) { return PARTS == 1 ? 2 * e + (lane >> 5) : 4 * e + (lane >> 4); };
-  for (int u = first; u < last; ++u) {
-    const U now = next;
-    next = load(u + 1);
-    const int slot = u / per;
+  auto add = [&](const U& now, const DownTurn& w, int u) __attribute__((always_inline)) {
+    const int slot = w.s0 + w.expert_of(u), kb = (u - (slot - w.s0) * w.per) * kN;   // of the turn
     const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
+    const int pair = __builtin_amdgcn_readfirstlane(before[slot]) - w.pair0;
+    auto row_of = [&](int t) { return 2 * (pair + __popc(chosen & ((1u << t) - 1u))) * row; };
+    // a lane whose token did not choose the expert reads zeros
+    const bool in = (chosen >> (vrow >> 1)) & 1u;
+    const int at = (in ? row_of(vrow >> 1) + (vrow & 1) * row + kb * 256 : zeros) + (lane >> 4) * 16;
+    const int rest = in ? row : 0;
+    auto h = [&](int j, int i, int p) {
+      // a block behind the last one: whatever lies there is not used
+      return as_v8<V>(*reinterpret_cast<const uint4*>(lds + at + (in ? j * 256 : 0) + i * 64 + p * rest));
+    };
     floatx4 acc = {0.f, 0.f, 0.f, 0.f};
     if constexpr (FMT < 0) {
       floatx4 p[kN];
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         p[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (j && kb + j >= w.nb) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int q = PARTS - 1; q >= 0; --q)
-            p[j] = mfma16(as_v8<V>(now.h[j][q][i]), as_v8<V>(now.w[0].q[i]), p[j]);
+          for (int q = PARTS - 1; q >= 0; --q) p[j] = mfma16(h(j, i, q), as_v8<V>(now.w[0].q[i]), p[j]);
       }
 #pragma unroll
       for (int e = 0; e < NI; ++e) acc[e] = R == 8 && second_col ? p[kN - 1][e] : p[0][e];
     } else {
 #pragma unroll
       for (int b = 0; b < kW; ++b) {
+        if (b && kb + b >= w.nb) break;
         uint32_t prm[FMT == 1 ? 4 : 2];
         block_params<FMT, kWhole>(now.w[b], prm);
         const Q4Steps<FMT> q = q4_steps<FMT, kWhole>(now.w[b].q, prm, 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const V w = q4_widen<S, FMT>(q.word[i]);
+          const V wv = q4_widen<S, FMT>(q.word[i]);
           // R = 8: the strip against both blocks' h; R = 16: a strip a block
           constexpr int kH = R == 8 ? 2 : 1;
           floatx4 m[kH], c[kH];
 #pragma unroll
           for (int j = 0; j < kH; ++j) {
-            c[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+            m[j] = c[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+            if (j && kb + j >= w.nb) break;
+            V v[PARTS];
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) c[j] = x_constant<S, FMT>(as_v8<V>(now.h[b + j][p][i]), c[j]);
+            for (int p = PARTS - 1; p >= 0; --p) {
+              v[p] = h(b + j, i, p);
+              c[j] = x_constant<S, FMT>(v[p], c[j]);
+            }
             m[j] = c[j];
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) m[j] = mfma16(as_v8<V>(now.h[b + j][p][i]), w, m[j]);
+            for (int p = PARTS - 1; p >= 0; --p) m[j] = mfma16(v[p], wv, m[j]);
           }
 #pragma unroll
           for (int e = 0; e < NI; ++e) {
@@ -393,15 +491,43 @@ __global__ __launch_bounds__(64 * (kDownWaves<FMT, PARTS>)) void few_down_kernel
     // a token of another expert takes nothing: its zeros times an infinite weight are NaN
 #pragma unroll
     for (int e = 0; e < NI; ++e)
-      if ((chosen >> token(e)) & 1u) sum[e] = fmaf(weights[slot * a.T + token(e)], acc[e], sum[e]);
+      if ((chosen >> token(e)) & 1u)
+        sum[e] = fmaf(*reinterpret_cast<const float*>(lds + row_of(token(e)) + KL * 2), acc[e], sum[e]);
+  };
+
+  DownTurn now{0, 0, 0, 0, 0, 0, 0, 0, 0};
+  bool open = turn(now);
+  U ring[kDepth];
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) load(ring[i], now, now.u + i);
+  while (open) {
+    stage(now);
+    __syncthreads();
+    DownTurn next = now;
+    open = turn(next);
+    // in whole rings: the last one's places are filled for the next turn
+    do {
+      const bool end = now.u + kDepth >= now.last;
+      const DownTurn from = end ? next : now;
+      const int u = end ? next.u : now.u + kDepth;
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        if (now.u + i < now.last) add(ring[i], now, now.u + i);
+        load(ring[i], from, u + i);
+      }
+      now.u += kDepth;
+    } while (now.u < now.last);
+    now = next;
+    __syncthreads();   // all waves are done with the turn
   }
+  float* part = (float*)lds;   // [waves][NI][64]
 #pragma unroll
   for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = sum[e];
   __syncthreads();
   if (threadIdx.x < 64 * NI) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
+    for (int w = 0; w < kDownWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
     if constexpr (R == 8) v += __shfl_xor(v, 8);        // the two blocks
     if constexpr (PARTS == 1) v += __shfl_xor(v, 16);   // the two parts
     const int t = token(wave), c = lane & 15;
@@ -413,7 +539,8 @@ __global__ __launch_bounds__(64 * (kDownWaves<FMT, PARTS>)) void few_down_kernel
 template <class S, int FMT>
 hipError_t gateup_launch(const FewArgs& a, int ncu, hipStream_t s) {
   const int ni = a.T <= 4 ? 1 : a.T <= 8 ? 2 : 4;
-  const size_t other = (size_t)kRowWaves * ni * 256 + (size_t)8 * a.T * ((a.E + 63) / 64);
+  const size_t other = (size_t)kRowWaves * (ni <= 2 ? 2 : 1) * ni * 256 + (size_t)8 * kFewT * ((a.E + 63) / 64)
+                     + (size_t)4 * (1 + 3 * few_slots(a.T, a.E, a.k, a.n_shared));
   const int KL = lds_turn(x_lds_bytes<FMT>(a.T, 128), x_lds_bytes<FMT>(a.T, 256), other, a.D);
   const size_t lds = x_lds_bytes<FMT>(a.T, KL) + other;
 #define MOE_FEW(NI) \
@@ -427,10 +554,19 @@ template <class S, class O, int FMT>
 hipError_t down_launch(const FewArgs& a, int ncu, hipStream_t s) {
   const int ni = a.T <= 2 ? 1 : a.T <= 4 ? 2 : 4;   // with both parts of h; above 8 tokens, of one
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  const size_t lds = (size_t)kRowWaves * ni * 256 + (size_t)4 * cap * (2 + a.T);
+  // the range of F whose rows of T tokens fit (in whole pairs of blocks, if not all of
+  // it), and as many pairs' rows as there can be or fit
+  const size_t other = 256 + (size_t)12 * cap, room = kLdsBytes - other;
+  int KL = a.F;
+  if (a.T * 2 * h_row(KL) > room) KL = (int)((room / (a.T * 2) - 16) / 512) * 256;
+  const int64_t pairs = (int64_t)a.T * (a.k + a.n_shared), fit = (int64_t)(room / (2 * h_row(KL)));
+  const int rows = (int)(pairs < fit ? pairs : fit);
+  size_t lds = rows * 2 * h_row(KL) + other;
+  const size_t part = (size_t)kDownWaves * ni * 256;
+  if (lds < part) lds = part;
 #define MOE_FEW(NI, R, PARTS) \
   hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI, R, PARTS>), dim3(a.D / R), \
-                     dim3(64 * (kDownWaves<FMT, PARTS>)), lds, s, a)
+                     dim3(64 * kDownWaves), lds, s, a, KL, rows)
   if (a.D / 16 >= ncu) {
     if (ni == 1) MOE_FEW(1, 16, 1); else if (ni == 2) MOE_FEW(2, 16, 1);
     else if (a.T <= 8) MOE_FEW(4, 16, 1); else MOE_FEW(4, 16, 2);
@@ -464,7 +600,25 @@ hipError_t down_fmt(const FewArgs& a, int ncu, hipStream_t s) {
   }
 }
 
+template <class S>
+hipError_t router_launch(const void* x, const void* w, float* logits, int T, int D, int E, hipStream_t s) {
+  const int threads = D >= 4096 ? 512 : (D / 8 + 63) / 64 * 64;
+#define MOE_FEW(NT) \
+  hipLaunchKernelGGL((few_router_kernel<S, NT>), dim3(E), dim3(threads), 0, s, (const S*)x, (const S*)w, logits, \
+                     T, D, E)
+  if (T == 1) MOE_FEW(1); else if (T <= 4) MOE_FEW(4); else if (T <= 8) MOE_FEW(8); else MOE_FEW(16);
+#undef MOE_FEW
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_few_router(const void* x, int xdt, const void* w, float* logits, int T, int D, int E,
+                             hipStream_t s) {
+  if (xdt == MOE_BF16) return router_launch<__bf16>(x, w, logits, T, D, E, s);
+  if (xdt == MOE_F16) return router_launch<_Float16>(x, w, logits, T, D, E, s);
+  return hipErrorInvalidValue;
+}
 
 hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s) {
   if (a.xdt == MOE_BF16) return gateup_fmt<__bf16>(a, ncu, s);

@@ -1,5 +1,4 @@
-// Products of rows with 4-bit weights on gfx950 (moe_gemm_q4), and, on the same
-// kernel, the router's map of a few tokens (16-bit weights).
+// Products of up to 16 rows with 4-bit weights on gfx950 (moe_gemm_q4).
 #include "rows16.h"
 #include "q4_internal.h"
 
@@ -21,9 +20,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_strip_kernel(RowsArgs a, 
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = (int64_t)blockIdx.y * 16;
-  const int T = (int)min<int64_t>(16, a.M - t0);
-  const S* x = (const S*)a.x + (size_t)t0 * a.K;
+  const int T = (int)a.M;
+  const S* x = (const S*)a.x;
   float* part = (float*)(lds + x_lds_bytes<FMT>(T, KL));   // [waves][NI][64], shared strips
   const int blocks = (a.K + 127) / 128, per = KL / 128;
   const int strips = (int)(((int64_t)a.N + 15) / 16);
@@ -61,7 +59,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_strip_kernel(RowsArgs a, 
 #pragma unroll
       for (int e = 0; e < NI; ++e) {
         const int t = 4 * e + (lane >> 4);
-        if (t < T && n < a.N) store_out<O>(a.out, (size_t)(t0 + t) * a.N + n, acc[0][e]);
+        if (t < T && n < a.N) store_out<O>(a.out, (size_t)t * a.N + n, acc[0][e]);
       }
     }
   }
@@ -70,26 +68,16 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_strip_kernel(RowsArgs a, 
 template <class S, class O, int FMT, int RAGGED>
 hipError_t strip_launch(const RowsArgs& a, int ncu, hipStream_t s) {
   const int strips = (int)(((int64_t)a.N + 15) / 16);
-  const int64_t chunks = (a.M + 15) / 16;
-  const int T = (int)(a.M < 16 ? a.M : 16), ni = T <= 4 ? 1 : T <= 8 ? 2 : 4;
+  const int T = (int)a.M, ni = T <= 4 ? 1 : T <= 8 ? 2 : 4;
   const int gx = strips < ncu ? strips : ncu;
   const size_t part = (size_t)kRowWaves * ni * 256;
   const int KL = lds_turn(x_lds_bytes<FMT>(T, 128), x_lds_bytes<FMT>(T, 256), part, a.K);
   const size_t lds = x_lds_bytes<FMT>(T, KL) + part;
-  for (int64_t c = 0; c < chunks; c += 32768) {
-    RowsArgs b = a;
-    b.x = (const S*)a.x + (size_t)c * 16 * a.K;
-    b.out = (O*)a.out + (size_t)c * 16 * a.N;
-    b.M = a.M - c * 16;
-    const dim3 grid(gx, (unsigned)(chunks - c < 32768 ? chunks - c : 32768)), block(64 * kRowWaves);
 #define MOE_STRIP(NI) \
-  hipLaunchKernelGGL((rows_strip_kernel<S, O, FMT, NI, RAGGED>), grid, block, lds, s, b, KL)
-    if (ni == 1) MOE_STRIP(1); else if (ni == 2) MOE_STRIP(2); else MOE_STRIP(4);
+  hipLaunchKernelGGL((rows_strip_kernel<S, O, FMT, NI, RAGGED>), dim3(gx), dim3(64 * kRowWaves), lds, s, a, KL)
+  if (ni == 1) MOE_STRIP(1); else if (ni == 2) MOE_STRIP(2); else MOE_STRIP(4);
 #undef MOE_STRIP
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  return hipGetLastError();
 }
 
 template <class S, class O>
@@ -107,10 +95,6 @@ hipError_t by_format(const RowsArgs& a, int ncu, hipStream_t s) {
 
 template <class S>
 hipError_t by_output(const RowsArgs& a, int ncu, hipStream_t s) {
-  if (a.fmt < 0) {   // the router's map
-    if (a.odt != MOE_F32 || a.K % 128) return hipErrorInvalidValue;
-    return strip_launch<S, float, -1, kWhole>(a, ncu, s);
-  }
   return a.odt == MOE_F32 ? by_format<S, float>(a, ncu, s)
        : a.odt == MOE_BF16 ? by_format<S, __bf16>(a, ncu, s) : by_format<S, _Float16>(a, ncu, s);
 }
@@ -118,6 +102,7 @@ hipError_t by_output(const RowsArgs& a, int ncu, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rows_product(const RowsArgs& a, int ncu, hipStream_t s) {
+  if (a.M < 1 || a.M > 16) return hipErrorInvalidValue;
   if (a.xdt == MOE_F16) return by_output<_Float16>(a, ncu, s);
   if (a.xdt == MOE_BF16) return by_output<__bf16>(a, ncu, s);
   return hipErrorInvalidValue;

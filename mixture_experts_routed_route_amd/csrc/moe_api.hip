@@ -624,16 +624,16 @@ size_t moe_forward_workspace_bytes(const moe_plan* p, int32_t D, int32_t F,
 }
 
 // The workspace of moe_decode: SwiGLU outputs in two parts, routing weights, slots.
-struct FewLayout { size_t h, w, slots, bytes; };
+struct FewLayout { size_t h, w, list, bytes; };
 
 static FewLayout few_layout(const moe_plan_desc& d, int F) {
   FewLayout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   const size_t cap = few_slots(d.T, d.E, d.k, d.n_shared);
-  L.h = take(cap * d.T * F * 4);
+  L.h = take((size_t)d.T * (d.k + d.n_shared) * F * 4);
   L.w = take((size_t)d.T * d.E * 4);
-  L.slots = take((1 + 2 * cap) * 4);
+  L.list = take((1 + 3 * cap) * 4);
   L.bytes = o;
   return L;
 }
@@ -698,8 +698,7 @@ moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
   hipError_t e;
   if (w_router) {
     PhaseScope ps(rec, 7, s);
-    e = launch_rows_product({x, x_dtype, w_router, nullptr, -1, d->T, d->E, D, logits, MOE_F32},
-                            info.ncu, s);
+    e = launch_few_router(x, x_dtype, w_router, logits, d->T, D, d->E, s);
     if (e != hipSuccess) return hip_fail(e, "router kernel");
   }
   FewArgs a{};
@@ -713,7 +712,7 @@ moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
   a.clamp = o.swiglu_limit;
   a.h = b + L.h;
   a.w = (float*)(b + L.w);
-  a.slots = (int32_t*)(b + L.slots);
+  a.list = (int32_t*)(b + L.list);
   a.y = y; a.ydt = y_dtype;
   {
     PhaseScope ps(rec, 3, s);

@@ -25,15 +25,14 @@ hipError_t launch_quant_q4(const void* w, int dt, int fmt, int64_t rows, int64_t
                            void* params, hipStream_t s);
 
 // ---- products (gemm_q4.hip) --------------------------------------------------
-// out[M, N] = x[M, K] . w[N, K]^T; fmt a 4-bit format, or -1: w in x's type
-// (K then a multiple of 128).
+// out[M, N] = x[M, K] . w[N, K]^T; fmt a 4-bit format
 struct RowsArgs {
   const void* x; int xdt;
   const void* w; const void* params; int fmt;
   int64_t M; int N, K;
   void* out; int odt;
 };
-// up to 16 rows (more in turns)
+// up to 16 rows
 hipError_t launch_rows_product(const RowsArgs& a, int ncu, hipStream_t s);
 // any number of rows, 4-bit weights (gemm_q4_tile.hip)
 hipError_t launch_q4_tile(const RowsArgs& a, int ncu, hipStream_t s);
@@ -50,9 +49,9 @@ struct FewArgs {
   int limit;                         // most pairs an expert keeps (T: all)
   float clamp;
   // workspace
-  void* h;                           // [slots, T, 2, F] SwiGLU outputs, in two 16-bit parts
+  void* h;                           // [pairs, 2, F] SwiGLU outputs by expert, in two 16-bit parts
   float* w;                          // [T, E] routing weights of chosen experts
-  int32_t* slots;                    // [1 + 2 slots]: their number, experts, token masks
+  int32_t* list;                     // [1 + 3 slots]: their number, experts, token masks, pairs before
   void* y; int ydt;                  // [T, D]
 };
 // experts that tokens can choose, and the shared one
@@ -60,6 +59,8 @@ constexpr int few_slots(int T, int E, int k, int n_shared) {
   const int64_t n = (int64_t)T * k;
   return (int)(n < E ? n : E) + n_shared;
 }
+hipError_t launch_few_router(const void* x, int xdt, const void* w, float* logits, int T, int D, int E,
+                             hipStream_t s);
 hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s);
 hipError_t launch_few_down(const FewArgs& a, int ncu, hipStream_t s);
 
