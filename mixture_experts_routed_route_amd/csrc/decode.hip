@@ -140,8 +140,9 @@ __device__ __forceinline__ void route_token(const FewArgs& a, int t, uint64_t* c
 }
 
 // The experts in use, in order, the shared one last: their tokens (bits, after the
-// limit, which keeps an expert's first ones) and the pairs before them. list in LDS:
+// limit, which keeps an expert's first ones; T <= TOKENS) and the pairs before them. list in LDS:
 // [0] their number, then [cap] experts, [cap] tokens, [cap] pairs before. A wave a word of experts.
+template <int TOKENS>
 __device__ __forceinline__ void list_experts(const FewArgs& a, const uint64_t* chosen, int32_t* list) {
   const int lane = threadIdx.x & 63, words = choice_words(a.E);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -151,12 +152,12 @@ __device__ __forceinline__ void list_experts(const FewArgs& a, const uint64_t* c
   for (int p = 0; p <= wave; ++p) {
     uint32_t m = 0u;
 #pragma unroll
-    for (int t = 0; t < kFewT; ++t) m |= (uint32_t)((chosen[t * words + p] >> lane) & 1ull) << t;
+    for (int t = 0; t < TOKENS; ++t) m |= (uint32_t)((chosen[t * words + p] >> lane) & 1ull) << t;
     for (int over = __popc(m) - a.limit; over > 0; --over) m &= ~(0x80000000u >> __clz((int)m));
     const uint64_t used = __ballot(m != 0u), below = (1ull << lane) - 1ull;
     int here = 0, before = pairs;
 #pragma unroll
-    for (int t = 0; t < kFewT; ++t) {
+    for (int t = 0; t < TOKENS; ++t) {
       const uint64_t of = __ballot((m >> t) & 1u);
       here += __popcll(of);
       before += __popcll(of & below);
@@ -210,11 +211,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
     if (a.E <= 128) route_token<2>(a, wave, chosen, weights);
     else if (a.E <= 256) route_token<4>(a, wave, chosen, weights);
     else route_token<16>(a, wave, chosen, weights);
-  } else if (lane < choice_words(a.E)) {
+  } else if (wave < 4 * NI && lane < choice_words(a.E)) {
     chosen[wave * choice_words(a.E) + lane] = 0ull;   // no token
   }
   __syncthreads();
-  list_experts(a, chosen, list);
+  list_experts<4 * NI>(a, chosen, list);
   __syncthreads();
   const int n_slots = __builtin_amdgcn_readfirstlane(list[0]);
   if (blockIdx.x == 0)   // for the second launch
@@ -286,7 +287,7 @@ template <int FMT, int R> struct FewUnit {
   WBlock<FMT> w[kW];
 };
 // units in flight a wave
-template <int FMT, int R> constexpr int kDownDepth = FMT == 0 && R == 8 ? 8 : 4;
+template <int FMT, int PARTS> constexpr int kDownDepth = FMT < 0 && PARTS == 1 ? 2 : 4;
 
 constexpr int kDownWaves = 16;
 static_assert(kRowWaves >= kFewT, "a wave a token");
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, in
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using V = typename R16<S>::V;
   using U = FewUnit<FMT, R>;
-  constexpr int kN = U::kN, kW = U::kW, kDepth = kDownDepth<FMT, R>;
+  constexpr int kN = U::kN, kW = U::kW, kDepth = kDownDepth<FMT, PARTS>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
