@@ -4,17 +4,23 @@
 //
 //  * gate/up: every workgroup routes all tokens itself (a wave a token, k rounds of
 //    a wave-wide maximum; the first one writes the routing for the second launch),
-//    then takes (expert, 16 features) items: the expert's 16 gate and 16 up rows
-//    against all tokens' rows of x at once, which stay in registers as fragments
-//    (rows16.h). A token that did not choose the expert costs no memory, only
-//    lanes of a matrix instruction. h is kept in two 16-bit parts, its rounding
-//    and the rest (about 16 or 22 bits): the matrix units wait for memory anyway.
-//  * down: a workgroup takes 16 output columns and walks all experts that were
-//    chosen, its waves taking blocks of 128 of F in turn; each block's sums are
-//    scaled by the routing weights in f32 and added, the waves' sums meet in LDS,
-//    y is rounded once. Sums run in a fixed order: the same bits every time.
+//    then its waves take (expert, 16 features) items: the expert's 16 gate and 16 up
+//    rows against all tokens' rows of x at once, which lie in LDS (rows16.h). A token
+//    that did not choose the expert costs no memory, only lanes of a matrix
+//    instruction. h is kept in two 16-bit parts, its rounding and the rest (about 16
+//    or 22 bits): the matrix units wait for memory anyway.
+//  * down: a workgroup takes 8 or 16 output columns and all experts that were chosen,
+//    in turns of as many as LDS holds h of, its waves taking runs of blocks of 128 of
+//    F; each block's sums are scaled by the routing weights in f32 and added, the
+//    waves' sums meet in LDS, y is rounded once. Sums run in a fixed order: the same
+//    bits every time.
+// The router's map, where asked for, is a launch before them.
 //
-// Bound by the chosen experts' weights, read once.
+// Bound by the chosen experts' weights, read once. Of D 2048, F 768, 16-bit, k 8 and a
+// shared one of 128: one token 19 + 9 us (57 and 28 MB, 3 TB/s: about 8 and 4 us are
+// launch, routing and latency), sixteen 100 + 55 us (5.1 and 4.7 TB/s). Of D 4096, F 2048,
+// 4-bit with scales, 8 of 256: one token 24 + 14 us (3.1 and 2.7 TB/s), eight 115 + 75 us
+// (4.6 and 3.6 TB/s; widening and scaling the codes is about half of that).
 #include "rows16.h"
 #include "route_key.h"
 #include "q4_internal.h"
@@ -286,8 +292,10 @@ template <int FMT, int R> struct FewUnit {
   static constexpr int kN = R == 8 || FMT >= 0 ? 2 : 1;
   WBlock<FMT> w[kW];
 };
-// units in flight a wave
-template <int FMT, int PARTS> constexpr int kDownDepth = FMT < 0 && PARTS == 1 ? 2 : 4;
+// Units in flight a wave. Two: with four, the longer code and the whole rings of a turn
+// cost more than they bring (one token on 8 of 256 4-bit experts of 4096 x 2048: 16.7
+// against 14.2 us; sixteen on 16-bit ones of 2048 x 768: 55.2 against 55.6).
+constexpr int kDownDepth = 2;
 
 constexpr int kDownWaves = 16;
 static_assert(kRowWaves >= kFewT, "a wave a token");
@@ -311,7 +319,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, in
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using V = typename R16<S>::V;
   using U = FewUnit<FMT, R>;
-  constexpr int kN = U::kN, kW = U::kW, kDepth = kDownDepth<FMT, PARTS>;
+  constexpr int kN = U::kN, kW = U::kW, kDepth = kDownDepth;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
