@@ -18,6 +18,20 @@ __device__ __forceinline__ uint32_t half_bits(float v) {
   return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
+// d / s rounded to f32, r = 1 / s rounded: a product and two of Markstein's corrections
+// (IBM J. Res. Dev. 34, 1990). The first leaves less than a unit of the last place, the
+// second the nearest value, as its remainder d - q s is exact: s has 11 bits and at least
+// 2^-24; quotients so small that the remainder is not have the code 0 either way. Where
+// infinities leave no remainder (inf - inf) the product is the answer: 0, inf or NaN.
+// Fewer operations than a division's, all at the full rate: 65536 x 4096 fp16 values to
+// scales alone 190 -> 170 us (683 MB, 4.0 TB/s; 140 at best).
+__device__ __forceinline__ float quotient(float d, float s, float r) {
+  const float q0 = d * r;
+  const float q1 = __builtin_fmaf(__builtin_fmaf(-q0, s, d), r, q0);
+  const float q2 = __builtin_fmaf(__builtin_fmaf(-q1, s, d), r, q1);
+  return q2 == q2 ? q2 : q0;
+}
+
 // A thread owns 8 neighbouring values, a group is 4 (32 values) or 8 (64) lanes.
 // The minimum and maximum keep a NaN, so that its group's scale is one. s = 0 (all
 // values of a group equal, or too small for fp16) has codes of zero.
@@ -64,11 +78,12 @@ __global__ __launch_bounds__(256) void quant_q4_kernel(const void* __restrict__ 
     const float b = (float)__builtin_bit_cast(_Float16, (uint16_t)bb);
     constexpr float kMin = FMT == 0 ? -8.f : 0.f, kMax = FMT == 0 ? 7.f : 15.f;
     uint32_t word = 0u;
+    const float r = 1.f / s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = FMT == 0 ? v[i] : v[i] - b;
       // fmin / fmax give the bound for a NaN: its group has a NaN scale anyway
-      const float q = fminf(fmaxf(__builtin_rintf(d / s), kMin), kMax);
+      const float q = fminf(fmaxf(__builtin_rintf(quotient(d, s, r)), kMin), kMax);
       word |= ((uint32_t)(int)q & 15u) << (4 * i);
     }
     data[at] = s == 0.f ? 0u : word;

@@ -66,6 +66,28 @@ def test_quantiser_edges(fmt, dt):
     assert (~got[bad.isnan().any(-1)].isfinite()).all() and (~got[bad.isinf().any(-1)].isfinite()).all()
 
 
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_quantiser_codes_beside_infinite_parameters(fmt):
+    """Where a scale or a bias leaves fp16's range the codes are still the formula's: quotients of infinity, of an
+    infinite scale, and of the largest f32 values."""
+    G = GROUP[fmt]
+    step = torch.arange(G).float()
+    rows = [-7e4 - step, -7e4 + step * 4e3, step * 1e5, -step * 1e5, step * 1e37, step * 1e-3 - 6.5e4, step * 2e-7,
+            (step - G // 2) * 1e-7]
+    for dt in (torch.float32, torch.bfloat16):
+        v = torch.stack(rows).to(dt)
+        data, p = moe.moe_quant_q4_weights(v.cuda(), FORMATS[fmt])
+        q, want, _ = quantise(v, fmt)
+        assert torch.equal(p.cpu(), want)
+        fixed = ~want.isnan() if fmt == "b32" else ~want.isnan().any(-1)
+        got, q = (t.unflatten(-1, (-1, G)) for t in (codes(data.cpu(), fmt), q))
+        # a NaN quotient (infinity minus or over itself) has any code: its group's values are infinite or NaN
+        s = (want if fmt == "b32" else want[..., 0]).float()[..., None]
+        b = 0.0 if fmt == "b32" else want[..., 1].float()[..., None]
+        fixed = fixed[..., None] & ~((v.float().unflatten(-1, (-1, G)) - b) / s).isnan()
+        assert torch.equal(got[fixed], q[fixed])
+
+
 def test_quantiser_views():
     v = torch.randn(6, 300, generator=_gen(2)).cuda()
     a = v[:, 4:260]                       # strided, off 16 bytes
