@@ -63,14 +63,14 @@ typedef enum {
     /* 4-bit block weights: `data` is uint8 [.., N, K/2] holding two's-
      * complement nibbles (low nibble = even K index), `scales` is fp16
      * [.., N, K/32], one scale per 32 consecutive K values of a row; the
-     * value is q * s. Weights only; x must be F16. */
+     * value is q * s. Weights only; x F16 (moe_decode, moe_gemm_q4: or BF16). */
     MOE_Q4B32 = 3,
     /* Affine 4-bit groups (the MLX 4-bit checkpoints of TensorFold PR
      * #1607, "group 32" / "group 64" in its tuner tables): `data` is uint8
      * [.., N, K/2] holding unsigned nibbles 0..15 (low nibble = even K
      * index), `scales` is fp16 [.., N, K/G, 2]: per group of G = 32 / 64
      * consecutive K values of a row, its scale s then its bias b; the value
-     * is q * s + b. Weights only; x must be F16. */
+     * is q * s + b. Weights only; x as for MOE_Q4B32. */
     MOE_Q4A32 = 4,
     MOE_Q4A64 = 5,
     /* 8-bit blocks: `data` is e4m3 (finite range to 448, no infinity, one
