@@ -419,8 +419,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, in
     for (int j = 0; j < kW; ++j) n.w[j] = load_wblock<FMT, kWhole, !kPair>(m, kb + j, end, a.F);
     if constexpr (kPair) {
       using Q = Q4F<FMT>;
-      const uint4 p = buffer16(m.p, kb < end ? m.vp : kPastEnd,
-                               (uint32_t)(kb < end ? kb : 0) * (128 / Q::kGroup * Q::kPB));
+      const uint4 p = buffer16(m.p, kb < end ? run_at(m.vp, kb, 128 / Q::kGroup * Q::kPB) : kNoLoad);
       n.w[0].p[0] = p.x; n.w[0].p[1] = p.y;
       n.w[kW - 1].p[0] = p.z; n.w[kW - 1].p[1] = p.w;
     }

@@ -20,6 +20,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "q4_addr.h"
 
 namespace moe {
 
@@ -115,9 +116,9 @@ __device__ __forceinline__ uint2 buffer8(__amdgpu_buffer_rsrc_t r, uint32_t v, u
   return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, v, s, 0));
 }
 
-// a lane's offset past every descriptor's end (the scalar offset is left out of the
-// range check)
-constexpr uint32_t kPastEnd = 0x80000000u;
+__device__ __forceinline__ uint4 buffer16(__amdgpu_buffer_rsrc_t r, LoadAt at) { return buffer16(r, at.v, at.s); }
+__device__ __forceinline__ uint2 buffer8(__amdgpu_buffer_rsrc_t r, LoadAt at) { return buffer8(r, at.v, at.s); }
+constexpr LoadAt kNoLoad = {kPastEnd, 0u};
 
 // Rows n0 .. of the matrix [N, K] at data / params.
 template <int FMT, int RAGGED>
@@ -137,10 +138,10 @@ __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void
     using Q = Q4F<FMT>;
     const uint32_t pb = (uint32_t)(K / Q::kGroup) * Q::kPB;
     const char* p = (const char*)params + n0 * (int64_t)pb;
-    r.vq = (lane >> 2) * rb + (lane & 3) * 16u;
+    r.vq = codes_start(lane, rb);
     r.p = make_rsrc(p, rows * pb);
-    r.vp = lane < 16 ? lane * pb : kPastEnd;
-    r.vr = (lane >> 2) * pb + (lane & 3) * 16u;
+    r.vp = params_start(lane, pb);
+    r.vr = run_start(lane, pb);
     if constexpr (RAGGED == kOdd)   // rows past the last read the matrix's first
       r.prow = (lane & 15) < rows ? p + (size_t)(lane & 15) * pb : (const char*)params;
   }
@@ -149,35 +150,35 @@ __device__ __forceinline__ WStrip<FMT> weight_strip(const void* data, const void
 
 // Block kb (values 128 kb ..) of the strip; kb >= end gives zeros. In a short last
 // block the pieces behind the row's end have parameters of zero (their codes are the
-// next row's, x's fragments are zero there).
+// next row's, or zeros behind the last row; x's fragments are zero there).
 template <int FMT, int RAGGED, bool PARAMS = true>
 __device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb, int end, int K) {
   WBlock<FMT> b;
-  const uint32_t at = (uint32_t)(kb < end ? kb : end - 1);
-  const uint32_t v = kb < end ? r.vq : kPastEnd;
   if constexpr (FMT < 0) {
     static_assert(RAGGED == kWhole, "16-bit weights come in whole blocks");
+    const uint32_t at = (uint32_t)(kb < end ? kb : 0);
+    const uint32_t v = kb < end ? r.vq : kPastEnd;
 #pragma unroll
     for (int i = 0; i < 4; ++i) b.q[i] = buffer16(r.q, v + 64u * i, at * 256u);
   } else {
     using Q = Q4F<FMT>;
     constexpr int kP = FMT == 1 ? 4 : 2;
     constexpr uint32_t kPer = 128 / Q::kGroup * Q::kPB;
-    b.q = buffer16(r.q, v, at * 64u);
+    b.q = buffer16(r.q, kb < end ? codes_at(r.vq, kb, RAGGED == kWhole) : kNoLoad);
     if constexpr (!PARAMS) {
     } else if constexpr (RAGGED != kOdd) {
-      const uint32_t vp = kb < end ? r.vp : kPastEnd;
+      const LoadAt at = kb < end ? params_at(r.vp, kb, kPer, RAGGED == kWhole) : kNoLoad;
       if constexpr (FMT == 1) {
-        const uint4 w = buffer16(r.p, vp, at * kPer);
+        const uint4 w = buffer16(r.p, at);
         b.p[0] = w.x; b.p[1] = w.y; b.p[2] = w.z; b.p[3] = w.w;
       } else {
-        const uint2 w = buffer8(r.p, vp, at * kPer);
+        const uint2 w = buffer8(r.p, at);
         b.p[0] = w.x; b.p[1] = w.y;
       }
     } else {
       static_assert(RAGGED != kOdd || FMT == 0, "only scales alone have two bytes");
       const int left = kb < end ? K / 32 - 4 * kb : 0;   // pieces
-      const char* p = r.prow + (size_t)at * kPer;
+      const char* p = r.prow + (size_t)(kb < end ? kb : 0) * kPer;
       b.p[0] = b.p[1] = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -190,14 +191,14 @@ __device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb,
 
 // Parameters of kRun blocks from block kb on, as loaded: lane 4 r + q has 16 bytes of
 // row r. A run's bytes are asked for at once: 8 bytes a row and block would be a
-// request each.
+// request each. What lies behind the row (its next row, or zeros behind the strip's
+// last) is not used.
 template <int FMT> constexpr int kRun = FMT == 1 ? 4 : 8;
 
 template <int FMT>
 __device__ __forceinline__ uint4 load_params(const WStrip<FMT>& r, int kb, int end) {
   using Q = Q4F<FMT>;
-  return buffer16(r.p, kb < end ? r.vr : kPastEnd,
-                  (uint32_t)(kb < end ? kb : 0) * (128 / Q::kGroup * Q::kPB));
+  return buffer16(r.p, kb < end ? run_at(r.vr, kb, 128 / Q::kGroup * Q::kPB) : kNoLoad);
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
