@@ -377,12 +377,15 @@ size_t moe_decode_workspace_bytes(const moe_plan_desc *desc, int32_t D,
  * [E, D] in x's dtype, f32 sums) are written first and then used. x is BF16 or
  * F16, the weights x's dtype or a 4-bit format (as moe_forward's, also beside
  * a BF16 x; MOE_Q4B32, MOE_Q4A32 and MOE_Q4A64 are used unrounded, q * s (+ b)
- * in f32). Products are summed in f32; the SwiGLU output is held in two 16-bit
- * parts (its rounding to x's dtype and the rest), a token's pairs are weighed
- * and summed in f32 and y (MOE_F32 or x's dtype) is rounded once. The same
- * bits from run to run. A token whose pairs all drop, without a shared expert,
- * has a row of zeros. On 4-bit weights a row of x (or a SwiGLU row) that holds
- * an infinity or a NaN gives NaN. D and F are multiples of 128 up to 2^20.
+ * in f32). Products are summed in f32; a SwiGLU output keeps 23 bits and more
+ * (beside F16 and 4-bit weights those above 2^-46 at the default limit, 2^-37
+ * without one; beside F16 weights it is infinite past 65504 without a limit, as
+ * in moe_forward); a token's pairs are weighed and summed in f32 and y (MOE_F32
+ * or x's dtype) is rounded once. The same bits from run to run. A token whose
+ * pairs all drop, without a shared expert, has a row of zeros. On 4-bit weights a
+ * row of x (or a SwiGLU row) that holds an infinity or a NaN gives NaN; an
+ * infinite weight of w_down gives an infinity or a NaN. D and F are multiples of
+ * 128 up to 2^20.
  * opt: swiglu_limit and the phase flags (7 the router's map, 3 gate/up with
  * the routing, 5 down with the weighted sum; NULL: defaults). Pointers 16-byte
  * aligned, ws 256-byte aligned; calls that may overlap need a workspace each.

@@ -7,8 +7,8 @@
 //    then its waves take (expert, 16 features) items: the expert's 16 gate and 16 up
 //    rows against all tokens' rows of x at once, which lie in LDS (rows16.h). A token
 //    that did not choose the expert costs no memory, only lanes of a matrix
-//    instruction. h is kept in two 16-bit parts, its rounding and the rest (about 16
-//    or 22 bits): the matrix units wait for memory anyway.
+//    instruction. h is kept in 16-bit parts that together hold its f32 bits
+//    (FewH): the matrix units wait for memory anyway.
 //  * down: a workgroup takes 8 or 16 output columns and all experts that were chosen,
 //    in turns of as many as LDS holds h of, its waves taking runs of blocks of 128 of
 //    F; each block's sums are scaled by the routing weights in f32 and added, the
@@ -187,14 +187,30 @@ __device__ __forceinline__ void list_experts(const FewArgs& a, const uint64_t* c
   }
 }
 
-// h's rounding at h[at], the rest at h[at + F].
-template <class S>
-__device__ __forceinline__ void split_store(S* h, size_t at, int F, float v) {
-  const S hi = (S)v;
-  h[at] = hi;
-  // an infinity stays one: inf - inf would make the sum of the parts a NaN
-  const float rest = v - (float)hi;
-  h[at + F] = (S)(rest == rest ? rest : 0.f);
+// h, the SwiGLU's f32 output, as the second launch's matrix operand: 16-bit parts, each
+// the rounding of what the ones before leave (few_hold).
+template <int PARTS> struct FewH;
+template <> struct FewH<2> { using T = _Float16; };
+template <> struct FewH<3> { using T = __bf16; };
+
+// v's parts at h[at], h[at + F], ..: an infinity or a NaN in the first one
+__device__ __forceinline__ void split_store(void* h, int parts, size_t at, int F, float v) {
+  if (parts == 3) {
+    __bf16* p = (__bf16*)h + at;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const __bf16 part = (__bf16)v;
+      p[(size_t)i * F] = part;
+      v -= (float)part;
+      if (!__builtin_isfinite(v)) v = 0.f;
+    }
+  } else {
+    _Float16* p = (_Float16*)h + at;
+    const _Float16 part = (_Float16)v;
+    p[0] = part;
+    v = (v - (float)part) * kRestUp;
+    p[F] = (_Float16)(__builtin_isfinite(v) ? v : 0.f);
+  }
 }
 
 // Both matrices' sums of waves that share strips lie in LDS at once, up to 8 tokens.
@@ -275,8 +291,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void few_gateup_kernel(FewArgs a, i
       for (int e = 0; e < NI; ++e) {
         const int t = 4 * e + (lane >> 4);
         if ((tokens >> t) & 1u)   // a token's bit: t < T
-          split_store((S*)a.h, (size_t)(pair0 + __popc(tokens & ((1u << t) - 1u))) * 2 * a.F + f0 + at,
-                      a.F, swiglu(acc[0][e], acc[1][e], a.clamp));
+          split_store(a.h, a.parts, (size_t)(pair0 + __popc(tokens & ((1u << t) - 1u))) * a.parts * a.F + f0 + at,
+                      a.F, swiglu(acc[0][e], acc[1][e], a.clamp) * a.up);
       }
     }
   }
@@ -300,8 +316,9 @@ constexpr int kDownDepth = 2;
 constexpr int kDownWaves = 16;
 static_assert(kRowWaves >= kFewT, "a wave a token");
 
-// h in LDS: a row a pair and part (2 pair + part), KL values, then 16 bytes, whose first
-// four are the pair's routing weight; behind the rows 256 bytes of zeros.
+// h in LDS: a row a pair and part (parts * pair + part), KL values, then 16 bytes, whose
+// first four are the pair's routing weight, over the part's power of two; behind the rows
+// 256 bytes of zeros.
 constexpr size_t h_row(int KL) { return (size_t)KL * 2 + 16; }
 
 // A turn: a range of F and the experts s0 .. s1 - 1, as many as LDS holds h of; its
@@ -314,16 +331,22 @@ struct DownTurn {
   __device__ __forceinline__ int expert_of(int unit) const { return per == 1 ? unit : (int)__umulhi(unit, inv); }
 };
 
-template <class S, class O, int FMT, int NI, int R, int PARTS>
+// h in PARTS parts, kSlots rows of a matrix operand a token: an instruction a step holds
+// all parts of kGroup tokens, 4 of three parts or 8 of two. There are G such groups, each
+// with sums of its own; an expert takes those that hold a token of its own (with 16 tokens
+// mostly one).
+template <int PARTS, class O, int FMT, int NI, int R, int G>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, int KL, int rows) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
+  using S = typename FewH<PARTS>::T;
   using V = typename R16<S>::V;
   using U = FewUnit<FMT, R>;
   constexpr int kN = U::kN, kW = U::kW, kDepth = kDownDepth;
+  constexpr int kSlots = PARTS == 3 ? 4 : 2, kGroup = 16 / kSlots;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
-  const int row = (int)h_row(KL), zeros = rows * 2 * row;
+  const int row = (int)h_row(KL), zeros = rows * PARTS * row;
   int* experts = (int*)(lds + zeros + 256);   // [cap]
   uint32_t* masks = (uint32_t*)(experts + cap);   // [cap]
   int* before = (int*)(masks + cap);              // [cap]
@@ -372,12 +395,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, in
       const uint32_t m = masks[s];
       if ((m >> t) & 1u) {
         const int e = experts[s], p = before[s] - w.pair0 + __popc(m & ((1u << t) - 1u));
-        *reinterpret_cast<float*>(lds + 2 * p * row + KL * 2) = e < a.E ? a.w[(size_t)t * a.E + e] : 1.f;
+        float v = (e < a.E ? a.w[(size_t)t * a.E + e] : 1.f) * a.down;
+        *reinterpret_cast<float*>(lds + PARTS * p * row + KL * 2) = v;
+        if constexpr (PARTS == 2) *reinterpret_cast<float*>(lds + (PARTS * p + 1) * row + KL * 2) = v * (1.f / kRestUp);
       }
     }
     // sixteen lanes a row's block
-    const int n = (end - w.pair0) * 2 * w.nb, c = lane & 15;
-    const auto h = make_rsrc((const S*)a.h + (size_t)w.pair0 * 2 * a.F, (uint32_t)(end - w.pair0) * 4u * a.F);
+    const int n = (end - w.pair0) * PARTS * w.nb, c = lane & 15;
+    const auto h = make_rsrc((const S*)a.h + (size_t)w.pair0 * PARTS * a.F,
+                             (uint32_t)(end - w.pair0) * (PARTS * 2u) * a.F);
     constexpr int kStep = kDownWaves * 4;
     const int dr = kStep / w.nb, db = kStep - dr * w.nb, i0 = threadIdx.x >> 4;
     int r = i0 / w.nb, b = i0 - r * w.nb;
@@ -425,82 +451,94 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, in
     }
   };
 
-  // what the lane reads of h: the row 2 t + part of a fragment's row, or 2 t; what it
-  // adds to: the token of element e
-  const int vrow = PARTS == 1 ? fragment_token() : 2 * fragment_token();
-  auto token = [&](int e) { return PARTS == 1 ? 2 * e + (lane >> 5) : 4 * e + (lane >> 4); };
-  float sum[NI];
+  // what the lane reads of h, a token's part; what it adds to, the token of element e (both
+  // within a group)
+  const int my_token = fragment_token() / kSlots, my_part = fragment_token() % kSlots;
+  auto token = [&](int e) { return kSlots == 4 ? e : 2 * e + (lane >> 5); };
+  // the second of two parts has a weight of its own
+  const int weight_at = KL * 2 + (PARTS == 2 && (lane & 16) ? row : 0);
+  float sum[G][NI];
 #pragma unroll
-  for (int e = 0; e < NI; ++e) sum[e] = 0.f;
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < NI; ++e) sum[g][e] = 0.f;
   auto add = [&](const U& now, const DownTurn& w, int u) __attribute__((always_inline)) {
     const int slot = w.s0 + w.expert_of(u), kb = (u - (slot - w.s0) * w.per) * kN;   // of the turn
     const uint32_t chosen = __builtin_amdgcn_readfirstlane(masks[slot]);
     const int pair = __builtin_amdgcn_readfirstlane(before[slot]) - w.pair0;
-    auto row_of = [&](int t) { return 2 * (pair + __popc(chosen & ((1u << t) - 1u))) * row; };
-    // a lane whose token did not choose the expert reads zeros
-    const bool in = (chosen >> (vrow >> 1)) & 1u;
-    const int at = (in ? row_of(vrow >> 1) + (vrow & 1) * row + kb * 256 : zeros) + (lane >> 4) * 16;
-    const int rest = in ? row : 0;
-    auto h = [&](int j, int i, int p) {
-      // a block behind the last one: whatever lies there is not used
-      return as_v8<V>(*reinterpret_cast<const uint4*>(lds + at + (in ? j * 256 : 0) + i * 64 + p * rest));
-    };
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (FMT < 0) {
-      floatx4 p[kN];
+    auto row_of = [&](int t) { return PARTS * (pair + __popc(chosen & ((1u << t) - 1u))) * row; };
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        p[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (j && kb + j >= w.nb) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int q = PARTS - 1; q >= 0; --q) p[j] = mfma16(h(j, i, q), as_v8<V>(now.w[0].q[i]), p[j]);
-      }
-#pragma unroll
-      for (int e = 0; e < NI; ++e) acc[e] = R == 8 && second_col ? p[kN - 1][e] : p[0][e];
-    } else {
-#pragma unroll
-      for (int b = 0; b < kW; ++b) {
-        if (b && kb + b >= w.nb) break;
+    for (int b = 0; b < kW; ++b) {
+      if (b && kb + b >= w.nb) break;
+      Q4Steps<FMT> q;
+      if constexpr (FMT >= 0) {
         uint32_t prm[FMT == 1 ? 4 : 2];
         block_params<FMT, kWhole>(now.w[b], prm);
-        const Q4Steps<FMT> q = q4_steps<FMT, kWhole>(now.w[b].q, prm, 4);
+        q = q4_steps<FMT, kWhole>(now.w[b].q, prm, 4);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const V wv = q4_widen<S, FMT>(q.word[i]);
-          // R = 8: the strip against both blocks' h; R = 16: a strip a block
-          constexpr int kH = R == 8 ? 2 : 1;
-          floatx4 m[kH], c[kH];
+      for (int g = 0; g < G; ++g) {
+        if (G > 1 && !((chosen >> (kGroup * g)) & ((1u << kGroup) - 1u))) continue;
+        // R = 8: the strip against two blocks' h
+        constexpr int kH = R == 8 ? 2 : 1;
+        // a lane whose token did not choose the expert reads zeros, as one behind the parts
+        // does, and all do of a second block behind the last one
+        const int t = kGroup * g + my_token;
+        const bool in = ((chosen >> t) & 1u) && my_part < PARTS;
+        const int mine = row_of(t) + my_part * row + (kb + b) * 256;
+        int at[kH];
+#pragma unroll
+        for (int j = 0; j < kH; ++j)
+          at[j] = (in && kb + b + j < w.nb ? mine + j * 256 : zeros) + (lane >> 4) * 16;
+        auto h = [&](int j, int i) { return as_v8<V>(*reinterpret_cast<const uint4*>(lds + at[j] + i * 64)); };
+        floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (FMT < 0) {
+          floatx4 p[kH];
 #pragma unroll
           for (int j = 0; j < kH; ++j) {
-            m[j] = c[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-            if (j && kb + j >= w.nb) break;
-            V v[PARTS];
+            p[j] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) {
-              v[p] = h(b + j, i, p);
-              c[j] = x_constant<S, FMT>(v[p], c[j]);
+            for (int i = 0; i < 4; ++i) p[j] = mfma16(h(j, i), as_v8<V>(now.w[0].q[i]), p[j]);
+          }
+#pragma unroll
+          for (int e = 0; e < NI; ++e) acc[e] = R == 8 && second_col ? p[kH - 1][e] : p[0][e];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const V wv = q4_widen<S, FMT>(q.word[i]);
+#pragma unroll
+            for (int j = 0; j < kH; ++j) {
+              const V v = h(j, i);
+              const floatx4 c = x_constant<S, FMT>(v, floatx4{0.f, 0.f, 0.f, 0.f}), m = mfma16(v, wv, c);
+              // the other block's products with a scale of zero (an infinity or a NaN of h
+              // makes NaN of its token's row anyway)
+              const bool own = R == 16 || second_col == (j == 1);
+              const float scale = own ? q.scale(i) : 0.f;
+#pragma unroll
+              for (int e = 0; e < NI; ++e) acc[e] = fmaf(scale, m[e], acc[e]);
+              if constexpr (FMT != 0) {
+                const float bias = own ? q.bias(i) * (-1.f / kQ4Off<S, FMT>) : 0.f;
+#pragma unroll
+                for (int e = 0; e < NI; ++e) acc[e] = fmaf(bias, c[e], acc[e]);
+              }
             }
-            m[j] = c[j];
-#pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) m[j] = mfma16(v[p], wv, m[j]);
           }
+          // Here the sums end, or they sink into the branches below and every matrix
+          // instruction's result with them: spills with biases and two blocks (sixteen
+          // tokens of a 2048 x 768 layer 59 us, 46 so), elsewhere a looser order (142, 157 so).
+          if constexpr (FMT > 0 && R == 8)
 #pragma unroll
-          for (int e = 0; e < NI; ++e) {
-            const bool o = R == 8 && second_col;
-            acc[e] = fmaf(q.scale(i), o ? m[kH - 1][e] : m[0][e], acc[e]);
-            if constexpr (FMT != 0)
-              acc[e] = fmaf(q.bias(i) * (-1.f / kQ4Off<S, FMT>), o ? c[kH - 1][e] : c[0][e], acc[e]);
-          }
+            for (int e = 0; e < NI; ++e) asm volatile("" : "+v"(acc[e]));
+        }
+        // a token of another expert takes nothing: its zeros times an infinite weight are NaN
+#pragma unroll
+        for (int e = 0; e < NI; ++e) {
+          const int to = kGroup * g + token(e);
+          if ((chosen >> to) & 1u)
+            sum[g][e] = fmaf(*reinterpret_cast<const float*>(lds + row_of(to) + weight_at), acc[e], sum[g][e]);
         }
       }
     }
-    // a token of another expert takes nothing: its zeros times an infinite weight are NaN
-#pragma unroll
-    for (int e = 0; e < NI; ++e)
-      if ((chosen >> token(e)) & 1u)
-        sum[e] = fmaf(*reinterpret_cast<const float*>(lds + row_of(token(e)) + KL * 2), acc[e], sum[e]);
   };
 
   DownTurn now{0, 0, 0, 0, 0, 0, 0, 0, 0};
@@ -528,18 +566,22 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a, in
     now = next;
     __syncthreads();   // all waves are done with the turn
   }
-  float* part = (float*)lds;   // [waves][NI][64]
+  constexpr int kSums = G * NI;
+  float* part = (float*)lds;   // [waves][kSums][64]
 #pragma unroll
-  for (int e = 0; e < NI; ++e) part[(wave * NI + e) * 64 + lane] = sum[e];
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < NI; ++e) part[(wave * kSums + g * NI + e) * 64 + lane] = sum[g][e];
   __syncthreads();
-  if (threadIdx.x < 64 * NI) {
+  if (threadIdx.x < 64 * kSums) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) v += part[w * NI * 64 + threadIdx.x];
-    if constexpr (R == 8) v += __shfl_xor(v, 8);        // the two blocks
-    if constexpr (PARTS == 1) v += __shfl_xor(v, 16);   // the two parts
-    const int t = token(wave), c = lane & 15;
-    if (t < a.T && c < R && (PARTS == 2 || !(lane & 16)))
+    for (int w = 0; w < kDownWaves; ++w) v += part[w * kSums * 64 + threadIdx.x];
+    if constexpr (R == 8) v += __shfl_xor(v, 8);   // the two blocks
+    v += __shfl_xor(v, 16);                         // the parts
+    if constexpr (kSlots == 4) v += __shfl_xor(v, 32);
+    const int t = kGroup * (wave / NI) + token(wave % NI), c = lane & 15;
+    if (t < a.T && c < R && (lane & (16 * (kSlots - 1))) == 0)
       static_cast<O*>(a.y)[(size_t)t * a.D + d0 + c] = (O)v;
   }
 }
@@ -558,29 +600,36 @@ hipError_t gateup_launch(const FewArgs& a, int ncu, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class S, class O, int FMT>
+template <int P, class O, int FMT>
 hipError_t down_launch(const FewArgs& a, int ncu, hipStream_t s) {
-  const int ni = a.T <= 2 ? 1 : a.T <= 4 ? 2 : 4;   // with both parts of h; above 8 tokens, of one
   const int cap = few_slots(a.T, a.E, a.k, a.n_shared);
   // the range of F whose rows of T tokens fit (in whole pairs of blocks, if not all of
   // it), and as many pairs' rows as there can be or fit
   const size_t other = 256 + (size_t)12 * cap, room = kLdsBytes - other;
   int KL = a.F;
-  if (a.T * 2 * h_row(KL) > room) KL = (int)((room / (a.T * 2) - 16) / 512) * 256;
-  const int64_t pairs = (int64_t)a.T * (a.k + a.n_shared), fit = (int64_t)(room / (2 * h_row(KL)));
+  if (a.T * P * h_row(KL) > room) KL = (int)((room / (a.T * P) - 16) / 512) * 256;
+  const int64_t pairs = (int64_t)a.T * (a.k + a.n_shared), fit = (int64_t)(room / (P * h_row(KL)));
   const int rows = (int)(pairs < fit ? pairs : fit);
-  size_t lds = rows * 2 * h_row(KL) + other;
-  const size_t part = (size_t)kDownWaves * ni * 256;
+  size_t lds = rows * P * h_row(KL) + other;
+  const size_t part = (size_t)kDownWaves * 16 * 256;   // the most sums
   if (lds < part) lds = part;
-#define MOE_FEW(NI, R, PARTS) \
-  hipLaunchKernelGGL((few_down_kernel<S, O, FMT, NI, R, PARTS>), dim3(a.D / R), \
-                     dim3(64 * kDownWaves), lds, s, a, KL, rows)
-  if (a.D / 16 >= ncu) {
-    if (ni == 1) MOE_FEW(1, 16, 1); else if (ni == 2) MOE_FEW(2, 16, 1);
-    else if (a.T <= 8) MOE_FEW(4, 16, 1); else MOE_FEW(4, 16, 2);
-  } else {
-    if (ni == 1) MOE_FEW(1, 8, 1); else if (ni == 2) MOE_FEW(2, 8, 1);
-    else if (a.T <= 8) MOE_FEW(4, 8, 1); else MOE_FEW(4, 8, 2);
+#define MOE_FEW(NI, G) \
+  do { \
+    if (a.D / 16 >= ncu) \
+      hipLaunchKernelGGL((few_down_kernel<P, O, FMT, NI, 16, G>), dim3(a.D / 16), dim3(64 * kDownWaves), lds, s, \
+                         a, KL, rows); \
+    else \
+      hipLaunchKernelGGL((few_down_kernel<P, O, FMT, NI, 8, G>), dim3(a.D / 8), dim3(64 * kDownWaves), lds, s, \
+                         a, KL, rows); \
+  } while (0)
+  if constexpr (P == 2) {
+    if (a.T <= 2) MOE_FEW(1, 1); else if (a.T <= 4) MOE_FEW(2, 1); else if (a.T <= 8) MOE_FEW(4, 1);
+    else MOE_FEW(4, 2);
+  } else if constexpr (FMT < 0) {
+    if (a.T == 1) MOE_FEW(1, 1); else if (a.T == 2) MOE_FEW(2, 1); else if (a.T <= 4) MOE_FEW(4, 1);
+    else if (a.T <= 8) MOE_FEW(4, 2); else MOE_FEW(4, 4);
+  } else {   // 4-bit layers without a limit
+    if (a.T <= 4) MOE_FEW(4, 1); else MOE_FEW(4, 4);
   }
 #undef MOE_FEW
   return hipGetLastError();
@@ -597,15 +646,19 @@ hipError_t gateup_fmt(const FewArgs& a, int ncu, hipStream_t s) {
   }
 }
 
-template <class S, class O>
+template <int P, class O>
 hipError_t down_fmt(const FewArgs& a, int ncu, hipStream_t s) {
   switch (a.fmt) {
-    case -1: return down_launch<S, O, -1>(a, ncu, s);
-    case 0: return down_launch<S, O, 0>(a, ncu, s);
-    case 1: return down_launch<S, O, 1>(a, ncu, s);
-    case 2: return down_launch<S, O, 2>(a, ncu, s);
+    case 0: return down_launch<P, O, 0>(a, ncu, s);
+    case 1: return down_launch<P, O, 1>(a, ncu, s);
+    case 2: return down_launch<P, O, 2>(a, ncu, s);
     default: return hipErrorInvalidValue;
   }
+}
+
+template <class O>
+hipError_t down_parts(const FewArgs& a, int ncu, hipStream_t s) {
+  return a.parts == 3 ? down_fmt<3, O>(a, ncu, s) : down_fmt<2, O>(a, ncu, s);
 }
 
 template <class S>
@@ -635,11 +688,11 @@ hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s) {
 }
 
 hipError_t launch_few_down(const FewArgs& a, int ncu, hipStream_t s) {
-  if (a.xdt == MOE_BF16)
-    return a.ydt == MOE_F32 ? down_fmt<__bf16, float>(a, ncu, s) : down_fmt<__bf16, __bf16>(a, ncu, s);
-  if (a.xdt == MOE_F16)
-    return a.ydt == MOE_F32 ? down_fmt<_Float16, float>(a, ncu, s) : down_fmt<_Float16, _Float16>(a, ncu, s);
-  return hipErrorInvalidValue;
+  const bool bf = a.xdt == MOE_BF16, f32 = a.ydt == MOE_F32;
+  if (a.fmt >= 0)
+    return f32 ? down_parts<float>(a, ncu, s) : bf ? down_parts<__bf16>(a, ncu, s) : down_parts<_Float16>(a, ncu, s);
+  if (bf) return f32 ? down_launch<3, float, -1>(a, ncu, s) : down_launch<3, __bf16, -1>(a, ncu, s);
+  return f32 ? down_launch<2, float, -1>(a, ncu, s) : down_launch<2, _Float16, -1>(a, ncu, s);
 }
 
 }  // namespace moe

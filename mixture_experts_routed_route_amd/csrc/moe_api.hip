@@ -623,15 +623,15 @@ size_t moe_forward_workspace_bytes(const moe_plan* p, int32_t D, int32_t F,
   return fwd_layout(p->desc, D, F, x_dtype, w_dtype, o).bytes;
 }
 
-// The workspace of moe_decode: SwiGLU outputs in two parts, routing weights, slots.
+// The workspace of moe_decode: SwiGLU outputs in parts, routing weights, slots.
 struct FewLayout { size_t h, w, list, bytes; };
 
-static FewLayout few_layout(const moe_plan_desc& d, int F) {
+static FewLayout few_layout(const moe_plan_desc& d, int F, int xdt, int wdt) {
   FewLayout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   const size_t cap = few_slots(d.T, d.E, d.k, d.n_shared);
-  L.h = take((size_t)d.T * (d.k + d.n_shared) * F * 4);
+  L.h = take((size_t)d.T * (d.k + d.n_shared) * F * 2 * few_max_parts(xdt, q4_fmt(wdt)));
   L.w = take((size_t)d.T * d.E * 4);
   L.list = take((1 + 3 * cap) * 4);
   L.bytes = o;
@@ -656,7 +656,7 @@ static moe_status few_ok(const moe_plan_desc* d, int D, int F, int xdt, int wdt)
 size_t moe_decode_workspace_bytes(const moe_plan_desc* d, int32_t D, int32_t F,
                                   int32_t x_dtype, int32_t w_dtype) {
   if (few_ok(d, D, F, x_dtype, w_dtype) != MOE_OK) return 0;
-  return few_layout(*d, F).bytes;
+  return few_layout(*d, F, x_dtype, w_dtype).bytes;
 }
 
 moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
@@ -680,7 +680,7 @@ moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
     return fail(MOE_EINVAL, "x, w_router, logits and y must be 16-byte aligned");
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return fail(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
-  const FewLayout L = few_layout(*d, F);
+  const FewLayout L = few_layout(*d, F, x_dtype, wdt);
   if (ws_bytes < L.bytes)
     return fail(MOE_EWORKSPACE, "decode workspace %zu bytes < %zu needed", ws_bytes, L.bytes);
   if (d->T == 0) return MOE_OK;
@@ -710,6 +710,8 @@ moe_status moe_decode(const moe_plan_desc* d, const void* x, int32_t x_dtype,
   const int64_t limit = capacity_limit(*d);
   a.limit = limit < 0 || limit > d->T ? d->T : (int)limit;
   a.clamp = o.swiglu_limit;
+  const FewHold hold = few_hold(x_dtype, a.fmt, a.clamp);
+  a.parts = hold.parts; a.up = hold.up; a.down = hold.down;
   a.h = b + L.h;
   a.w = (float*)(b + L.w);
   a.list = (int32_t*)(b + L.list);

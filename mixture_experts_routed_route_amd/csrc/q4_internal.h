@@ -2,6 +2,8 @@
 // the layer for a few tokens.
 #pragma once
 
+#include <cmath>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -48,8 +50,10 @@ struct FewArgs {
   int T, D, F, E, k, n_shared;
   int limit;                         // most pairs an expert keeps (T: all)
   float clamp;
+  int parts;                         // h's 16-bit parts (few_hold), its power of two and that back
+  float up, down;
   // workspace
-  void* h;                           // [pairs, 2, F] SwiGLU outputs by expert, in two 16-bit parts
+  void* h;                           // [pairs, parts, F] SwiGLU outputs by expert
   float* w;                          // [T, E] routing weights of chosen experts
   int32_t* list;                     // [1 + 3 slots]: their number, experts, token masks, pairs before
   void* y; int ydt;                  // [T, D]
@@ -59,6 +63,29 @@ constexpr int few_slots(int T, int E, int k, int n_shared) {
   const int64_t n = (int64_t)T * k;
   return (int)(n < E ? n : E) + n_shared;
 }
+// How h, the SwiGLU's f32 output, is held as an operand of the 16-bit matrix units.
+//  * Three bf16 parts: 24 bits, f32's range. Beside bf16 weights, and beside 4-bit ones
+//    whose layer has no limit.
+//  * Two fp16 parts of h * up, the second one * kRestUp as well: 23 bits of what lies above
+//    2^-14 / up, and 2^-37 / up in absolute terms below. A limit c bounds h by max(c, 0.28)
+//    c (silu is above -0.28), and up brings that bound to 2^15: with the default of 7, 2^9.
+//    Without (c^2 of 2^15 and more) up is 1, beside fp16 weights only: past 65504 h is
+//    infinite there, as moe_forward's 16-bit h.
+// Parts of 16 bits in all (two of bf16) put 1 output of bf16 in 300 to its neighbour.
+constexpr float kRestUp = 4096.f;
+struct FewHold { int parts; float up, down; };
+inline FewHold few_hold(int xdt, int fmt, float clamp) {
+  const float bound = (clamp > 0.28f ? clamp : 0.28f) * clamp;
+  const bool bounded = clamp > 0.f && bound < 32768.f;
+  if (fmt < 0 && xdt == MOE_BF16) return {3, 1.f, 1.f};
+  if (!bounded) return {fmt < 0 ? 2 : 3, 1.f, 1.f};
+  int e;
+  std::frexp(bound, &e);   // bound < 2^e
+  e = 15 - e < 100 ? 15 - e : 100;
+  return {2, std::ldexp(1.f, e), std::ldexp(1.f, -e)};
+}
+// the most parts that any limit asks for
+constexpr int few_max_parts(int xdt, int fmt) { return fmt >= 0 || xdt == MOE_BF16 ? 3 : 2; }
 hipError_t launch_few_router(const void* x, int xdt, const void* w, float* logits, int T, int D, int E,
                              hipStream_t s);
 hipError_t launch_few_gateup(const FewArgs& a, int ncu, hipStream_t s);
