@@ -382,10 +382,10 @@ size_t moe_decode_workspace_bytes(const moe_plan_desc *desc, int32_t D,
  * without one; beside F16 weights it is infinite past 65504 without a limit, as
  * in moe_forward); a token's pairs are weighed and summed in f32 and y (MOE_F32
  * or x's dtype) is rounded once. The same bits from run to run. A token whose
- * pairs all drop, without a shared expert, has a row of zeros. On 4-bit weights a
- * row of x (or a SwiGLU row) that holds an infinity or a NaN gives NaN; an
- * infinite weight of w_down gives an infinity or a NaN. D and F are multiples of
- * 128 up to 2^20.
+ * pairs all drop, without a shared expert, has a row of zeros. On 4-bit weights
+ * x is taken as in moe_gemm_q4: a row (or a SwiGLU row) that holds an infinity or
+ * a NaN gives NaN, and bf16 group sums must stay below 2^120; an infinite weight
+ * of w_down gives an infinity or a NaN. D and F are multiples of 128 up to 2^20.
  * opt: swiglu_limit and the phase flags (7 the router's map, 3 gate/up with
  * the routing, 5 down with the weighted sum; NULL: defaults). Pointers 16-byte
  * aligned, ws 256-byte aligned; calls that may overlap need a workspace each.
@@ -497,9 +497,11 @@ moe_status moe_quant_q4_weights(const void *w, int32_t dtype, int32_t w_dtype,
  * MOE_Q4A32 or MOE_Q4A64; data [N, K / 2] and scales as moe_quant_q4_weights
  * writes them): x BF16 or F16, out F32, BF16 or F16. The weights' values are
  * not rounded: each group's sum of codes times x comes from the matrix units in
- * f32 and is scaled and added in f32; one rounding to out_dtype. A row of x
- * that holds an infinity or a NaN gives NaN; bf16 rows' group sums must stay
- * below 2^120. K a multiple of the format's group up to 2^22; M below 2^31, N
+ * f32 and is scaled and added in f32; one rounding to out_dtype. Where a code is
+ * summed as 16 + q (24 + q if signed) less the constant's share, f32's rounding is
+ * that of such a sum; whole numbers below 2^24 in it are exact. A row of x that
+ * holds an infinity or a NaN gives NaN; bf16 rows' group sums must stay below
+ * 2^120. K a multiple of the format's group up to 2^22; M below 2^31, N
  * up to 2^26 (0 writes nothing). Pointers 16-byte aligned. Async on
  * `stream`. */
 moe_status moe_gemm_q4(const void *x, int32_t x_dtype, moe_weight w, int64_t M,

@@ -2,14 +2,16 @@
 // fragments of x against strips of 16 weight rows.
 //
 // As in rows16.h, a weight is never rounded: one matrix instruction a step of 32 values
-// (two for groups of 64) on the codes, off + c in 16 bits, from the accumulator -off *
-// sum x; its four sums a lane are scaled and added in f32. So an element costs one fma
-// a group beside its multiplications, and a code's widening is shared by all rows of a
-// tile: 128 rows a wave keep the vector units about as busy as the matrix units (a step
-// of 128 x 64: 40 matrix instructions of 16 cycles, about 170 vector operations of 4).
+// (two for groups of 64) on the codes, in bf16 as off + c from the accumulator -off *
+// sum x, in fp16 as they are; its four sums a lane are scaled and added in f32. So an
+// element costs one fma a group beside its multiplications, and a code's widening is
+// shared by all rows of a tile: 128 rows a wave keep the vector units about as busy as
+// the matrix units (a step of 128 x 64: 40 matrix instructions of 16 cycles in bf16, 32 in
+// fp16 without biases, about 170 and 190 vector operations of 4).
 // Weights rounded to 16 bits would cost neither the fma nor the constants, and an f32
 // output its precision (2^-12 of fp16, 2^-9 of bf16 weights).
 #include <algorithm>
+#include <type_traits>
 
 #include "rows16.h"
 #include "q4_internal.h"
@@ -18,24 +20,31 @@ namespace moe {
 
 namespace {
 
-// Eight codes of a word as off + code, in order: nine operations (q4_widen's seven
-// leave x's values to be reordered, here in every fragment).
+// Whether codes are widened without a constant: in fp16 a packed addition takes it away.
+template <class S> constexpr bool kPlainCodes = std::is_same<S, _Float16>::value;
+
+// Eight codes of a word in order (q4_widen's order would have x's values reordered in
+// every fragment): bf16 off + code, ten operations, the code's bits below those of 16 in
+// one byte; fp16 the code itself, thirteen, as 64 + c, whose code fills a byte's upper
+// half, less 64.
 template <class S, int FMT>
 __device__ __forceinline__ typename R16<S>::V q4_widen_in_order(uint32_t w) {
-  constexpr bool kHalf = R16<S>::kOff == 64.f;   // codes in the bytes' upper nibbles
-  constexpr uint32_t mask = kHalf ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-  constexpr uint32_t flip = FMT != 0 ? 0u : kHalf ? 0x80808080u : 0x08080808u;
-  const uint32_t lo = __builtin_amdgcn_bitop3_b32(kHalf ? w << 4 : w, mask, flip, 0x6A);   // 0 2 4 6
-  const uint32_t hi = __builtin_amdgcn_bitop3_b32(kHalf ? w : w >> 4, mask, flip, 0x6A);   // 1 3 5 7
+  constexpr bool kHalf = kPlainCodes<S>;
+  constexpr uint32_t mask = kHalf ? 0xF0F0F0F0u : 0x78787878u;
+  constexpr uint32_t flip = (kHalf ? 0u : 0x80808080u) | (FMT != 0 ? 0u : kHalf ? 0x80808080u : 0x40404040u);
+  const uint32_t lo = __builtin_amdgcn_bitop3_b32(w << (kHalf ? 4 : 3), mask, flip, 0x6A);      // 0 2 4 6
+  const uint32_t hi = __builtin_amdgcn_bitop3_b32(kHalf ? w : w >> 1, mask, flip, 0x6A);        // 1 3 5 7
   const uint32_t p0 = __builtin_amdgcn_perm(hi, lo, 0x05010400u);   // 0 1 2 3
   const uint32_t p1 = __builtin_amdgcn_perm(hi, lo, 0x07030602u);   // 4 5 6 7
-  constexpr uint32_t c = kHalf ? 0x54545454u : 0x43434343u;
+  constexpr uint32_t c = kHalf ? 0x54545454u : 0x41414141u;
   uint4 o;
   o.x = __builtin_amdgcn_perm(c, p0, 0x04010400u);
   o.y = __builtin_amdgcn_perm(c, p0, 0x04030402u);
   o.z = __builtin_amdgcn_perm(c, p1, 0x04010400u);
   o.w = __builtin_amdgcn_perm(c, p1, 0x04030402u);
-  return __builtin_bit_cast(typename R16<S>::V, o);
+  const auto v = __builtin_bit_cast(typename R16<S>::V, o);
+  if constexpr (kHalf) return v - (_Float16)(FMT == 0 ? 72.f : 64.f);
+  else return v;
 }
 
 // x staged as rows of 128 values, 16 pieces of 16 bytes; piece j of row r lies at place
@@ -73,12 +82,12 @@ __device__ __forceinline__ void tile_block(const char* x, const WBlock<FMT> (&w)
       for (int g = 0; g < kG; ++g) {
         a[g] = as_v8<V>(*reinterpret_cast<const uint4*>(
             x + place(m * 16 + (lane & 15), 4 * (i + g) + (lane >> 4))));
-        c = x_constant<S, FMT>(a[g], c);
+        if constexpr (FMT != 0 || !kPlainCodes<S>) c = x_constant<S, FMT>(a[g], c);
       }
       floatx4 d[NS];
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        d[s] = c;
+        d[s] = kPlainCodes<S> ? floatx4{0.f, 0.f, 0.f, 0.f} : c;
 #pragma unroll
         for (int g = 0; g < kG; ++g) d[s] = mfma16(a[g], b[s][g], d[s]);
       }

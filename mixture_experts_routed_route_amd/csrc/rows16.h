@@ -10,13 +10,16 @@
 // groups, and up to 4 NI tokens use the first NI elements only.
 //
 // 4-bit codes are not rounded to 16-bit weights: a code is ORed below a constant
-// exponent (f16 64 + c, bf16 128 + c for c = 0..15, exact), one instruction sums
-// one step of 32 values, a group or half of one, and that sum is scaled in f32.
-// The constant's share, off * sum of the step's x, is the instruction's starting
-// accumulator: -off * sum x, made once per fragment of x by an instruction
-// against a constant B. Seven integer operations a word of eight codes (three
-// shifts, four three-input logic operations), a lane exchange a word and NI fma a
-// step; widening to fp16 weights takes 16 and more.
+// exponent (16 + c for c = 0..15, exact), one instruction sums one step of 32
+// values, a group or half of one, and that sum is scaled in f32. The constant's
+// share, off * sum of the step's x, is the instruction's starting accumulator:
+// -off * sum x, made once per fragment of x by an instruction against a constant
+// B. 16 is the least power of two whose significand holds a code: what it adds to
+// a sum's rounding grows with it (rows of one sign, K 4096: 4e-7 to 1.6e-6 with 64 +
+// c and 128 + c, which need a shift less, 6e-8 to 3e-7 so). Eight
+// integer operations a word of eight codes (four shifts, four three-input logic
+// operations), a lane exchange a word and NI fma a step; widening to fp16 weights
+// takes 16 and more.
 #pragma once
 
 #include "device_common.h"
@@ -28,27 +31,25 @@ namespace moe {
 template <class S> struct R16;
 template <> struct R16<_Float16> {
   using V = half8;
-  static constexpr float kOff = 64.f;               // 0x5400: units of 2^-4, codes from bit 4
-  static constexpr uint32_t kBase = 0x54005400u, kMask = 0x00F000F0u;
-  static constexpr int kFlip = 7;                   // the codes' top bit
+  static constexpr uint32_t kBase = 0x4C004C00u, kMask = 0x03C003C0u;   // codes from bit 6
+  static constexpr int kFlip = 9;                                       // their top bit
   // word -> the nibbles (i, i + 4) at the mask's place
   template <int I> static __device__ __forceinline__ uint32_t place(uint32_t w) {
-    return I == 0 ? w << 4 : w >> (4 * I - 4);
+    return I < 2 ? w << (6 - 4 * I) : w >> (4 * I - 6);
   }
 };
 template <> struct R16<__bf16> {
   using V = bf16x8;
-  static constexpr float kOff = 128.f;              // 0x4300: units of 1
-  static constexpr uint32_t kBase = 0x43004300u, kMask = 0x000F000Fu;
-  static constexpr int kFlip = 3;
+  static constexpr uint32_t kBase = 0x41804180u, kMask = 0x00780078u;   // codes from bit 3
+  static constexpr int kFlip = 6;
   template <int I> static __device__ __forceinline__ uint32_t place(uint32_t w) {
-    return w >> (4 * I);
+    return I < 1 ? w << 3 : w >> (4 * I - 3);
   }
 };
 
 // What a signed code's widened value exceeds it by (its nibble is flipped to
 // code + 8), and an unsigned one's.
-template <class S, int FMT> constexpr float kQ4Off = R16<S>::kOff + (FMT == 0 ? 8.f : 0.f);
+template <class S, int FMT> constexpr float kQ4Off = FMT == 0 ? 24.f : 16.f;
 
 // Eight codes of a word as off + code, in the order 0 4 1 5 2 6 3 7.
 template <class S, int FMT>
