@@ -34,7 +34,8 @@ __device__ __forceinline__ float quotient(float d, float s, float r) {
 
 // A thread owns 8 neighbouring values, a group is 4 (32 values) or 8 (64) lanes.
 // The minimum and maximum keep a NaN, so that its group's scale is one. s = 0 (all
-// values of a group equal, or too small for fp16) has codes of zero.
+// values of a group equal, or too small for fp16) has codes of zero, and so has an
+// infinite s (an infinity in the group, or values too far apart), whose values are NaN.
 constexpr int kQ4Chunks = 4;   // loads in flight a thread
 template <int FMT>
 __global__ __launch_bounds__(256) void quant_q4_kernel(const void* __restrict__ w, int dt, int64_t n8,
@@ -82,11 +83,12 @@ __global__ __launch_bounds__(256) void quant_q4_kernel(const void* __restrict__ 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = FMT == 0 ? v[i] : v[i] - b;
-      // fmin / fmax give the bound for a NaN: its group has a NaN scale anyway
+      // fmin / fmax give the bound for a NaN: its group's scale is one, or infinite
       const float q = fminf(fmaxf(__builtin_rintf(quotient(d, s, r)), kMin), kMax);
       word |= ((uint32_t)(int)q & 15u) << (4 * i);
     }
-    data[at] = s == 0.f ? 0u : word;
+    // zero times an infinite scale: a NaN, as any code times a NaN scale
+    data[at] = s == 0.f || s == __builtin_inff() ? 0u : word;
     if (threadIdx.x % kLanes == 0) {
       const size_t g = (size_t)at / kLanes;
       if constexpr (FMT == 0) static_cast<uint16_t*>(params)[g] = (uint16_t)sb;
