@@ -10,11 +10,11 @@
 // fp16 without biases, about 170 and 190 vector operations of 4).
 // Weights rounded to 16 bits would cost neither the fma nor the constants, and an f32
 // output its precision (2^-12 of fp16, 2^-9 of bf16 weights).
-#include <algorithm>
 #include <type_traits>
 
 #include "rows16.h"
 #include "q4_internal.h"
+#include "q4_tiles.h"
 
 namespace moe {
 
@@ -114,7 +114,8 @@ __device__ __forceinline__ void store_as(void* out, int odt, size_t at, float v)
 // 128 rows x 256 columns a workgroup of four waves side by side, two workgroups a
 // compute unit; x by direct loads to LDS, a block of 128 values ahead, weights in
 // registers a block ahead, one barrier a block.
-constexpr int kTileM = 128, kTileN = 256, kStage = kTileM * 256;
+constexpr int kStage = kTileM * 256;
+static_assert(kTileM == 128 && kTileN == 4 * 64 && kTileThreads == 4 * 64, "four waves side by side");
 
 // MT x 16 rows from m0 on
 template <class S, int FMT, int RAGGED, int MT>
@@ -179,22 +180,11 @@ __device__ __forceinline__ void q4_tile(const RowsArgs& a, char* lds, int64_t m0
 }
 
 template <class S, int FMT, int RAGGED>
-__global__ __launch_bounds__(256, 2) void q4_tile_kernel(RowsArgs a, int tiles_n, int whole, int tiles) {
+__global__ __launch_bounds__(kTileThreads, 2) void q4_tile_kernel(RowsArgs a, int tiles_n, int whole, int tiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];   // two blocks of x
-  // An XCD's workgroups (numbers equal modulo 8) take neighbouring tiles, first of the
-  // `whole` ones, then of those of half the rows.
-  const int big = (whole + 7) & ~7, n = (int)blockIdx.x;
-  const bool all = n < big;
-  const int k = all ? n : n - big, count = all ? whole : tiles - whole;
-  const int per = (count + 7) / 8, local = (k & 7) * per + (k >> 3);
-  if ((k >> 3) >= per || local >= count) return;
-  const int64_t n0 = (int64_t)(local % tiles_n) * kTileN;
-  if (all) {
-    q4_tile<S, FMT, RAGGED, 8>(a, lds, (int64_t)(local / tiles_n) * kTileM, n0);
-  } else {
-    const int64_t m0 = (int64_t)(whole / tiles_n) * kTileM + (int64_t)(local / tiles_n) * (kTileM / 2);
-    q4_tile<S, FMT, RAGGED, 4>(a, lds, m0, n0);
-  }
+  const TileAt t = tile_at((int)blockIdx.x, tiles_n, whole, tiles);
+  if (t.rows == kTileM) q4_tile<S, FMT, RAGGED, 8>(a, lds, t.row, t.column);
+  else if (t.rows) q4_tile<S, FMT, RAGGED, 4>(a, lds, t.row, t.column);
 }
 
 // ---- some rows --------------------------------------------------------------------
@@ -283,27 +273,19 @@ hipError_t slice_launch(const RowsArgs& a, hipStream_t s) {
   return hipSuccess;
 }
 
-// Tiles in full rounds of the compute units' workgroups, and one more round of half
-// tiles where those rows fit it.
 template <class S, int FMT, int RAGGED>
 hipError_t whole_tiles(const RowsArgs& a, int64_t tn, int ncu, hipStream_t s) {
-  // rows of tiles in turns whose number fits an int
-  const int64_t tm = (a.M + kTileM - 1) / kTileM, step = std::max<int64_t>(1, (1 << 28) / tn);
-  for (int64_t y = 0; y < tm; y += step) {
+  for (int64_t row = 0; row < a.M;) {
+    const TileLaunch t = tile_launch_at(row, a.M, tn, ncu);
     RowsArgs b = a;
-    b.x = (const char*)a.x + (size_t)y * kTileM * a.K * 2;
-    b.out = (char*)a.out + (size_t)y * kTileM * a.N * (a.odt == MOE_F32 ? 4 : 2);
-    b.M = std::min<int64_t>(a.M - y * kTileM, step * kTileM);
-    const int64_t rows = (b.M + kTileM - 1) / kTileM, slots = 2 * ncu;
-    int64_t big = rows * tn / slots * slots / tn;   // rows of tiles in full rounds
-    const int64_t halves = (b.M - big * kTileM + kTileM / 2 - 1) / (kTileM / 2);
-    if (halves * tn > slots) big = rows;
-    const int64_t whole = big * tn, rest = big == rows ? 0 : halves * tn;
-    const unsigned grid = (unsigned)((whole + 7) / 8 * 8 + (rest + 7) / 8 * 8);
-    hipLaunchKernelGGL((q4_tile_kernel<S, FMT, RAGGED>), dim3(grid), dim3(256), 2 * kStage, s, b, (int)tn,
-                       (int)whole, (int)(whole + rest));
+    b.x = (const char*)a.x + (size_t)row * a.K * 2;
+    b.out = (char*)a.out + (size_t)row * a.N * (a.odt == MOE_F32 ? 4 : 2);
+    b.M = t.rows;
+    hipLaunchKernelGGL((q4_tile_kernel<S, FMT, RAGGED>), dim3(t.grid), dim3(kTileThreads), 2 * kStage, s, b, (int)tn,
+                       t.whole, t.tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    row += t.rows;
   }
   return hipSuccess;
 }
