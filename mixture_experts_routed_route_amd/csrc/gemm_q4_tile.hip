@@ -254,23 +254,14 @@ __global__ __launch_bounds__(64 * kSliceWaves) void q4_slice_kernel(RowsArgs a) 
   }
 }
 
+// (few slices: tile_launch)
 template <class S, int FMT, int RAGGED, int MT, int NS>
 hipError_t slice_launch(const RowsArgs& a, hipStream_t s) {
-  const int64_t gx = ((int64_t)a.N + NS * 16 - 1) / (NS * 16), gy = (a.M + MT * 16 - 1) / (MT * 16);
+  const dim3 grid((unsigned)(((int64_t)a.N + NS * 16 - 1) / (NS * 16)), (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
   const size_t stage = (size_t)kSliceWaves * MT * 16 * 256, sums = (size_t)kSliceWaves * MT * NS * 1024;
-  for (int64_t y = 0; y < gy; y += 32768) {
-    RowsArgs b = a;
-    const size_t osz = a.odt == MOE_F32 ? 4 : 2;
-    b.x = (const char*)a.x + (size_t)y * MT * 16 * a.K * 2;
-    b.out = (char*)a.out + (size_t)y * MT * 16 * a.N * osz;
-    b.M = a.M - y * MT * 16;
-    hipLaunchKernelGGL((q4_slice_kernel<S, FMT, RAGGED, MT, NS>),
-                       dim3((unsigned)gx, (unsigned)(gy - y < 32768 ? gy - y : 32768)),
-                       dim3(64 * kSliceWaves), stage > sums ? stage : sums, s, b);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  hipLaunchKernelGGL((q4_slice_kernel<S, FMT, RAGGED, MT, NS>), grid, dim3(64 * kSliceWaves),
+                     stage > sums ? stage : sums, s, a);
+  return hipGetLastError();
 }
 
 template <class S, int FMT, int RAGGED>

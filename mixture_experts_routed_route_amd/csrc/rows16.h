@@ -163,7 +163,6 @@ __device__ __forceinline__ WBlock<FMT> load_wblock(const WStrip<FMT>& r, int kb,
     for (int i = 0; i < 4; ++i) b.q[i] = buffer16(r.q, v + 64u * i, at * 256u);
   } else {
     using Q = Q4F<FMT>;
-    constexpr int kP = FMT == 1 ? 4 : 2;
     constexpr uint32_t kPer = 128 / Q::kGroup * Q::kPB;
     b.q = buffer16(r.q, kb < end ? codes_at(r.vq, kb, RAGGED == kWhole) : kNoLoad);
     if constexpr (!PARAMS) {
