@@ -985,6 +985,8 @@ def moe_decode(x: torch.Tensor, w_gate, w_up, w_down, k: int,
         nbytes = L.moe_decode_workspace_bytes(ctypes.byref(d), D, F, xdt, wg.dtype)
         if nbytes == 0:
             raise MoeError(MOE_EUNSUPPORTED, moe_last_error())
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on x's device")
         if workspace is None or workspace.numel() < nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         if out is None:
