@@ -383,8 +383,8 @@ size_t moe_decode_workspace_bytes(const moe_plan_desc *desc, int32_t D,
  * in moe_forward); a token's pairs are weighed and summed in f32 and y (MOE_F32
  * or x's dtype) is rounded once. The same bits from run to run. A token whose
  * pairs all drop, without a shared expert, has a row of zeros. On 4-bit weights
- * x is taken as in moe_gemm_q4: a row (or a SwiGLU row) that holds an infinity or
- * a NaN gives NaN, and bf16 group sums must stay below 2^120; an infinite weight
+ * x (and a SwiGLU row) is taken as in moe_gemm_q4: one that holds an infinity or a
+ * NaN gives NaN, and bf16 group sums must stay below 2^120; an infinite weight
  * of w_down gives an infinity or a NaN. D and F are multiples of 128 up to 2^20.
  * opt: swiglu_limit and the phase flags (7 the router's map, 3 gate/up with
  * the routing, 5 down with the weighted sum; NULL: defaults). Pointers 16-byte
@@ -485,7 +485,7 @@ moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,
  * format has them. MOE_Q4B32: s = fp16(max|v| / 7), q = clamp(rint(v / s), -8,
  * 7). Affine: s = fp16((max - min) / 15), b = fp16(min), q = clamp(rint((v - b)
  * / s), 0, 15). Quotients and differences are rounded to f32, rint and fp16()
- * go to nearest even; s = 0 has q = 0. A group that holds a NaN or an infinity,
+ * go to nearest even; s = 0 or infinite has q = 0. A group that holds a NaN or an infinity,
  * or whose s passes fp16's range, stands for NaN; one whose b does, for
  * infinities or NaN. K a multiple of the group. Pointers 16-byte aligned.
  * MOE_EUNSUPPORTED above 2^40 values. Async on `stream`. */
@@ -500,8 +500,8 @@ moe_status moe_quant_q4_weights(const void *w, int32_t dtype, int32_t w_dtype,
  * f32 and is scaled and added in f32; one rounding to out_dtype. Where a code is
  * summed as 16 + q (24 + q if signed) less the constant's share, f32's rounding is
  * that of such a sum; whole numbers below 2^24 in it are exact. A row of x that
- * holds an infinity or a NaN gives NaN; bf16 rows' group sums must stay below
- * 2^120. K a multiple of the format's group up to 2^22; M below 2^31, N
+ * holds a NaN gives NaN, one with an infinity infinities or NaN; bf16 rows' group
+ * sums must stay below 2^120. K a multiple of the format's group up to 2^22; M below 2^31, N
  * up to 2^26 (0 writes nothing). Pointers 16-byte aligned. Async on
  * `stream`. */
 moe_status moe_gemm_q4(const void *x, int32_t x_dtype, moe_weight w, int64_t M,
