@@ -285,13 +285,18 @@ template <class S, int FMT, int RAGGED>
 hipError_t tile_launch(const RowsArgs& a, int ncu, hipStream_t s) {
   const int64_t tn = ((int64_t)a.N + kTileN - 1) / kTileN;
   const int64_t strips = ((int64_t)a.N + 15) / 16;
-  // Slices of 64 x 64 take 23 us a round of the compute units at K = 4096, tiles 73 however
-  // few: us of slices / tiles at N = 4096, 300 rows 46 / 73, 640 rows 70 / 72, 1024 rows 90
-  // / 74, 2048 rows 180 / 119.
+  // Slices of 64 x 64 against tiles, us at N = K = 4096: 300 rows 46 / 71, 640 rows 70 / 73,
+  // 768 rows 71 / 73, 1024 rows 94 / 74, 2048 rows 183 / 114; at K = 14336 640 rows 196 / 230,
+  // 1024 rows 292 / 243; at K = 1024, where a tile's start and end count less, 300 rows 20 / 25,
+  // 640 rows 30 / 26. 33 rows of N = 32768 51 / 69, of 65536 101 / 75 (32 x 16: 17 rows 87 / 73).
   if ((a.M + 63) / 64 * (((int64_t)a.N + 63) / 64) > 3 * ncu) return whole_tiles<S, FMT, RAGGED>(a, tn, ncu, s);
+  // 32 x 16 against 64 x 16 and 64 x 64 at 32 rows, K = 4096: N = 4096 9 / 12 / 22, 14336 24 / 46
+  // / 26, 32768 43 / 85 / 50
   if (a.M <= 32) return slice_launch<S, FMT, RAGGED, 2, 1>(a, s);
+  // 64 x 16 in one round, against 64 x 64: 64 rows of 4096 13 / 24 (K = 14336 50 / 72), 186 rows
+  // of 1024 14 / 24; in more, 100 rows of 4096 28 / 25 (K = 14336 92 / 66), 300 of 1024 29 / 25
   const int64_t r64 = (a.M + 63) / 64;
-  if (r64 * strips <= 2 * ncu) return slice_launch<S, FMT, RAGGED, 4, 1>(a, s);
+  if (r64 * strips <= ncu) return slice_launch<S, FMT, RAGGED, 4, 1>(a, s);
   return slice_launch<S, FMT, RAGGED, 4, 4>(a, s);
 }
 
