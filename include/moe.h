@@ -485,10 +485,10 @@ moe_status moe_gemm_f8(const void *x, const float *x_scales, const void *w,
  * format has them. MOE_Q4B32: s = fp16(max|v| / 7), q = clamp(rint(v / s), -8,
  * 7). Affine: s = fp16((max - min) / 15), b = fp16(min), q = clamp(rint((v - b)
  * / s), 0, 15). Quotients and differences are rounded to f32, rint and fp16()
- * go to nearest even; s = 0 or infinite has q = 0. A group that holds a NaN or an infinity,
- * or whose s passes fp16's range, stands for NaN; one whose b does, for
- * infinities or NaN. K a multiple of the group. Pointers 16-byte aligned.
- * MOE_EUNSUPPORTED above 2^40 values. Async on `stream`. */
+ * go to nearest even; an s of 0 or infinity has q = 0. A group that holds a NaN
+ * or an infinity, or whose s passes fp16's range, stands for NaN; one whose b
+ * does, for infinities or NaN. K a multiple of the group. Pointers 16-byte
+ * aligned. MOE_EUNSUPPORTED above 2^40 values. Async on `stream`. */
 moe_status moe_quant_q4_weights(const void *w, int32_t dtype, int32_t w_dtype,
                                 int64_t rows, int64_t K, void *data,
                                 void *scales, void *stream);

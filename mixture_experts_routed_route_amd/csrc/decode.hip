@@ -18,9 +18,10 @@
 //
 // Bound by the chosen experts' weights, read once. Of D 2048, F 768, 16-bit, k 8 and a
 // shared one of 128: one token 19 + 9 us (57 and 28 MB, 3 TB/s: about 8 and 4 us are
-// launch, routing and latency), sixteen 100 + 55 us (5.1 and 4.7 TB/s). Of D 4096, F 2048,
-// 4-bit with scales, 8 of 256: one token 24 + 14 us (3.1 and 2.7 TB/s), eight 115 + 75 us
-// (4.6 and 3.6 TB/s; widening and scaling the codes is about half of that).
+// launch, routing and latency), sixteen 102 + 63 us (5.1 and 4.2 TB/s). Of D 4096, F 2048,
+// 4-bit with scales, 8 of 256: one token 24 + 13 us (3.2 and 2.9 TB/s), eight 125 + 88 us
+// (4.3 and 3.1 TB/s; widening and scaling the codes is about half of that). Medians under
+// the profiler, three sets of inputs in turn.
 #include "rows16.h"
 #include "route_key.h"
 #include "q4_internal.h"

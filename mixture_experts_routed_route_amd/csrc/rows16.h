@@ -388,7 +388,9 @@ __device__ __forceinline__ void block_product(const XBlock<S, FMT>& x, const Q4S
 template <class S, int FMT, int NI, int MATS, int RAGGED> struct Stream {
   static constexpr bool kRuns = FMT >= 0 && RAGGED != kOdd;   // parameters by runs
   static constexpr int kPair = FMT < 0 ? 1 : 2;
-  // as many as 128 registers a wave hold without spills
+  // as many as 128 registers a wave hold; beside them the two strips of gate and up spill
+  // 8 or 9 of 9 .. 16 tokens on 4-bit weights and 3 of 5 .. 8 (groups of 32 with biases), one strip 3 of rows
+  // with an odd number of scales
   static constexpr int kDepth = FMT < 0 ? 4 / MATS : MATS == 1 ? 8 : 4;
   static constexpr int kTurn = !kRuns ? kDepth : FMT == 1 ? (kDepth > 4 ? kDepth : 4) : 8;
   using Codes = WBlock<FMT>;
