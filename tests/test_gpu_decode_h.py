@@ -106,3 +106,42 @@ def test_4_bit_layers_of_small_and_large_h(fmt, xdt, T, scale, limit):
     err = rel(y, ref)
     say(f"  error {err:.2e} of {tol:.2e}")
     assert y.isfinite().all() and err <= tol
+
+
+@pytest.mark.parametrize("w,x", [("bf16", "bf16"), ("f16", "f16"), ("b32", "bf16"), ("a32", "f16")])
+@pytest.mark.parametrize("T", [5, 12, 16])
+@pytest.mark.parametrize("limit", [7.0, 0.0])
+def test_groups_of_tokens_do_not_mix(w, x, T, limit):
+    """A token of NaN or of infinities leaves the others' bits alone, in its own group of tokens and in the others; an
+    expert whose down weights are NaN or infinite reaches its own tokens only; few tokens an expert, and all at one."""
+    D, F, E, k = 256, 384, 24, 2
+    say(f"groups {w} {x} {T} {limit}")
+    g = torch.Generator().manual_seed(T)
+    mk = lambda N, K: (random_weights(g, (E + 1, N), K, w, "cuda") if w not in DT
+                       else (torch.randn(E + 1, N, K, generator=g) * K ** -0.5).to(DT[w]).cuda())
+    wg, wu, wd = mk(F, D), mk(F, D), mk(D, F)
+    xs = torch.randn(T, D, generator=g).to(DT[x]).cuda()
+    lg = torch.randn(T, E, generator=g).cuda()
+    kw = dict(logits=lg, n_shared=1, options=moe.make_options(swiglu_limit=limit))
+    y, _ = moe.moe_decode(xs, wg, wu, wd, k, **kw)
+    assert y.isfinite().all()
+    for t in (0, T // 2, T - 1):
+        for v in (math.nan, math.inf):
+            bad = xs.clone()
+            bad[t, 7] = v
+            z, _ = moe.moe_decode(bad, wg, wu, wd, k, **kw)
+            rows = torch.arange(T, device="cuda") != t
+            assert torch.equal(z[rows], y[rows])
+            assert z[t].isnan().all() if v != v else not z[t].isfinite().any()
+    ids, _, _ = route(lg, k)
+    e = int(ids[T - 1, 0])
+    hit = (ids == e).any(1).cuda()
+    for v in (math.nan, math.inf):
+        if w in DT:
+            broken = wd.clone()
+            broken[e] = v
+        else:
+            broken = (wd[0], wd[1].clone())
+            broken[1][e] = v
+        z, _ = moe.moe_decode(xs, wg, wu, broken, k, **kw)
+        assert torch.equal(z[~hit], y[~hit]) and not z[hit].isfinite().any()
